@@ -1,0 +1,278 @@
+// C-ABI front end of the 8-bit and mixture-of-experts operators: argument
+// checks, the choice of kernel shape, launch.  The contract of every entry
+// point is stated in include/gemm_bf16.h.  Nothing here allocates or throws.
+#include "../../include/gemm_bf16.h"
+
+#include <string.h>
+
+#include "block_launch.hpp"
+#include "gemm_internal.h"
+
+namespace gemm {
+
+const BlockConfig* block_configs() {
+  static const BlockConfig table[] = {
+#define ROW(NAME, A, B, C, D) {#NAME, A, B, true, &launch_block_tile<A, B, C, D>},
+      BLOCK_TILES(ROW)
+#undef ROW
+#define ROW(NAME, A, B, C, D) {#NAME, 16 * A, 16 * B, false, &launch_block_row<A, B, C, D>},
+      BLOCK_ROWS(ROW)
+#undef ROW
+      {nullptr, 0, 0, false, nullptr}};
+  return table;
+}
+
+namespace {
+
+constexpr int64_t k2G = int64_t(1) << 31;
+constexpr int64_t kRangeLimit = k2G - 4096;
+
+const BlockConfig* block_config(const char* name) {
+  for (const BlockConfig* c = block_configs(); c->name; ++c)
+    if (strcmp(c->name, name) == 0) return c;
+  return nullptr;
+}
+
+// Row tiles of a product: exact for a dense one, for experts the most that
+// R rows over E experts can need (each expert with rows adds at most one
+// tile that is not full).
+int64_t row_tile_bound(int64_t R, int64_t E, bool experts, int64_t bm) {
+  if (!experts) return (R + bm - 1) / bm;
+  const int64_t used = R < E ? R : E;
+  return used + (R - used) / bm;
+}
+
+// Shape by the rows that share one B (all of a dense product's, an expert's
+// on average).
+const BlockConfig* choose_block(int64_t R, int64_t N, int64_t E, bool experts) {
+  const int64_t used = R < E ? R : E;
+  const int64_t rows = used > 0 ? (R + used - 1) / used : 0;
+  if (rows <= 16) return block_config("r16x16");
+  if (rows <= 32) return block_config("r32x32");
+  if (rows <= 64) return block_config("r64x32");
+  const int64_t big = row_tile_bound(R, E, experts, 256) * ((N + 255) / 256);
+  return block_config(rows > 128 && big >= 256 ? "b256x256" : "b128x128");
+}
+
+int element_bytes(int type) { return type == GEMM_TYPE_E4M3 ? 1 : type == GEMM_TYPE_F32 ? 4 : 2; }
+bool misaligned(const void* p, int bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
+int op_of(int type) {
+  return type == GEMM_TYPE_E4M3 ? kOpE4m3 : type == GEMM_TYPE_BF16 ? kOpBf16 : kOpF16;
+}
+int store_of(int type) {
+  return type == GEMM_TYPE_F32 ? kStoreF32 : type == GEMM_TYPE_F16 ? kStoreF16 : kStoreBf16;
+}
+bool is_float_type(int type) {
+  return type == GEMM_TYPE_BF16 || type == GEMM_TYPE_F16 || type == GEMM_TYPE_F32;
+}
+
+// The dense (offsets null, E = 1) and the experts' product.  R rows of C;
+// a_rows rows of A.
+int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K, int64_t E,
+                  bool experts, int64_t a_rows, const void* A, int64_t lda, const float* SA,
+                  int64_t ldsa, const int32_t* offsets, const int32_t* rows, const void* B,
+                  int64_t ldb, int64_t stride_b, const float* SB, int64_t ldsb, int64_t stride_sb,
+                  void* C, int64_t ldc, int c_type, void* stream) {
+  if (R < 0 || N < 0 || K < 0 || E < 0 || a_rows < 0) return GEMM_ERR_INVALID_ARG;
+  if (type != GEMM_TYPE_E4M3 && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16)
+    return GEMM_ERR_INVALID_ARG;
+  if (!is_float_type(c_type)) return GEMM_ERR_INVALID_ARG;
+  const bool scaled = type == GEMM_TYPE_E4M3;
+  const int es = element_bytes(type);
+  const int64_t kb = (K + 127) / 128;
+  if (lda < K || ldb < K || ldc < N || stride_b < 0 || stride_sb < 0) return GEMM_ERR_INVALID_ARG;
+  if (scaled && (ldsa < a_rows || ldsb < kb)) return GEMM_ERR_INVALID_ARG;
+  const bool work = R > 0 && N > 0 && E > 0;
+  if (work) {
+    if (!C || (experts && !offsets)) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && (!B || (a_rows > 0 && !A))) return GEMM_ERR_INVALID_ARG;
+    if (K > 0 && scaled && (!SB || (a_rows > 0 && !SA))) return GEMM_ERR_INVALID_ARG;
+  }
+  if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 16)) return GEMM_ERR_MISALIGNED;
+  if (misaligned(SA, 4) || misaligned(SB, 4) || misaligned(offsets, 4) || misaligned(rows, 4))
+    return GEMM_ERR_MISALIGNED;
+  const int64_t step = 16 / es - 1;
+  if (((lda | ldb | stride_b) & step) != 0 || (ldc & 7) != 0) return GEMM_ERR_MISALIGNED;
+
+  const BlockConfig* c = config && config[0] ? block_config(config) : choose_block(R, N, E, experts);
+  if (!c) return GEMM_ERR_UNSUPPORTED;
+  if (R >= k2G || N >= k2G || K >= k2G / 2 || E >= k2G || a_rows >= k2G / 4 || lda >= k2G ||
+      ldb >= k2G)
+    return GEMM_ERR_UNSUPPORTED;
+  if (scaled && kb > kMaxKSteps) return GEMM_ERR_UNSUPPORTED;
+  if (c->bn * ldb * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
+  if ((rows ? a_rows : (int64_t)c->bm) * lda * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
+  if (!work) return GEMM_OK;
+  const int64_t tiles_n = (N + c->bn - 1) / c->bn;
+  const int64_t row_tiles = row_tile_bound(R, E, experts, c->bm);
+  if (row_tiles * tiles_n >= k2G) return GEMM_ERR_UNSUPPORTED;
+
+  BlockArgs a{};
+  a.A = (const uint8_t*)A;
+  a.B = (const uint8_t*)B;
+  a.C = C;
+  a.SA = SA;
+  a.SB = SB;
+  a.offsets = experts ? offsets : nullptr;
+  a.rows = rows;
+  a.lda = lda * es;
+  a.ldb = ldb * es;
+  a.ldc = ldc;
+  a.ldsa = ldsa;
+  a.ldsb = ldsb;
+  a.stride_b = stride_b * es;
+  a.stride_sb = stride_sb;
+  a.M = (int32_t)R;
+  a.N = (int32_t)N;
+  a.kbytes = (int32_t)(K * es);
+  a.a_rows = (int32_t)a_rows;
+  a.E = (int32_t)E;
+  a.tiles_n = (int32_t)tiles_n;
+  a.k_steps = (int32_t)((K * es + kStepBytes - 1) / kStepBytes);
+  a.row_tiles = (int32_t)row_tiles;
+  a.group_m = 4;
+  const hipError_t e =
+      c->launch(a, (int)(row_tiles * tiles_n), (hipStream_t)stream, op_of(type), store_of(c_type));
+  return e == hipSuccess ? GEMM_OK : hip_fail(e);
+}
+
+}  // namespace
+}  // namespace gemm
+
+extern "C" {
+
+int gemm_fp8_ex(const char* config, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+                const float* SA, int64_t ldsa, const void* B, int64_t ldb, const float* SB,
+                int64_t ldsb, void* C, int64_t ldc, int c_type, void* stream) {
+  return gemm::block_product(config, GEMM_TYPE_E4M3, M, N, K, 1, false, M, A, lda, SA, ldsa,
+                             nullptr, nullptr, B, ldb, 0, SB, ldsb, 0, C, ldc, c_type, stream);
+}
+
+int gemm_fp8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA,
+             int64_t ldsa, const void* B, int64_t ldb, const float* SB, int64_t ldsb, void* C,
+             int64_t ldc, int c_type, void* stream) {
+  return gemm_fp8_ex(nullptr, M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, c_type, stream);
+}
+
+int gemm_moe_ex(const char* config, int type, int64_t R, int64_t N, int64_t K, int64_t E,
+                int64_t T, const void* A, int64_t lda, const float* SA, int64_t ldsa,
+                const int32_t* offsets, const int32_t* rows, const void* B, int64_t ldb,
+                int64_t stride_b, const float* SB, int64_t ldsb, int64_t stride_sb, void* C,
+                int64_t ldc, int c_type, void* stream) {
+  if (!rows && T < R) return GEMM_ERR_INVALID_ARG;
+  return gemm::block_product(config, type, R, N, K, E, true, T, A, lda, SA, ldsa, offsets, rows, B,
+                             ldb, stride_b, SB, ldsb, stride_sb, C, ldc, c_type, stream);
+}
+
+int gemm_moe(int type, int64_t R, int64_t N, int64_t K, int64_t E, int64_t T, const void* A,
+             int64_t lda, const float* SA, int64_t ldsa, const int32_t* offsets,
+             const int32_t* rows, const void* B, int64_t ldb, int64_t stride_b, const float* SB,
+             int64_t ldsb, int64_t stride_sb, void* C, int64_t ldc, int c_type, void* stream) {
+  return gemm_moe_ex(nullptr, type, R, N, K, E, T, A, lda, SA, ldsa, offsets, rows, B, ldb,
+                     stride_b, SB, ldsb, stride_sb, C, ldc, c_type, stream);
+}
+
+const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K) {
+  if (M < 0 || N < 0 || K < 0) return "invalid";
+  return gemm::choose_block(M, N, 1, false)->name;
+}
+
+const char* gemm_moe_config_name(int64_t R, int64_t N, int64_t K, int64_t E) {
+  if (R < 0 || N < 0 || K < 0 || E < 0) return "invalid";
+  return gemm::choose_block(R, N, E, true)->name;
+}
+
+const char* gemm_fp8_config_at(int i) {
+  if (i < 0) return nullptr;
+  for (const gemm::BlockConfig* c = gemm::block_configs(); c->name; ++c)
+    if (i-- == 0) return c->name;
+  return nullptr;
+}
+
+int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_type, int act,
+                      int block_rows, void* Q, int64_t ldq, float* S, int64_t lds, void* stream) {
+  if (M < 0 || K < 0 || !gemm::is_float_type(x_type)) return GEMM_ERR_INVALID_ARG;
+  if (act != GEMM_ACT_NONE && act != GEMM_ACT_SWIGLU) return GEMM_ERR_INVALID_ARG;
+  if (block_rows != 1 && block_rows != 128) return GEMM_ERR_INVALID_ARG;
+  if (block_rows == 128 && act != GEMM_ACT_NONE) return GEMM_ERR_UNSUPPORTED;
+  if (K >= gemm::k2G || M >= gemm::k2G || ldx >= (int64_t(1) << 40) || ldq >= (int64_t(1) << 40))
+    return GEMM_ERR_UNSUPPORTED;
+  const int64_t width = act == GEMM_ACT_SWIGLU ? 2 * K : K;
+  if (ldx < width || ldq < K) return GEMM_ERR_INVALID_ARG;
+  if (lds < (block_rows == 1 ? M : (K + 127) / 128)) return GEMM_ERR_INVALID_ARG;
+  if (M > 0 && K > 0 && (!X || !Q || !S)) return GEMM_ERR_INVALID_ARG;
+  if (gemm::misaligned(X, 16) || gemm::misaligned(Q, 16) || gemm::misaligned(S, 4))
+    return GEMM_ERR_MISALIGNED;
+  if ((ldx & 7) != 0 || (ldq & 15) != 0) return GEMM_ERR_MISALIGNED;
+  if ((M + 15) / 16 > 65535 || (block_rows == 128 && (M + 127) / 128 > 65535))
+    return GEMM_ERR_UNSUPPORTED;
+  if (M == 0 || K == 0) return GEMM_OK;
+  const gemm::QuantArgs a{X, (uint8_t*)Q, S, M, K, ldx, ldq, lds};
+  const int t = gemm::store_of(x_type);
+  const hipError_t e =
+      block_rows == 1
+          ? gemm::launch_quantize_rows(a, t, act == GEMM_ACT_SWIGLU, (hipStream_t)stream)
+          : gemm::launch_quantize_blocks(a, t, (hipStream_t)stream);
+  return e == hipSuccess ? GEMM_OK : gemm::hip_fail(e);
+}
+
+int gemm_moe_route(int64_t T, int64_t E, int64_t k, const void* X, int64_t ldx, int x_type,
+                   const float* bias, int score, int64_t groups, int64_t topk_groups,
+                   int group_top, int renorm, float scale, int32_t* ids, float* weights,
+                   void* stream) {
+  if (T < 0 || E < 1 || k < 1 || groups < 1 || topk_groups < 1) return GEMM_ERR_INVALID_ARG;
+  if (!gemm::is_float_type(x_type) || ldx < E) return GEMM_ERR_INVALID_ARG;
+  if (score != GEMM_SCORE_SOFTMAX && score != GEMM_SCORE_SIGMOID) return GEMM_ERR_INVALID_ARG;
+  if (group_top != 1 && group_top != 2) return GEMM_ERR_INVALID_ARG;
+  if (groups > E || E % groups != 0 || topk_groups > groups) return GEMM_ERR_INVALID_ARG;
+  if (k > topk_groups * (E / groups)) return GEMM_ERR_INVALID_ARG;
+  if (T > 0 && (!X || !ids || !weights)) return GEMM_ERR_INVALID_ARG;
+  if (gemm::misaligned(X, gemm::element_bytes(x_type)) || gemm::misaligned(bias, 4) ||
+      gemm::misaligned(ids, 4) || gemm::misaligned(weights, 4))
+    return GEMM_ERR_MISALIGNED;
+  if (E > 1024 || k > 64 || groups > 64 || T * k >= gemm::k2G / 2) return GEMM_ERR_UNSUPPORTED;
+  if (T == 0) return GEMM_OK;
+  const gemm::RouteArgs a{X,        bias,     ids,      weights,          T,
+                          ldx,      (int)E,   (int)k,   (int)groups,      (int)topk_groups,
+                          group_top, score == GEMM_SCORE_SIGMOID, renorm != 0, scale};
+  const hipError_t e = gemm::launch_route(a, gemm::store_of(x_type), (hipStream_t)stream);
+  return e == hipSuccess ? GEMM_OK : gemm::hip_fail(e);
+}
+
+int gemm_moe_plan(int64_t T, int64_t k, int64_t E, const int32_t* ids, int32_t* offsets,
+                  int32_t* rows, int32_t* pos, void* stream) {
+  if (T < 0 || k < 1 || E < 1 || !offsets) return GEMM_ERR_INVALID_ARG;
+  if (T > 0 && (!ids || !rows || !pos)) return GEMM_ERR_INVALID_ARG;
+  if (gemm::misaligned(ids, 4) || gemm::misaligned(offsets, 4) || gemm::misaligned(rows, 4) ||
+      gemm::misaligned(pos, 4))
+    return GEMM_ERR_MISALIGNED;
+  if (E > 65535 || k >= gemm::k2G / 2 || T >= gemm::k2G / 2 || T * k >= gemm::k2G / 2)
+    return GEMM_ERR_UNSUPPORTED;
+  const hipError_t e =
+      gemm::launch_plan(ids, T, (int)k, (int)E, offsets, rows, pos, (hipStream_t)stream);
+  return e == hipSuccess ? GEMM_OK : gemm::hip_fail(e);
+}
+
+int gemm_moe_combine(int64_t T, int64_t k, int64_t N, int64_t R, const void* Y, int64_t ldy,
+                     int y_type, const int32_t* pos, const float* weights, void* out, int64_t ldo,
+                     int out_type, void* stream) {
+  if (T < 0 || k < 0 || N < 0 || R < 0) return GEMM_ERR_INVALID_ARG;
+  if (!gemm::is_float_type(y_type) || !gemm::is_float_type(out_type)) return GEMM_ERR_INVALID_ARG;
+  if (ldy < N || ldo < N) return GEMM_ERR_INVALID_ARG;
+  if (T > 0 && N > 0) {
+    if (!out || (k > 0 && (!pos || !weights || (R > 0 && !Y)))) return GEMM_ERR_INVALID_ARG;
+  }
+  if (gemm::misaligned(Y, 16) || gemm::misaligned(out, 16) || gemm::misaligned(pos, 4) ||
+      gemm::misaligned(weights, 4) || ((ldy | ldo) & 7) != 0)
+    return GEMM_ERR_MISALIGNED;
+  if (T >= gemm::k2G || N >= gemm::k2G || R >= gemm::k2G || k >= gemm::k2G ||
+      T * ((N + 7) / 8) >= gemm::k2G * 256 - 256)
+    return GEMM_ERR_UNSUPPORTED;
+  if (T == 0 || N == 0) return GEMM_OK;
+  const gemm::CombineArgs a{Y, pos, weights, out, T, N, R, ldy, ldo, (int)k};
+  const hipError_t e = gemm::launch_combine(a, gemm::store_of(y_type), gemm::store_of(out_type),
+                                            (hipStream_t)stream);
+  return e == hipSuccess ? GEMM_OK : gemm::hip_fail(e);
+}
+
+}  // extern "C"

@@ -1,0 +1,536 @@
+// Products over e4m3 operands with a scale for each block of 128, and the
+// experts' products (rows sorted by expert) over e4m3, bf16 and fp16:
+//
+//   dense     C[m,n] = sum_b SA[b,m] SB[n/128,b] sum_{k in block b} A[m,k] B[n,k]
+//   experts   the same for every row p of expert e's range
+//             [offsets[e], offsets[e+1]), with A's row rows[p] (or p) and
+//             expert e's B and SB; bf16 and fp16 operands carry no scales
+//
+// Two kernels.  block_tile_kernel stages BM x BN tiles through LDS for many
+// rows; block_row_kernel streams B straight into registers for few rows.
+// Both walk K in steps of 128 bytes of a row: one scale block of e4m3, 64
+// elements of a 16-bit type.
+//
+// A scale in fp32 cannot ride in the matrix instruction (its own scales are
+// powers of two), so each K-step's partial sums of a 16 x 16 block start
+// from zero in one 16x16x128 MFMA and are added to the fp32 accumulators by
+// one FMA each with SA * SB: 4 FMAs (16 cycles of the SIMD's vector unit)
+// per MFMA of 32 cycles, issued while the next MFMA runs.
+#pragma once
+
+#include "gemm_kernel.hpp"
+
+namespace gemm {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kStepBytes = 128;     // bytes of a row in one K-step
+constexpr int kMaxKSteps = 2048;    // K-steps whose B scales fit in LDS
+constexpr int kScaleBlock = 128;    // rows of B (and columns of C) of one scale
+
+// Operand types.
+enum : int { kOpE4m3 = 0, kOpBf16 = 1, kOpF16 = 2 };
+
+struct BlockArgs {
+  const uint8_t* A;
+  const uint8_t* B;
+  void* C;
+  const float* SA;         // SA[b * ldsa + row of A]
+  const float* SB;         // SB[(n / 128) * ldsb + b]
+  const int32_t* offsets;  // experts: E + 1 row offsets; null: dense
+  const int32_t* rows;     // experts: A's row of each row of C, or null
+  int64_t lda, ldb;        // bytes
+  int64_t ldc;             // elements
+  int64_t ldsa, ldsb;
+  int64_t stride_b;   // bytes from one expert's B to the next
+  int64_t stride_sb;  // floats from one expert's SB to the next
+  int32_t M;          // rows of C
+  int32_t N;
+  int32_t kbytes;     // bytes of a row of A or B that count
+  int32_t a_rows;     // rows of A
+  int32_t E;          // experts (1: dense)
+  int32_t tiles_n;
+  int32_t k_steps;
+  int32_t row_tiles;  // dense: row tiles; experts: an upper bound on them
+  int32_t group_m;    // raster group height in tiles
+};
+
+// ------------------------------------------------------------- row tiles
+
+// Expert e's rows of C, clamped so that no offsets, whatever they hold,
+// lead outside C.
+__device__ __forceinline__ void expert_rows(const BlockArgs& a, int e, int& begin, int& end) {
+  const int b = a.offsets[e], n = a.offsets[e + 1];
+  begin = b < 0 ? 0 : b;
+  end = n > a.M ? a.M : n;
+  if (end < begin) end = begin;
+}
+
+// Inclusive sum over the wave's lanes.
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(v, d, 64);
+    if (lane >= d) v += o;
+  }
+  return v;
+}
+
+struct RowTile {
+  int expert, begin, end;  // rows [begin, end) of C, at most BM of them used
+};
+
+// Row tiles (of BM rows) of all experts: expert e has ceil(rows / BM).
+__device__ __forceinline__ int count_row_tiles(const BlockArgs& a, int BM, int lane) {
+  int total = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 64) {
+    int b = 0, n = 0;
+    if (e0 + lane < a.E) expert_rows(a, e0 + lane, b, n);
+    total += __shfl(wave_scan((n - b + BM - 1) / BM, lane), 63, 64);
+  }
+  return __builtin_amdgcn_readfirstlane(total);
+}
+
+// The t-th row tile, experts in order; false past the last one.
+__device__ __forceinline__ bool find_row_tile(const BlockArgs& a, int BM, int t, int lane,
+                                              RowTile& r) {
+  int before = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 64) {
+    int b = 0, n = 0;
+    if (e0 + lane < a.E) expert_rows(a, e0 + lane, b, n);
+    const int tiles = (n - b + BM - 1) / BM;
+    const int upto = before + wave_scan(tiles, lane);
+    const uint64_t hit = __ballot(t < upto);
+    if (hit != 0) {
+      const int l = __builtin_ctzll(hit);  // the first expert whose tiles pass t
+      r.expert = e0 + l;
+      r.begin = __builtin_amdgcn_readlane(b, l) +
+                (t - __builtin_amdgcn_readlane(upto - tiles, l)) * BM;
+      r.end = __builtin_amdgcn_readlane(n, l);
+      return true;
+    }
+    before = __builtin_amdgcn_readlane(upto, 63);
+  }
+  return false;
+}
+
+// A's row of row p of C (p < end), or -1 where the rows array points outside A.
+__device__ __forceinline__ int source_row(const BlockArgs& a, int p) {
+  if (!a.rows) return p;
+  const int r = a.rows[p];
+  return r >= 0 && r < a.a_rows ? r : -1;
+}
+
+// ------------------------------------------------------------------ MFMA
+
+// The partial sums of one K-step: D[n][m] = C + sum_k B[n][k] A[m][k] over
+// the two 16-byte chunks a lane holds of its row.  Which k a chunk stands
+// for does not matter as long as both operands agree.
+template <int OP>
+__device__ __forceinline__ f32x4 step_mfma(const u32x4 (&b)[2], const u32x4 (&a)[2], f32x4 c) {
+  if constexpr (OP == kOpE4m3) {
+    const i32x8 vb = {(int)b[0][0], (int)b[0][1], (int)b[0][2], (int)b[0][3],
+                      (int)b[1][0], (int)b[1][1], (int)b[1][2], (int)b[1][3]};
+    const i32x8 va = {(int)a[0][0], (int)a[0][1], (int)a[0][2], (int)a[0][3],
+                      (int)a[1][0], (int)a[1][1], (int)a[1][2], (int)a[1][3]};
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, c, 0, 0, 0, 0, 0, 0);
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (OP == kOpBf16)
+        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b[h]),
+                                                    __builtin_bit_cast(bf16x8, a[h]), c, 0, 0, 0);
+      else
+        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b[h]),
+                                                   __builtin_bit_cast(f16x8, a[h]), c, 0, 0, 0);
+    }
+    return c;
+  }
+}
+
+// One LDS-DMA load of 4 bytes per lane (see dma16).
+__device__ __forceinline__ void dma4(const u32x4& rsrc, uint32_t lds_addr, uint32_t voff,
+                                     uint32_t soff) {
+  asm volatile(
+      "s_nop 0\n\t"
+      "buffer_load_dword %1, %2, %3 offen lds" ::"{m0}"(
+          __builtin_amdgcn_readfirstlane(lds_addr)),
+      "v"(voff), "s"(rsrc), "s"(__builtin_amdgcn_readfirstlane(soff))
+      : "memory");
+}
+
+// ----------------------------------------------------------- tile kernel
+
+// BM x BN tiles, WM x WN waves, two LDS slots of 128-byte rows swizzled as in
+// the direct-to-LDS kernel.  Per K-step: wait for the step's loads, barrier
+// (which also frees the other slot), then the wave's MFMAs with the next
+// step's loads spread between them.
+template <int BM, int BN, int WM, int WN, int OP, int OUT>
+__global__ __attribute__((amdgpu_flat_work_group_size(WM * WN * 64, WM * WN * 64),
+                          amdgpu_waves_per_eu(2, 2))) void
+block_tile_kernel(BlockArgs a) {
+  using Cfg = TileCfg<BM, BN, 64, WM, WN, 2, 3, 16>;
+  constexpr int T = Cfg::kThreads, W = WM * WN;
+  constexpr int FM = Cfg::kFragM, FN = Cfg::kFragN;
+  constexpr int LA = Cfg::kLoadsA, LB = Cfg::kLoadsB, L = LA + LB;
+  constexpr int RPI = T / 8;  // rows of one load of all threads
+  constexpr bool kScaled = OP == kOpE4m3;
+  constexpr int NB = (BN + kScaleBlock - 1) / kScaleBlock;  // scale blocks across a tile
+  static_assert(RPI % 16 == 0, "the swizzle repeats every 16 rows");
+  static_assert(kScaleBlock % Cfg::kWaveN == 0, "a wave's columns share one scale");
+  static_assert(BM / 64 <= W, "one wave loads 64 row scales");
+  static_assert(L <= FM * FN, "loads fit between the MFMAs");
+
+  __shared__ __attribute__((aligned(1024))) uint8_t smem_raw[Cfg::kLdsBytes];
+  __shared__ float sa_lds[kScaled ? 2 * BM : 1];
+  __shared__ float sb_lds[kScaled ? NB * kMaxKSteps : 1];
+  lds_u8* const smem = (lds_u8*)smem_raw;
+  const uint32_t smem_addr = (uint32_t)(uintptr_t)smem;
+  typedef const __attribute__((address_space(3))) float lds_f32;
+  lds_f32* const sa_s = (lds_f32*)sa_lds;
+  lds_f32* const sb_s = (lds_f32*)sb_lds;
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+
+  // ---- which tile --------------------------------------------------------
+  const int row_tiles = a.offsets ? count_row_tiles(a, BM, lane) : a.row_tiles;
+  const int units = row_tiles * a.tiles_n;
+  if ((int)blockIdx.x >= units) return;  // the grid is an upper bound
+  const int logical = xcd_remap(blockIdx.x, units);
+  const int span = a.group_m * a.tiles_n;
+  const int gid = logical / span;
+  const int first = gid * a.group_m;
+  const int gsz = min(row_tiles - first, a.group_m);
+  const int in = logical - gid * span;
+  const int rt = first + in % gsz;
+  const int n0 = (in / gsz) * BN;
+  RowTile tile;
+  if (a.offsets) {
+    if (!find_row_tile(a, BM, rt, lane, tile)) return;
+  } else {
+    tile = RowTile{0, rt * BM, a.M};
+  }
+  const int m0 = tile.begin;
+  const int rows_a = min(BM, tile.end - m0);
+  const int rows_b = min(BN, a.N - n0);
+
+  // ---- loads -------------------------------------------------------------
+  const bool gather = a.rows != nullptr;
+  const u32x4 rsrc_a = gather ? make_rsrc(a.A, (uint32_t)((int64_t)a.a_rows * a.lda))
+                              : make_rsrc(a.A + (int64_t)m0 * a.lda, (uint32_t)(rows_a * a.lda));
+  const u32x4 rsrc_b = make_rsrc(a.B + tile.expert * a.stride_b + (int64_t)n0 * a.ldb,
+                                 (uint32_t)(rows_b * a.ldb));
+  const int r0 = tid / 8;
+  const int chunk = (tid & 7) ^ swz<3, 8>(r0);
+  uint32_t voff[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int row = (i < LA ? i : i - LA) * RPI + r0;
+    if (i < LA) {
+      const int src = row < rows_a ? (gather ? source_row(a, m0 + row) : row) : -1;
+      voff[i] = src >= 0 ? (uint32_t)(src * (int)a.lda + chunk * 16) : kOOB;
+    } else {
+      voff[i] = row < rows_b ? (uint32_t)(row * (int)a.ldb + chunk * 16) : kOOB;
+    }
+  }
+  uint32_t voff_s = kOOB;  // this lane's row scale (waves 0 .. BM / 64 - 1)
+  if constexpr (kScaled) {
+    const int row = wave * 64 + lane;
+    if (row < rows_a) {
+      const int src = gather ? source_row(a, m0 + row) : m0 + row;
+      if (src >= 0) voff_s = (uint32_t)src * 4;
+    }
+    // the tile's B scales of every K-step, once
+    const float* sb = a.SB + tile.expert * a.stride_sb;
+    const int per = (a.k_steps + 63) / 64;
+    for (int c = wave; c < NB * per; c += W) {
+      const int nb = c / per, k = (c % per) * 64 + lane;
+      const int row = n0 / kScaleBlock + nb;
+      const u32x4 rs = make_rsrc(sb + (int64_t)row * a.ldsb,
+                                 row * kScaleBlock < a.N ? (uint32_t)a.k_steps * 4 : 0u);
+      dma4(rs, (uint32_t)(uintptr_t)sb_s + (nb * kMaxKSteps + (c % per) * 64) * 4, (uint32_t)k * 4,
+           0u);
+    }
+  }
+  const bool past_k = (a.k_steps - 1) * kStepBytes + chunk * 16 >= a.kbytes;  // in the last step
+  auto load_one = [&](int X, int i) __attribute__((always_inline)) {
+    const uint32_t dst = smem_addr + (X & 1) * Cfg::kStageBytes + (i < LA ? 0 : Cfg::kABytes) +
+                         (((i < LA ? i : i - LA) * T + wave * 64) * 16);
+    // past K, and in the step past the last one, a load reads zeros: no
+    // branch splits the loop body
+    const uint32_t v = X >= a.k_steps - (past_k ? 1 : 0) ? kOOB : voff[i];
+    dma16(i < LA ? rsrc_a : rsrc_b, dst, v, (uint32_t)(X * kStepBytes));
+  };
+  auto load_scales = [&](int X) __attribute__((always_inline)) {
+    if constexpr (kScaled) {
+      if (wave < BM / 64) {
+        const u32x4 rs =
+            make_rsrc(a.SA + X * a.ldsa, X < a.k_steps ? (uint32_t)a.a_rows * 4 : 0u);
+        dma4(rs, (uint32_t)(uintptr_t)sa_s + ((X & 1) * BM + wave * 64) * 4, voff_s, 0u);
+      }
+    }
+  };
+  // Zero the bytes past K of the 16-byte chunk that straddles it, each
+  // thread in the chunks it loaded (their loads have landed).
+  auto trim = [&](int X) __attribute__((always_inline)) {
+    const int keep = a.kbytes - (X * kStepBytes + chunk * 16);
+    if (keep > 0 && keep < 16) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) {
+        lds_u32x4* p = (lds_u32x4*)(smem + (X & 1) * Cfg::kStageBytes + (i < LA ? 0 : Cfg::kABytes) +
+                                    ((i < LA ? i : i - LA) * T + tid) * 16);
+        u32x4 v = *p;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const int left = keep - 4 * w;
+          v[w] &= left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+        }
+        *p = v;
+      }
+    }
+  };
+
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+
+#pragma unroll
+  for (int i = 0; i < L; ++i) load_one(0, i);
+  load_scales(0);
+
+  // byte address of this lane's first chunk of its row in fragment 0; the
+  // second chunk is 64 bytes away before the swizzle, so 64 by XOR after it
+  const int lrow = lane & 15;
+  const int at = lrow * kStepBytes + (((lane >> 4) ^ swz<3, 8>(lrow)) << 4);
+  const lds_u8* const pa = smem + wm * Cfg::kWaveM * kStepBytes;
+  const lds_u8* const pb = smem + Cfg::kABytes + wn * Cfg::kWaveN * kStepBytes;
+  auto read_frag = [&](const lds_u8* base, int f, u32x4 (&v)[2]) __attribute__((always_inline)) {
+    v[0] = *(const lds_u32x4*)(base + f * 16 * kStepBytes + at);
+    v[1] = *(const lds_u32x4*)(base + f * 16 * kStepBytes + (at ^ 64));
+  };
+
+  for (int X = 0; X < a.k_steps; ++X) {
+    if (X == a.k_steps - 1 && (a.kbytes & 15) != 0) {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      trim(X);
+    }
+    ring_wait_barrier<0>();
+    const uint32_t slot = (X & 1) * Cfg::kStageBytes;
+    u32x4 fb[FN][2], fa[2][2];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) read_frag(pb + slot, j, fb[j]);
+    read_frag(pa + slot, 0, fa[0]);
+    float sb = 0.0f;
+    if constexpr (kScaled)
+      sb = sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + X];
+    f32x4 part[2][FN];
+    float sc[2];
+#pragma unroll
+    for (int i = 0; i < FM + 1; ++i) {
+      if (i < FM) {
+        if constexpr (kScaled)
+          sc[i & 1] = sa_s[(X & 1) * BM + wm * Cfg::kWaveM + i * 16 + lrow] * sb;
+        if (i + 1 < FM) read_frag(pa + slot, i + 1, fa[(i + 1) & 1]);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          if constexpr (kScaled)
+            part[i & 1][j] =
+                step_mfma<OP>(fb[j], fa[i & 1], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+          else
+            acc[i][j] = step_mfma<OP>(fb[j], fa[i & 1], acc[i][j]);
+        }
+#pragma unroll
+        for (int l = 0; l < L; ++l)
+          if (l * FM / L == i) load_one(X + 1, l);
+        if (i == 0) load_scales(X + 1);
+      }
+      if constexpr (kScaled) {
+        if (i > 0) {
+#pragma unroll
+          for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[i - 1][j][r] =
+                  __builtin_fmaf(part[(i - 1) & 1][j][r], sc[(i - 1) & 1], acc[i - 1][j][r]);
+        }
+      }
+      // (without it the scheduler reads every fragment first, and spills)
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+
+  KernelArgs k{};
+  k.C = a.C;
+  k.ldc = a.ldc;
+  k.M = tile.end;
+  k.N = a.N;
+  finish_tile<Cfg, OUT, false>(k, smem, wave, m0, n0, acc, m0 + wm * Cfg::kWaveM,
+                               n0 + wn * Cfg::kWaveN, lane, 0);
+}
+
+// ------------------------------------------------------------ row kernel
+
+// Buffer resource over num_bytes bytes from base, for the load builtins.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, uint32_t num_bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, (int)num_bytes, 0x00020000);
+}
+
+// 16 FM rows x 16 FN columns per workgroup, its W waves taking every W-th
+// K-step.  Operands go from global memory into registers in the MFMA's own
+// layout (a lane holds two 16-byte chunks of its row), U steps ahead; the
+// waves' sums meet in LDS and are added in the order of the waves.
+template <int FM, int FN, int W, int U, int OP, int OUT>
+__global__ __attribute__((amdgpu_flat_work_group_size(W * 64, W * 64))) void
+block_row_kernel(BlockArgs a) {
+  constexpr bool kScaled = OP == kOpE4m3;
+  constexpr int BM = 16 * FM, BN = 16 * FN;
+  static_assert(kScaleBlock % BN == 0, "the tile's columns share one scale");
+  __shared__ f32x4 sums[W][FM * FN][64];
+
+  const int tid = threadIdx.x;
+  const int lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lrow = lane & 15, lchunk = (lane >> 4) * 16;
+
+  const int rt = blockIdx.x / a.tiles_n;
+  const int n0 = (blockIdx.x - rt * a.tiles_n) * BN;
+  RowTile tile;
+  if (a.offsets) {
+    if (!find_row_tile(a, BM, rt, lane, tile)) return;
+  } else {
+    tile = RowTile{0, rt * BM, a.M};
+  }
+  const int m0 = tile.begin;
+  const bool gather = a.rows != nullptr;
+  const int rows_a = min(BM, tile.end - m0), rows_b = min(BN, a.N - n0);
+  const __amdgpu_buffer_rsrc_t rsrc_a =
+      gather ? buffer_of(a.A, (uint32_t)((int64_t)a.a_rows * a.lda))
+             : buffer_of(a.A + (int64_t)m0 * a.lda, (uint32_t)(rows_a * a.lda));
+  const __amdgpu_buffer_rsrc_t rsrc_b = buffer_of(a.B + tile.expert * a.stride_b + (int64_t)n0 * a.ldb,
+                                 (uint32_t)(rows_b * a.ldb));
+  uint32_t va[FM], vb[FN], vs[FM];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    const int row = i * 16 + lrow;
+    const int src = row < rows_a ? (gather ? source_row(a, m0 + row) : row) : -1;
+    va[i] = src >= 0 ? (uint32_t)(src * (int)a.lda + lchunk) : kOOB;
+    vs[i] = src >= 0 ? (uint32_t)(gather ? src : m0 + src) * 4 : kOOB;
+  }
+#pragma unroll
+  for (int j = 0; j < FN; ++j) {
+    const int row = j * 16 + lrow;
+    vb[j] = row < rows_b ? (uint32_t)(row * (int)a.ldb + lchunk) : kOOB;
+  }
+  const float* sb_row = a.SB + tile.expert * a.stride_sb + (int64_t)(n0 / kScaleBlock) * a.ldsb;
+
+  struct Stage {
+    u32x4 fa[FM][2], fb[FN][2];
+    float sa[FM], sb;
+  };
+  Stage st[U];
+  auto load = [&](Stage& s, int X) __attribute__((always_inline)) {
+    // bytes left of the row at this lane's two chunks; past K reads zero
+    const int k0 = X * kStepBytes;
+    const bool in0 = k0 + lchunk < a.kbytes, in1 = k0 + 64 + lchunk < a.kbytes;
+    auto get = [&](__amdgpu_buffer_rsrc_t rs, uint32_t v, bool in, int off, auto nt)
+        __attribute__((always_inline)) {
+      return __builtin_amdgcn_raw_buffer_load_b128(rs, in ? v + off : kOOB, k0,
+                                                   decltype(nt)::value ? 2 : 0);
+    };
+    const std::true_type nt{};    // B is read by this workgroup alone
+    const std::false_type keep{};
+#pragma unroll
+    for (int j = 0; j < FN; ++j) {
+      s.fb[j][0] = get(rsrc_b, vb[j], in0, 0, nt);
+      s.fb[j][1] = get(rsrc_b, vb[j], in1, 64, nt);
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      s.fa[i][0] = get(rsrc_a, va[i], in0, 0, keep);
+      s.fa[i][1] = get(rsrc_a, va[i], in1, 64, keep);
+    }
+    if constexpr (kScaled) {
+      const __amdgpu_buffer_rsrc_t rs = buffer_of(a.SA + X * a.ldsa, (uint32_t)a.a_rows * 4);
+#pragma unroll
+      for (int i = 0; i < FM; ++i)
+        s.sa[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(rs, vs[i], 0, 0));
+      s.sb = sb_row[X];
+    }
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+  // Zero the bytes past K of a chunk that straddles it.
+  auto trim = [&](u32x4& v, int keep) __attribute__((always_inline)) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int left = keep - 4 * w;
+      v[w] &= left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
+    }
+  };
+  auto multiply = [&](Stage& s, int X) __attribute__((always_inline)) {
+    if (X == a.k_steps - 1 && (a.kbytes & 15) != 0) {
+      const int keep = a.kbytes - X * kStepBytes - lchunk;
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        trim(s.fa[i][0], keep);
+        trim(s.fa[i][1], keep - 64);
+      }
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        trim(s.fb[j][0], keep);
+        trim(s.fb[j][1], keep - 64);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        if constexpr (kScaled) {
+          const f32x4 p = step_mfma<OP>(s.fb[j], s.fa[i], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+          const float sc = s.sa[i] * s.sb;
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], sc, acc[i][j][r]);
+        } else {
+          acc[i][j] = step_mfma<OP>(s.fb[j], s.fa[i], acc[i][j]);
+        }
+      }
+  };
+#pragma unroll
+  for (int u = 0; u < U; ++u)
+    if (wave + u * W < a.k_steps) load(st[u], wave + u * W);
+  for (int X = wave; X < a.k_steps; X += U * W) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int Y = X + u * W;
+      if (Y < a.k_steps) {
+        multiply(st[u], Y);
+        if (Y + U * W < a.k_steps) load(st[u], Y + U * W);
+      }
+    }
+  }
+
+#pragma unroll
+  for (int i = 0; i < FM; ++i)
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sums[wave][i * FN + j][lane] = acc[i][j];
+  __syncthreads();
+  for (int q = tid; q < FM * FN * 64; q += W * 64) {
+    const int f = q >> 6, l = q & 63;
+    f32x4 v = sums[0][f][l];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += sums[w][f][l];
+    const int row = (f / FN) * 16 + (l & 15);
+    if (row < rows_a)
+      store_quad<OUT>(a.C, a.ldc, v, m0 + row, n0 + (f % FN) * 16 + 4 * (l >> 4), a.N);
+  }
+}
+
+}  // namespace gemm

@@ -1,0 +1,63 @@
+// Launchers of the block-scaled and experts' products: each block_inst_*.hip
+// file instantiates one workgroup shape for its operand and output types.
+#pragma once
+
+#include "block_internal.h"
+
+namespace gemm {
+
+template <typename Launch>
+hipError_t by_types(int op, int out, Launch&& launch) {
+  auto by_out = [&](auto o) {
+    switch (out) {
+      case kStoreBf16: return launch(o, std::integral_constant<int, kStoreBf16>{});
+      case kStoreF16: return launch(o, std::integral_constant<int, kStoreF16>{});
+      default: return launch(o, std::integral_constant<int, kStoreF32>{});
+    }
+  };
+  switch (op) {
+    case kOpE4m3: return by_out(std::integral_constant<int, kOpE4m3>{});
+    case kOpBf16: return by_out(std::integral_constant<int, kOpBf16>{});
+    default: return by_out(std::integral_constant<int, kOpF16>{});
+  }
+}
+
+template <int BM, int BN, int WM, int WN>
+hipError_t launch_block_tile(const BlockArgs& a, int grid, hipStream_t s, int op, int out) {
+  return by_types(op, out, [&](auto o, auto t) {
+    hipLaunchKernelGGL((block_tile_kernel<BM, BN, WM, WN, decltype(o)::value, decltype(t)::value>),
+                       dim3(grid), dim3(WM * WN * 64), 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+template <int FM, int FN, int W, int U>
+hipError_t launch_block_row(const BlockArgs& a, int grid, hipStream_t s, int op, int out) {
+  return by_types(op, out, [&](auto o, auto t) {
+    hipLaunchKernelGGL((block_row_kernel<FM, FN, W, U, decltype(o)::value, decltype(t)::value>),
+                       dim3(grid), dim3(W * 64), 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+// Built shapes: X(name, launcher template arguments).
+#define BLOCK_TILES(X)        \
+  X(b256x256, 256, 256, 2, 4) \
+  X(b128x128, 128, 128, 2, 2)
+#define BLOCK_ROWS(X)    \
+  X(r16x16, 1, 1, 4, 4)  \
+  X(r32x32, 2, 2, 4, 2)  \
+  X(r64x32, 4, 2, 4, 2)
+
+#define BLOCK_DECLARE(NAME, A, B, C, D)                                                       \
+  extern template hipError_t launch_block_tile<A, B, C, D>(const BlockArgs&, int, hipStream_t, \
+                                                           int, int);
+BLOCK_TILES(BLOCK_DECLARE)
+#undef BLOCK_DECLARE
+#define BLOCK_DECLARE(NAME, A, B, C, D)                                                      \
+  extern template hipError_t launch_block_row<A, B, C, D>(const BlockArgs&, int, hipStream_t, \
+                                                          int, int);
+BLOCK_ROWS(BLOCK_DECLARE)
+#undef BLOCK_DECLARE
+
+}  // namespace gemm

@@ -13,14 +13,15 @@
 #include "gemm_internal.h"
 
 namespace gemm {
-namespace {
 
-thread_local int g_last_hip_error = 0;
+static thread_local int g_last_hip_error = 0;
 
 int hip_fail(hipError_t e) {
   g_last_hip_error = (int)e;
   return GEMM_ERR_HIP;
 }
+
+namespace {
 
 // ---------------------------------------------------------------- workspaces
 // One split-K workspace per (device, stream), holding the fp32 partial

@@ -25,6 +25,10 @@ struct TileConfig {
   hipError_t (*launch)(const KernelArgs&, int grid, hipStream_t, int flags);
 };
 
+// Records a failed HIP call for gemm_bf16_last_hip_error and returns
+// GEMM_ERR_HIP.
+int hip_fail(hipError_t e);
+
 // Table of built configurations, terminated by an entry with name == NULL.
 const TileConfig* tile_configs();
 

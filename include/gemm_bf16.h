@@ -240,6 +240,162 @@ int gemm_bf16_ex_noalloc(const char* config,
                          void* C, int64_t ldc,
                          int out_f32, void* stream);
 
+/* ------------------------------------------------- 8-bit floating point
+ * Products over e4m3 operands (OCP 8-bit floating point, 4 exponent and 3
+ * mantissa bits, largest value 448, no infinities) with one fp32 scale for
+ * each block of 128:
+ *
+ *   C[m,n] = sum_b SA[b,m] * SB[n / 128, b] * sum_{k in block b} A[m,k] * B[n,k]
+ *
+ * where block b is columns 128 b .. 128 b + 127 of K (the last one may be
+ * shorter).  A has a scale for each row and block, B one for each 128 x 128
+ * block.
+ *
+ * Layouts (strides in elements, pointers on the current device):
+ *   A(m,k) = A[m*lda + k], B(n,k) = B[n*ldb + k], C(m,n) = C[m*ldc + n]
+ *   SA(b,m) = SA[b*ldsa + m], ldsa >= M            (block-major: the scales
+ *                          of one K-step are contiguous)
+ *   SB(j,b) = SB[j*ldsb + b], ldsb >= ceil(K / 128), ceil(N / 128) rows
+ * A and B 16-byte aligned with lda and ldb multiples of 16; C 16-byte
+ * aligned with ldc a multiple of 8; scales 4-byte aligned.  Any M, N, K >= 0
+ * up to K = 262144 (GEMM_ERR_UNSUPPORTED past it); K == 0 sets C to zeros.
+ *
+ * Numerics: the 128 products of a block are summed by the matrix core in
+ * fp32, multiplied by the fp32 product of the two scales and added to an
+ * fp32 sum, in an order fixed by the shape's kernel; C is that sum rounded
+ * once to its type.  Scales may be any fp32 value; a NaN code or scale makes
+ * the sums it enters NaN.  Elements past K in a row (up to lda) are not used
+ * whatever they hold.
+ *
+ * Streams and errors as above.  These calls need no workspace: nothing is
+ * allocated, calls on different streams may overlap, and all may be
+ * captured into graphs. */
+
+/* Element types. */
+#define GEMM_TYPE_BF16 0
+#define GEMM_TYPE_F16 1
+#define GEMM_TYPE_F32 2
+#define GEMM_TYPE_E4M3 3
+
+/* The product; c_type is GEMM_TYPE_BF16, _F16 or _F32.  Returns a status. */
+int gemm_fp8(int64_t M, int64_t N, int64_t K,
+             const void* A, int64_t lda, const float* SA, int64_t ldsa,
+             const void* B, int64_t ldb, const float* SB, int64_t ldsb,
+             void* C, int64_t ldc, int c_type, void* stream);
+
+/* As gemm_fp8 with the kernel shape named (one that gemm_fp8_config_at
+ * enumerates; NULL or "" = automatic).  Unknown name: GEMM_ERR_UNSUPPORTED. */
+int gemm_fp8_ex(const char* config, int64_t M, int64_t N, int64_t K,
+                const void* A, int64_t lda, const float* SA, int64_t ldsa,
+                const void* B, int64_t ldb, const float* SB, int64_t ldsb,
+                void* C, int64_t ldc, int c_type, void* stream);
+
+/* Name of the kernel shape gemm_fp8 chooses: "b<BM>x<BN>" stages tiles
+ * through LDS, "r<BM>x<BN>" streams B into registers.  Static storage. */
+const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K);
+
+/* The i-th kernel shape (of gemm_fp8 and gemm_moe), or NULL past the end. */
+const char* gemm_fp8_config_at(int i);
+
+/* Activations of gemm_fp8_quantize. */
+#define GEMM_ACT_NONE 0
+#define GEMM_ACT_SWIGLU 1 /* silu(g) * u; g: columns 0 .. K-1 of X, u: K .. 2K-1 */
+
+/* Quantise X (M rows of K columns, 2 K with GEMM_ACT_SWIGLU; x_type BF16, F16
+ * or F32; 16-byte aligned, ldx a multiple of 8) to e4m3 codes Q (M x K,
+ * 16-byte aligned, ldq a multiple of 16; a row's bytes past K are left as
+ * they were) and scales S:
+ *   amax = max(largest |x| of the block, 2^-100), S = amax / 448,
+ *   Q = x * (448 / amax) rounded to nearest even (all in fp32).
+ * block_rows 1: blocks of 1 x 128, S(b,m) = S[b*lds + m] (gemm_fp8's SA);
+ * block_rows 128: blocks of 128 x 128, S(j,b) = S[j*lds + b] (its SB;
+ * without activation only).  NaN gives a NaN code and is left out of amax;
+ * a block with an infinity gets an infinite scale.  M is limited to
+ * 1048560 rows a call.  Returns a status. */
+int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_type, int act,
+                      int block_rows, void* Q, int64_t ldq, float* S, int64_t lds,
+                      void* stream);
+
+/* ----------------------------------------------------- mixture of experts
+ * The pieces of a mixture-of-experts layer around and between its products:
+ * route tokens, plan (sort the routed rows by expert), the experts'
+ * products, and the weighted sum back to tokens.  Everything stays on the
+ * device: no call waits for, or copies back, how many rows an expert got. */
+
+/* Scores of gemm_moe_route. */
+#define GEMM_SCORE_SOFTMAX 0
+#define GEMM_SCORE_SIGMOID 1
+
+/* Route T tokens over E experts (E <= 1024), k each (k <= 64).  X: T rows of
+ * E logits (x_type BF16, F16 or F32, row stride ldx, any alignment of the
+ * type).  Per token:
+ *   s = softmax or sigmoid of the logits
+ *   c = s + bias            (bias: E fp32 values, or NULL for none)
+ *   the experts form `groups` equal groups (<= 64, dividing E); a group's
+ *   score is its largest c (group_top 1) or the sum of its two largest
+ *   (group_top 2); only the topk_groups best groups stay
+ *   ids = the k largest c that stay, in descending order
+ *   weights = s[ids], divided by their sum if renorm != 0, times scale
+ * ids (T x k int32) and weights (T x k fp32) are contiguous.  The order is
+ * that of the exact values, ties by lowest index (of groups too): it does
+ * not depend on rounding in the scores.  A NaN logit counts as -infinity, a
+ * logit of +infinity as the largest finite number; masked (-infinity)
+ * experts have score 0 and are taken, at weight 0, only when the others run
+ * out; weights that sum to 0 are all 0.  k may not exceed the experts of
+ * topk_groups groups.  Returns a status. */
+int gemm_moe_route(int64_t T, int64_t E, int64_t k, const void* X, int64_t ldx, int x_type,
+                   const float* bias, int score, int64_t groups, int64_t topk_groups,
+                   int group_top, int renorm, float scale, int32_t* ids, float* weights,
+                   void* stream);
+
+/* Sort the R = T * k (token, slot) pairs by expert, stably.
+ *   offsets (E + 1): expert e's sorted rows are offsets[e] .. offsets[e+1]-1
+ *   rows (R): the token of each sorted row; -1 from offsets[E] on
+ *   pos (T x k): the sorted row of each pair; -1 where the id names no expert
+ * An id outside 0 .. E-1 drops its pair (an expert another device holds, a
+ * padded token).  R < 2^30, E <= 65535.  Returns a status. */
+int gemm_moe_plan(int64_t T, int64_t k, int64_t E, const int32_t* ids, int32_t* offsets,
+                  int32_t* rows, int32_t* pos, void* stream);
+
+/* The experts' products: for each expert e and sorted row p in
+ * [offsets[e], offsets[e+1]),
+ *   C[p] = A[rows[p]] . B_e^T     (A[p] where rows is NULL)
+ * type GEMM_TYPE_E4M3: scaled as gemm_fp8, with SA over A's rows and expert
+ * e's scales at SB + e*stride_sb; GEMM_TYPE_BF16 / _F16: plain products with
+ * fp32 sums (SA and SB unused).  C has R rows; A has T rows (T >= R where
+ * rows is NULL); expert e's B, N rows of K, is at B + e*stride_b.  Rows of C
+ * that no expert's range holds are left as they were.  Alignment as for
+ * gemm_fp8 (16-bit types: lda, ldb and stride_b multiples of 8); with rows,
+ * T * lda must stay below 2^31 - 4096 bytes.  offsets and rows that point
+ * outside C or A are cut to them (a row outside A reads as zeros); ranges
+ * that overlap give unspecified rows.  Returns a status. */
+int gemm_moe(int type, int64_t R, int64_t N, int64_t K, int64_t E, int64_t T,
+             const void* A, int64_t lda, const float* SA, int64_t ldsa,
+             const int32_t* offsets, const int32_t* rows,
+             const void* B, int64_t ldb, int64_t stride_b,
+             const float* SB, int64_t ldsb, int64_t stride_sb,
+             void* C, int64_t ldc, int c_type, void* stream);
+
+/* As gemm_moe with the kernel shape named (see gemm_fp8_ex). */
+int gemm_moe_ex(const char* config, int type, int64_t R, int64_t N, int64_t K, int64_t E,
+                int64_t T, const void* A, int64_t lda, const float* SA, int64_t ldsa,
+                const int32_t* offsets, const int32_t* rows,
+                const void* B, int64_t ldb, int64_t stride_b,
+                const float* SB, int64_t ldsb, int64_t stride_sb,
+                void* C, int64_t ldc, int c_type, void* stream);
+
+/* Name of the kernel shape gemm_moe chooses.  Static storage. */
+const char* gemm_moe_config_name(int64_t R, int64_t N, int64_t K, int64_t E);
+
+/* out[t] = sum over j = 0 .. k-1 of weights[t*k + j] * Y[pos[t*k + j]], fp32
+ * sums in that order, rounded once.  Y: R rows of N (y_type), out: T rows of
+ * N (out_type; BF16, F16 or F32 each), both 16-byte aligned with strides
+ * multiples of 8.  A pos outside 0 .. R-1 adds nothing; a token whose pairs
+ * were all dropped gets zeros.  Returns a status. */
+int gemm_moe_combine(int64_t T, int64_t k, int64_t N, int64_t R, const void* Y, int64_t ldy,
+                     int y_type, const int32_t* pos, const float* weights, void* out,
+                     int64_t ldo, int out_type, void* stream);
+
 /* Human-readable text for a status code.  Static storage; never NULL. */
 const char* gemm_bf16_status_string(int status);
 

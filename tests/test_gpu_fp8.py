@@ -1,0 +1,336 @@
+"""Quantising to e4m3 blocks and the products over them, on the GPU, against
+64-bit forms: bit-exact where every sum is exact, else within bounds counted
+from the roundings."""
+import numpy as np
+import pytest
+
+from block_ref import HALF_STEP, block_product, check_rounded, dtype, padded
+
+pytestmark = pytest.mark.gpu
+
+CONFIGS = ["b256x256", "b128x128", "r16x16", "r32x32", "r64x32"]
+
+
+def small_ints(rng, shape):
+    return rng.integers(-4, 5, shape).astype(np.float32)
+
+
+def two_powers(rng, shape):
+    return 2.0 ** rng.integers(-2, 3, shape).astype(np.float32)
+
+
+def product(a, sa, b, sb, out, config=None, extra=1, c=None):
+    """The GPU's C; operands sit in wider buffers filled with NaN."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    A = padded(torch.from_numpy(a).to(dtype("e4m3")), 16, extra)
+    B = padded(torch.from_numpy(b).to(dtype("e4m3")), 16, extra)
+    SA = padded(torch.from_numpy(sa), 1, extra)
+    SB = padded(torch.from_numpy(sb), 1, extra)
+    C = g.matmul_fp8(A, SA, B, SB, out=c, out_dtype=None if c is not None else dtype(out),
+                     config=config)
+    torch.cuda.synchronize()
+    return C.float().cpu().numpy().astype(np.float64)
+
+
+def exact_case(M, N, K, seed):
+    rng = np.random.default_rng(seed)
+    kb, nb = -(-K // 128), -(-N // 128)
+    return (small_ints(rng, (M, K)), two_powers(rng, (kb, M)), small_ints(rng, (N, K)),
+            two_powers(rng, (nb, kb)))
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("config", CONFIGS)
+def test_every_shape_is_exact_on_integers(config, out):
+    """Ragged in M, N and K; products of integers and powers of two sum
+    exactly in fp32 in any order, so C is one rounding of the true sum."""
+    import torch
+
+    from dense_gemm_bf16_amd import fp8_config_names
+
+    assert sorted(fp8_config_names()) == sorted(CONFIGS)
+    a, sa, b, sb = exact_case(300, 389, 712, 1)
+    got = product(a, sa, b, sb, out, config)
+    want, _ = block_product(a, sa, b, sb)
+    assert np.array_equal(want, want.astype(np.float32))
+    ref = torch.from_numpy(want.astype(np.float32)).to(dtype(out)).float().numpy()
+    assert np.array_equal(got, ref.astype(np.float64))
+
+
+@pytest.mark.parametrize("K", [1, 15, 16, 17, 64, 100, 127, 128, 129, 143, 255, 257, 1000])
+@pytest.mark.parametrize("config", ["b256x256", "b128x128", "r16x16", "r64x32"])
+def test_every_end_of_k(config, K):
+    a, sa, b, sb = exact_case(37, 70, K, K)
+    want, _ = block_product(a, sa, b, sb)
+    assert np.array_equal(product(a, sa, b, sb, "f32", config), want)
+
+
+@pytest.mark.parametrize("M, N, K", [
+    (1, 1, 128), (1, 8192, 1024), (3, 17, 4096), (16, 130, 2048), (17, 257, 384), (33, 1000, 640),
+    (64, 512, 8192), (65, 127, 256), (129, 385, 1152), (256, 640, 2048), (500, 513, 1100)])
+def test_automatic_shapes_on_normal_values(M, N, K):
+    import torch
+
+    rng = np.random.default_rng(M * 7 + N)
+    kb, nb = -(-K // 128), -(-N // 128)
+    a = torch.from_numpy(rng.normal(0, 100, (M, K)).clip(-448, 448)).to(dtype("e4m3")).float().numpy()
+    b = torch.from_numpy(rng.normal(0, 100, (N, K)).clip(-448, 448)).to(dtype("e4m3")).float().numpy()
+    sa = np.exp(rng.normal(-5, 1, (kb, M))).astype(np.float32)
+    sb = np.exp(rng.normal(-7, 1, (nb, kb))).astype(np.float32)
+    want, err = block_product(a, sa, b, sb)
+    for out in ("f32", "bf16", "f16"):
+        check_rounded(product(a, sa, b, sb, out), want, err, out)
+
+
+def test_special_codes_and_scales():
+    """Every finite e4m3 code, large scales, zero scales; a NaN code or scale
+    reaches only the sums it enters.  (Codes from 256 = 2^8 on, times 2^120,
+    pass fp32's largest value, just below 2^128: infinity.)"""
+    import torch
+
+    codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
+    codes = np.where(np.isnan(codes), 0, codes)
+    a = np.tile(codes, (3, 1)).astype(np.float32)
+    b = np.eye(256, dtype=np.float32)
+    sa = np.array([[1, 2.0 ** 60, 0], [1, 2.0 ** 60, 0]], np.float32)
+    sb = np.full((2, 2), 2.0 ** 60, np.float32)
+    for config in CONFIGS:
+        got = product(a, sa, b, sb, "f32", config)
+        want = codes[None].astype(np.float64) * np.array([[2.0 ** 60], [2.0 ** 120], [0]])
+        want[want >= 2.0 ** 128], want[want <= -2.0 ** 128] = np.inf, -np.inf
+        assert np.array_equal(got, want)
+        a2 = a.copy()
+        a2[1, 5] = np.nan
+        s2 = sb.copy()
+        s2[1, 1] = np.nan
+        got = product(a2, sa, b, s2, "f32", config)
+        assert np.isnan(got[:, 128:]).all() and np.isnan(got[1]).all()
+        assert np.isfinite(got[[0, 2], :128]).all()
+
+
+def test_c_outside_its_range_is_left_alone():
+    import torch
+
+    for config in CONFIGS:
+        a, sa, b, sb = exact_case(70, 45, 200, 3)
+        buf = torch.full((74, 64), 7.0, device="cuda", dtype=torch.bfloat16)
+        product(a, sa, b, sb, "bf16", config, c=buf[2:72, 8:53])
+        got = buf.float().cpu().numpy()
+        want, _ = block_product(a, sa, b, sb)
+        ref = torch.from_numpy(want.astype(np.float32)).bfloat16().float().numpy()
+        assert np.array_equal(got[2:72, 8:53], ref)
+        got[2:72, 8:53] = 7.0
+        assert (got == 7.0).all()
+
+
+def test_k_zero_gives_zeros_and_empty_shapes():
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    e = torch.empty((5, 0), device="cuda", dtype=torch.float8_e4m3fn)
+    s = torch.empty((0, 5), device="cuda")
+    for config in CONFIGS:
+        C = g.matmul_fp8(e, s, e, torch.empty((1, 0), device="cuda"), config=config)
+        assert C.shape == (5, 5) and bool((C == 0).all())
+    A = torch.zeros((0, 256), device="cuda", dtype=torch.float8_e4m3fn)
+    B = torch.zeros((8, 256), device="cuda", dtype=torch.float8_e4m3fn)
+    assert g.matmul_fp8(A, torch.empty((2, 0), device="cuda"), B, torch.ones((1, 2), device="cuda")).shape == (0, 8)
+
+
+def test_repeats_are_the_same_bits():
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = torch.Generator(device="cuda").manual_seed(1)
+    for M, N, K in ((8, 4096, 4096), (300, 1000, 2000), (1024, 2048, 1024)):
+        A = torch.randn((M, K), device="cuda", generator=rng).to(torch.float8_e4m3fn)
+        B = torch.randn((N, K), device="cuda", generator=rng).to(torch.float8_e4m3fn)
+        kb = -(-K // 128)
+        SA = torch.rand((kb, M), device="cuda", generator=rng)
+        SB = torch.rand((-(-N // 128), kb), device="cuda", generator=rng)
+        first = g.matmul_fp8(A, SA, B, SB, out_dtype=torch.float32)
+        for _ in range(5):
+            assert torch.equal(first, g.matmul_fp8(A, SA, B, SB, out_dtype=torch.float32))
+
+
+# ------------------------------------------------------------------ quantising
+
+def quantize_ref(x):
+    """Codes (as values) and scales of rows, in fp32 as the header states."""
+    import torch
+
+    M, K = x.shape
+    kb = -(-K // 128)
+    p = np.zeros((M, kb * 128), np.float32)
+    p[:, :K] = x
+    p = p.reshape(M, kb, 128)
+    with np.errstate(all="ignore"):
+        amax = np.fmax(np.fmax.reduce(np.abs(p), 2), np.float32(2.0 ** -100))
+        inv = (np.float32(448) / amax).astype(np.float32)
+        q = (p * inv[:, :, None]).reshape(M, -1)[:, :K]
+        S = (amax / np.float32(448)).T
+    return torch.from_numpy(q).to(torch.float8_e4m3fn).float().numpy(), S
+
+
+@pytest.mark.parametrize("x_type", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M, K", [(1, 1), (1, 128), (3, 7), (5, 129), (16, 512), (17, 1000), (64, 2048),
+                                  (130, 640), (3001, 4100)])
+def test_quantize_rows_bits(M, K, x_type):
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = np.random.default_rng(M + K)
+    x = torch.from_numpy(rng.normal(0, 1, (M, K)) * np.exp(rng.normal(0, 3, (M, 1)))).to(dtype(x_type))
+    q, S = g.quantize_fp8(padded(x, 8, 1))
+    want, scale = quantize_ref(x.float().numpy())
+    assert q.shape == (M, K) and S.shape == (-(-K // 128), M)
+    assert np.array_equal(S.cpu().numpy(), scale)
+    # (rows of the largest factor overflow fp16: infinities, so NaN codes)
+    assert np.array_equal(q.float().cpu().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("x_type", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M, K", [(1, 1), (128, 128), (129, 100), (300, 1000), (1024, 512)])
+def test_quantize_blocks_bits(M, K, x_type):
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = np.random.default_rng(M + K)
+    x = torch.from_numpy(rng.normal(0, 1, (M, K))).to(dtype(x_type))
+    q, S = g.quantize_fp8(padded(x, 8, 1), block_rows=128)
+    assert S.shape == (-(-M // 128), -(-K // 128))
+    for i in range(S.shape[0]):
+        part = x[128 * i:128 * i + 128].float().numpy()
+        rows = part.shape[0]
+        for b in range(S.shape[1]):
+            block = part[:, 128 * b:128 * b + 128]
+            amax = np.maximum(np.abs(block).max(), np.float32(2.0 ** -100))
+            assert S[i, b].item() == amax / np.float32(448)
+            want = torch.from_numpy(block * (np.float32(448) / amax)).to(torch.float8_e4m3fn)
+            got = q[128 * i:128 * i + rows, 128 * b:128 * b + block.shape[1]]
+            assert np.array_equal(got.float().cpu().numpy(), want.float().numpy())
+
+
+def test_quantize_special_values():
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    x = torch.randn(8, 256)
+    x[0] = 0
+    x[1] = 1e-38
+    x[2, 3] = float("nan")
+    x[3, 200] = float("inf")
+    x[4, 128:] = 0
+    x[5] = 3.4e38
+    x[6, 0] = 2.0 ** -110
+    x[7] = torch.finfo(torch.float32).tiny / 4
+    q, S = g.quantize_fp8(x.cuda())
+    want, scale = quantize_ref(x.numpy())
+    assert np.array_equal(S.cpu().numpy(), scale)
+    assert np.array_equal(q.float().cpu().numpy(), want, equal_nan=True)
+    assert np.isnan(want[2]).sum() == 1 and np.isnan(want[3]).sum() == 1
+    assert (want[0] == 0).all() and np.isinf(scale[1, 3])
+
+
+@pytest.mark.parametrize("x_type", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M, K", [(1, 8), (5, 100), (64, 2048), (1025, 4096)])
+def test_quantize_swiglu(M, K, x_type):
+    """Each code times its scale is within half an e4m3 step of the 64-bit
+    value (a subnormal step, 2^-9 of the scale, at least).  fp32 adds: expf
+    and the divisions and products, under 8 steps of 2^-23 relative; the same
+    in the scale."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = np.random.default_rng(M + K)
+    x = torch.from_numpy(rng.normal(0, 2, (M, 2 * K))).to(dtype(x_type))
+    q, S = g.quantize_fp8(padded(x, 8, 1), act="swiglu")
+    v = x.double().numpy()
+    want = v[:, :K] / (1 + np.exp(-v[:, :K])) * v[:, K:]
+    scale = np.repeat(S.double().cpu().numpy().T, 128, 1)[:, :K]
+    got = q.double().cpu().numpy() * scale
+    slack = 8 * 2.0 ** -23
+    assert (np.abs(got - want) <= 2.0 ** -4 * np.abs(want) + 2.0 ** -10 * scale + slack * scale * 448).all()
+    for b in range(S.shape[0]):
+        amax = np.maximum(np.abs(want[:, 128 * b:128 * b + 128]).max(1), 2.0 ** -100)
+        assert (np.abs(S[b].double().cpu().numpy() - amax / 448) <= slack * amax / 448).all()
+
+
+def test_quantize_leaves_padding_alone():
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    x = torch.randn(20, 130, device="cuda")
+    wide = torch.randn(20, 136, device="cuda")
+    wide[:, :130] = x
+    q = torch.full((20, 160), 3, device="cuda", dtype=torch.uint8)
+    S = torch.full((3, 24), -1.0, device="cuda")
+    g.gemm_fp8_quantize(20, 130, wide, 136, g.GEMM_TYPE_F32, g.GEMM_ACT_NONE, 1, q, 160, S, 24)
+    want, scale = quantize_ref(x.cpu().numpy())
+    assert np.array_equal(q.view(torch.float8_e4m3fn).float().cpu().numpy()[:, :130], want)
+    assert bool((q[:, 130:] == 3).all())
+    assert np.array_equal(S.cpu().numpy()[:2, :20], scale)
+    assert bool((S[2] == -1).all()) and bool((S[:, 20:] == -1).all())
+
+
+@pytest.mark.parametrize("M, N, K", [(4, 512, 1024), (300, 640, 520)])
+def test_quantised_product_is_near_the_unquantised(M, N, K):
+    """quantize_fp8 of both operands into matmul_fp8, against the product of
+    the dequantised codes in 64 bits."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = torch.Generator().manual_seed(3)
+    x, w = torch.randn((M, K), generator=rng), torch.randn((N, K), generator=rng) / K ** 0.5
+    q, s = g.quantize_fp8(x.to(torch.bfloat16).cuda())
+    qw, sw = g.quantize_fp8(w.to(torch.bfloat16).cuda(), block_rows=128)
+    got = g.matmul_fp8(q, s, qw, sw, out_dtype=torch.float32).double().cpu().numpy()
+    want, err = block_product(q.float().cpu().numpy(), s.cpu().numpy(), qw.float().cpu().numpy(),
+                              sw.cpu().numpy())
+    check_rounded(got, want, err, "f32")
+    # a code is at most half an e4m3 step off: 2^-4 of each factor, to first order
+    mag = np.abs(x.bfloat16().double().numpy()) @ np.abs(w.bfloat16().double().numpy()).T
+    true = x.bfloat16().double().numpy() @ w.bfloat16().double().numpy().T
+    assert (np.abs(got - true) <= 0.15 * mag).all()
+
+
+def test_other_stream_and_graph():
+    """A captured product replayed on new inputs, eager work between."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((96, 1024), device="cuda", generator=gen).bfloat16()
+    w = torch.randn((768, 1024), device="cuda", generator=gen).bfloat16()
+    qw, sw = g.quantize_fp8(w, block_rows=128)
+
+    def layer():
+        q, s = g.quantize_fp8(x)
+        return g.matmul_fp8(q, s, qw, sw)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = layer()
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(other, layer())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer()
+    for i in range(4):
+        x.copy_(torch.randn((96, 1024), device="cuda", generator=gen).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, layer()), i
