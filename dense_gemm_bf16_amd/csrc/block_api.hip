@@ -201,9 +201,9 @@ int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_ty
   if (ldx < width || ldq < K) return GEMM_ERR_INVALID_ARG;
   if (lds < (block_rows == 1 ? M : (K + 127) / 128)) return GEMM_ERR_INVALID_ARG;
   if (M > 0 && K > 0 && (!X || !Q || !S)) return GEMM_ERR_INVALID_ARG;
-  if (gemm::misaligned(X, 16) || gemm::misaligned(Q, 16) || gemm::misaligned(S, 4))
+  if (gemm::misaligned(X, gemm::element_bytes(x_type)) || gemm::misaligned(Q, 16) ||
+      gemm::misaligned(S, 4) || (ldq & 15) != 0)
     return GEMM_ERR_MISALIGNED;
-  if ((ldx & 7) != 0 || (ldq & 15) != 0) return GEMM_ERR_MISALIGNED;
   if ((M + 15) / 16 > 65535 || (block_rows == 128 && (M + 127) / 128 > 65535))
     return GEMM_ERR_UNSUPPORTED;
   if (M == 0 || K == 0) return GEMM_OK;
@@ -262,8 +262,8 @@ int gemm_moe_combine(int64_t T, int64_t k, int64_t N, int64_t R, const void* Y, 
   if (T > 0 && N > 0) {
     if (!out || (k > 0 && (!pos || !weights || (R > 0 && !Y)))) return GEMM_ERR_INVALID_ARG;
   }
-  if (gemm::misaligned(Y, 16) || gemm::misaligned(out, 16) || gemm::misaligned(pos, 4) ||
-      gemm::misaligned(weights, 4) || ((ldy | ldo) & 7) != 0)
+  if (gemm::misaligned(Y, gemm::element_bytes(y_type)) || gemm::misaligned(out, 16) ||
+      gemm::misaligned(pos, 4) || gemm::misaligned(weights, 4) || (ldo & 7) != 0)
     return GEMM_ERR_MISALIGNED;
   if (T >= gemm::k2G || N >= gemm::k2G || R >= gemm::k2G || k >= gemm::k2G ||
       T * ((N + 7) / 8) >= gemm::k2G * 256 - 256)

@@ -123,30 +123,67 @@ __device__ __forceinline__ int source_row(const BlockArgs& a, int p) {
 
 // ------------------------------------------------------------------ MFMA
 
-// The partial sums of one K-step: D[n][m] = C + sum_k B[n][k] A[m][k] over
-// the two 16-byte chunks a lane holds of its row.  Which k a chunk stands
-// for does not matter as long as both operands agree.
-template <int OP>
-__device__ __forceinline__ f32x4 step_mfma(const u32x4 (&b)[2], const u32x4 (&a)[2], f32x4 c) {
-  if constexpr (OP == kOpE4m3) {
-    const i32x8 vb = {(int)b[0][0], (int)b[0][1], (int)b[0][2], (int)b[0][3],
-                      (int)b[1][0], (int)b[1][1], (int)b[1][2], (int)b[1][3]};
-    const i32x8 va = {(int)a[0][0], (int)a[0][1], (int)a[0][2], (int)a[0][3],
-                      (int)a[1][0], (int)a[1][1], (int)a[1][2], (int)a[1][3]};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, c, 0, 0, 0, 0, 0, 0);
-  } else {
+// What a lane holds of one fragment (16 rows of 128 bytes): two 16-byte
+// chunks of its row.  Which k a chunk stands for does not matter as long as
+// both operands agree.
+//
+// e4m3 has two forms.  The 8-bit MFMA aligns a step's products to the
+// largest and drops what falls below about 2^-17 of it (counted on MI355X:
+// sums of 128 products of normal values are 1.5e-5 off in norm, in all of
+// its shapes, and 4 chained 16x16x32 no better): a hundredth of a bf16
+// output's rounding and a tenth of an fp16 one's, so 16-bit outputs take it.
+// An fp32 output would show it, so there the codes are widened to bf16,
+// which holds every e4m3 value, and the bf16 MFMA keeps whole fp32 sums, at
+// half the rate.
+template <int OP, int OUT>
+struct Step {
+  static constexpr bool kWide = OP == kOpE4m3 && OUT == kStoreF32;
+  static constexpr int kRegs = kWide ? 4 : 2;  // 16-byte registers of a fragment
+  struct Frag {
+    u32x4 v[kRegs];
+  };
+  // A fragment from its two chunks.
+  static __device__ __forceinline__ Frag make(const u32x4& lo, const u32x4& hi) {
+    Frag f;
+    if constexpr (kWide) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      if constexpr (OP == kOpBf16)
-        c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b[h]),
-                                                    __builtin_bit_cast(bf16x8, a[h]), c, 0, 0, 0);
-      else
-        c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b[h]),
-                                                   __builtin_bit_cast(f16x8, a[h]), c, 0, 0, 0);
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t c = h ? hi[w] : lo[w];
+          f.v[2 * h + w / 2][w % 2 * 2] = __builtin_bit_cast(
+              uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, false));
+          f.v[2 * h + w / 2][w % 2 * 2 + 1] = __builtin_bit_cast(
+              uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c, 1.0f, true));
+        }
+    } else {
+      f.v[0] = lo;
+      f.v[1] = hi;
     }
-    return c;
+    return f;
   }
-}
+  // c + the step's sums: D[n][m] += sum_k B[n][k] A[m][k].
+  static __device__ __forceinline__ f32x4 mfma(const Frag& b, const Frag& a, f32x4 c) {
+    if constexpr (OP == kOpE4m3 && !kWide) {
+      const i32x8 vb = {(int)b.v[0][0], (int)b.v[0][1], (int)b.v[0][2], (int)b.v[0][3],
+                        (int)b.v[1][0], (int)b.v[1][1], (int)b.v[1][2], (int)b.v[1][3]};
+      const i32x8 va = {(int)a.v[0][0], (int)a.v[0][1], (int)a.v[0][2], (int)a.v[0][3],
+                        (int)a.v[1][0], (int)a.v[1][1], (int)a.v[1][2], (int)a.v[1][3]};
+      return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, c, 0, 0, 0, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int h = 0; h < kRegs; ++h) {
+        if constexpr (OP == kOpF16)
+          c = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b.v[h]),
+                                                     __builtin_bit_cast(f16x8, a.v[h]), c, 0, 0, 0);
+        else
+          c = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, b.v[h]),
+                                                      __builtin_bit_cast(bf16x8, a.v[h]), c, 0, 0, 0);
+      }
+      return c;
+    }
+  }
+};
 
 // One LDS-DMA load of 4 bytes per lane (see dma16).
 __device__ __forceinline__ void dma4(const u32x4& rsrc, uint32_t lds_addr, uint32_t voff,
@@ -309,9 +346,12 @@ block_tile_kernel(BlockArgs a) {
   const int at = lrow * kStepBytes + (((lane >> 4) ^ swz<3, 8>(lrow)) << 4);
   const lds_u8* const pa = smem + wm * Cfg::kWaveM * kStepBytes;
   const lds_u8* const pb = smem + Cfg::kABytes + wn * Cfg::kWaveN * kStepBytes;
-  auto read_frag = [&](const lds_u8* base, int f, u32x4 (&v)[2]) __attribute__((always_inline)) {
-    v[0] = *(const lds_u32x4*)(base + f * 16 * kStepBytes + at);
-    v[1] = *(const lds_u32x4*)(base + f * 16 * kStepBytes + (at ^ 64));
+  using St = Step<OP, OUT>;
+  using Frag = typename St::Frag;
+  auto read_frag = [&](const lds_u8* base, int f) __attribute__((always_inline)) {
+    const u32x4 lo = *(const lds_u32x4*)(base + f * 16 * kStepBytes + at);
+    const u32x4 hi = *(const lds_u32x4*)(base + f * 16 * kStepBytes + (at ^ 64));
+    return St::make(lo, hi);
   };
 
   for (int X = 0; X < a.k_steps; ++X) {
@@ -321,10 +361,10 @@ block_tile_kernel(BlockArgs a) {
     }
     ring_wait_barrier<0>();
     const uint32_t slot = (X & 1) * Cfg::kStageBytes;
-    u32x4 fb[FN][2], fa[2][2];
+    Frag fb[FN], fa[2];
 #pragma unroll
-    for (int j = 0; j < FN; ++j) read_frag(pb + slot, j, fb[j]);
-    read_frag(pa + slot, 0, fa[0]);
+    for (int j = 0; j < FN; ++j) fb[j] = read_frag(pb + slot, j);
+    fa[0] = read_frag(pa + slot, 0);
     float sb = 0.0f;
     if constexpr (kScaled)
       sb = sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + X];
@@ -335,14 +375,14 @@ block_tile_kernel(BlockArgs a) {
       if (i < FM) {
         if constexpr (kScaled)
           sc[i & 1] = sa_s[(X & 1) * BM + wm * Cfg::kWaveM + i * 16 + lrow] * sb;
-        if (i + 1 < FM) read_frag(pa + slot, i + 1, fa[(i + 1) & 1]);
+        if (i + 1 < FM) fa[(i + 1) & 1] = read_frag(pa + slot, i + 1);
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
           if constexpr (kScaled)
             part[i & 1][j] =
-                step_mfma<OP>(fb[j], fa[i & 1], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+                St::mfma(fb[j], fa[i & 1], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
           else
-            acc[i][j] = step_mfma<OP>(fb[j], fa[i & 1], acc[i][j]);
+            acc[i][j] = St::mfma(fb[j], fa[i & 1], acc[i][j]);
         }
 #pragma unroll
         for (int l = 0; l < L; ++l)
@@ -489,19 +529,25 @@ block_row_kernel(BlockArgs a) {
         trim(s.fb[j][1], keep - 64);
       }
     }
+    using St = Step<OP, OUT>;
+    typename St::Frag fb[FN];
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+    for (int j = 0; j < FN; ++j) fb[j] = St::make(s.fb[j][0], s.fb[j][1]);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const typename St::Frag fa = St::make(s.fa[i][0], s.fa[i][1]);
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
         if constexpr (kScaled) {
-          const f32x4 p = step_mfma<OP>(s.fb[j], s.fa[i], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+          const f32x4 p = St::mfma(fb[j], fa, (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
           const float sc = s.sa[i] * s.sb;
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(p[r], sc, acc[i][j][r]);
         } else {
-          acc[i][j] = step_mfma<OP>(s.fb[j], s.fa[i], acc[i][j]);
+          acc[i][j] = St::mfma(fb[j], fa, acc[i][j]);
         }
       }
+    }
   };
 #pragma unroll
   for (int u = 0; u < U; ++u)

@@ -28,24 +28,29 @@ __device__ __forceinline__ float to_float(const void* p, int64_t i) {
   else return (float)((const __bf16*)p)[i];
 }
 
-// Elements i .. i+7; `vec`: all of them exist and i is a multiple of 8 from
-// a 16-byte aligned base, else only the first `n` exist (the others read 0).
+// Elements i .. i+7, of which the first n exist (the others read 0), by
+// 16-byte loads where all do; rows may start at any element.
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef _Float16 f16x8u __attribute__((ext_vector_type(8), aligned(2)));
+typedef __bf16 bf16x8u __attribute__((ext_vector_type(8), aligned(2)));
+
 template <int TYPE>
-__device__ __forceinline__ void load8(const void* p, int64_t i, bool vec, int n, float (&v)[8]) {
-  if (vec) {
+__device__ __forceinline__ void load8(const void* p, int64_t i, int n, float (&v)[8]) {
+  if (n == 8) {
     if constexpr (TYPE == kStoreF32) {
-      const f32x4 a = *(const f32x4*)((const float*)p + i), b = *(const f32x4*)((const float*)p + i + 4);
+      const f32x4 a = *(const f32x4u*)((const float*)p + i);
+      const f32x4 b = *(const f32x4u*)((const float*)p + i + 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         v[j] = a[j];
         v[4 + j] = b[j];
       }
     } else if constexpr (TYPE == kStoreF16) {
-      const f16x8 a = *(const f16x8*)((const _Float16*)p + i);
+      const f16x8 a = *(const f16x8u*)((const _Float16*)p + i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = (float)a[j];
     } else {
-      const bf16x8 a = *(const bf16x8*)((const __bf16*)p + i);
+      const bf16x8 a = *(const bf16x8u*)((const __bf16*)p + i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = (float)a[j];
     }
@@ -85,16 +90,15 @@ __global__ __launch_bounds__(256) void quantize_rows_kernel(QuantArgs a) {
   const int64_t m0 = ((int64_t)blockIdx.y * 4 + wave) * RPW;
   const int64_t left = a.K - col;
   const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
-  const bool up_vec = n == 8 && (a.K & 7) == 0;  // the second half starts at column K
   float v[RPW][8];
 #pragma unroll
   for (int i = 0; i < RPW; ++i) {
     const bool in = m0 + i < a.M;
     const int64_t at = (m0 + i) * a.ldx + col;
-    load8<TYPE>(a.x, at, in && n == 8, in ? n : 0, v[i]);
+    load8<TYPE>(a.x, at, in ? n : 0, v[i]);
     if constexpr (SWIGLU) {
       float u[8];
-      load8<TYPE>(a.x, at + a.K, in && up_vec, in ? n : 0, u);
+      load8<TYPE>(a.x, at + a.K, in ? n : 0, u);  // the second half starts at column K
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = v[i][j] / (1.0f + expf(-v[i][j])) * u[j];
     }
@@ -127,7 +131,7 @@ __global__ __launch_bounds__(256) void quantize_blocks_kernel(QuantArgs a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const bool in = row + i * 16 < a.M;
-    load8<TYPE>(a.x, (row + i * 16) * a.ldx + col, in && n == 8, in ? n : 0, v[i]);
+    load8<TYPE>(a.x, (row + i * 16) * a.ldx + col, in ? n : 0, v[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[i][j]));
   }

@@ -354,8 +354,13 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
 }
 
 // out[t] = sum over slots j of w[t,j] Y[pos[t,j]], in fp32 in the order of
-// the slots.  Eight columns a thread; a slot whose pos lies outside Y
+// the slots.  Eight columns a thread, Y's rows
+// starting at any element; a slot whose pos lies outside Y
 // (dropped) adds nothing.
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+typedef _Float16 f16x8u __attribute__((ext_vector_type(8), aligned(2)));
+typedef __bf16 bf16x8u __attribute__((ext_vector_type(8), aligned(2)));
+
 template <int YT, int OT>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   const int64_t chunks = (a.N + 7) / 8;
@@ -372,14 +377,14 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     if (n + 8 <= a.N) {
       if constexpr (YT == kStoreF32) {
         const float* y = (const float*)a.Y + (int64_t)p * a.ldy + n;
-        const f32x4 lo = *(const f32x4*)y, hi = *(const f32x4*)(y + 4);
+        const f32x4 lo = *(const f32x4u*)y, hi = *(const f32x4u*)(y + 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           v[i] = lo[i];
           v[4 + i] = hi[i];
         }
       } else {
-        using V = std::conditional_t<YT == kStoreF16, f16x8, bf16x8>;
+        using V = std::conditional_t<YT == kStoreF16, f16x8u, bf16x8u>;
         const V y = *(const V*)((const uint16_t*)a.Y + (int64_t)p * a.ldy + n);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = (float)y[i];

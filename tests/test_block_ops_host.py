@@ -107,7 +107,7 @@ def quantize(g, M=8, K=256, X=P, ldx=512, x_type=BF16, act=0, block=1, Q=P, ldq=
     (dict(M=-1), 1), (dict(K=-1), 1), (dict(x_type=E4M3), 1), (dict(act=2), 1), (dict(block=64), 1),
     (dict(ldx=248), 1), (dict(ldx=504, act=1), 1), (dict(ldq=240), 1), (dict(lds=7), 1),
     (dict(block=128, lds=1), 1), (dict(X=NUL), 1), (dict(Q=NUL), 1), (dict(S=NUL), 1),
-    (dict(X=ODD), 2), (dict(Q=ODD), 2), (dict(ldx=516), 2), (dict(ldq=264), 2),
+    (dict(X=ctypes.c_void_p(0x10001)), 2), (dict(Q=ODD), 2), (dict(ldq=264), 2),
     (dict(block=128, act=1), 3), (dict(M=1 << 21, lds=1 << 21), 3)])
 def test_quantize_refusals(g, bad, code):
     assert quantize(g, **bad) == code
@@ -146,7 +146,7 @@ def combine(g, T=4, k=2, N=64, R=8, Y=P, ldy=64, y_type=BF16, pos=P, w=P, out=P,
 @pytest.mark.parametrize("bad, code", [
     (dict(T=-1), 1), (dict(k=-1), 1), (dict(N=-1), 1), (dict(R=-1), 1), (dict(ldy=56), 1),
     (dict(ldo=56), 1), (dict(y_type=E4M3), 1), (dict(out_type=E4M3), 1), (dict(Y=NUL), 1),
-    (dict(pos=NUL), 1), (dict(w=NUL), 1), (dict(out=NUL), 1), (dict(Y=ODD), 2), (dict(ldy=68), 2),
+    (dict(pos=NUL), 1), (dict(w=NUL), 1), (dict(out=NUL), 1), (dict(Y=ctypes.c_void_p(0x10001)), 2),
     (dict(out=ODD), 2), (dict(ldo=68), 2), (dict(T=1 << 31), 3)])
 def test_combine_refusals(g, bad, code):
     assert combine(g, **bad) == code

@@ -218,6 +218,28 @@ def test_quantize_blocks_bits(M, K, x_type):
             assert np.array_equal(got.float().cpu().numpy(), want.float().numpy())
 
 
+@pytest.mark.parametrize("x_type", ["bf16", "f16", "f32"])
+def test_quantize_rows_from_any_element(x_type):
+    """Odd strides, odd starts, and an odd second half."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = np.random.default_rng(9)
+    wide = torch.from_numpy(rng.normal(0, 1, (37, 603))).to(dtype(x_type))
+    x = wide.cuda()[:, 3:]
+    for rows in (1, 128):
+        q, S = g.quantize_fp8(x[:, :333], block_rows=rows)
+        r, s = g.quantize_fp8(x[:, :333].contiguous(), block_rows=rows)
+        assert torch.equal(S, s) and torch.equal(q.view(torch.uint8), r.view(torch.uint8))
+    want, scale = quantize_ref(wide[:, 3:].float().numpy())
+    q, S = g.quantize_fp8(x)
+    assert np.array_equal(q.float().cpu().numpy(), want) and np.array_equal(S.cpu().numpy(), scale)
+    a = g.quantize_fp8(x[:, :598], act="swiglu")  # 299 columns each
+    b = g.quantize_fp8(torch.cat([x[:, :299], x[:, :5], x[:, 299:598], x[:, :5]], 1), act="swiglu")
+    assert torch.equal(a[0][:, :256].float(), b[0][:, :256].float()) and torch.equal(a[1][:2], b[1][:2])
+
+
 def test_quantize_special_values():
     import torch
 

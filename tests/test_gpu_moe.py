@@ -331,6 +331,19 @@ def test_combine(T, k, N, y_type, out):
     check_rounded(got, want, ref.U * (k + 1) * mag, out)
 
 
+@pytest.mark.parametrize("y_type", ["bf16", "f16", "f32"])
+def test_combine_rows_from_any_element(y_type):
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    y = torch.randn(40, 203, device="cuda").to(dtype(y_type))[:, 3:]
+    pos = torch.randperm(40, device="cuda").to(torch.int32).view(10, 4)
+    w = torch.rand(10, 4, device="cuda")
+    for n in (199, 64, 8, 1):
+        assert torch.equal(g.moe_combine(y[:, :n], pos, w), g.moe_combine(y[:, :n].contiguous(), pos, w))
+
+
 def test_combine_skips_what_was_dropped():
     """A dropped slot does not touch the sum, not even as 0 * NaN."""
     import torch
