@@ -12,7 +12,7 @@ namespace gemm {
 
 const BlockConfig* block_configs() {
   static const BlockConfig table[] = {
-#define ROW(NAME, A, B, C, D) {#NAME, A, B, true, &launch_block_tile<A, B, C, D>},
+#define ROW(NAME, A, B, C, D, E, S) {#NAME, A, B, true, &launch_block_tile<A, B, C, D, E, S>},
       BLOCK_TILES(ROW)
 #undef ROW
 #define ROW(NAME, A, B, C, D) {#NAME, 16 * A, 16 * B, false, &launch_block_row<A, B, C, D>},
@@ -107,6 +107,7 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   const int64_t row_tiles = row_tile_bound(R, E, experts, c->bm);
   if (row_tiles * tiles_n >= k2G) return GEMM_ERR_UNSUPPORTED;
 
+  const int64_t row_tiles_per_b = experts ? 1 : row_tiles;
   BlockArgs a{};
   a.A = (const uint8_t*)A;
   a.B = (const uint8_t*)B;
@@ -131,6 +132,7 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   a.k_steps = (int32_t)((K * es + kStepBytes - 1) / kStepBytes);
   a.row_tiles = (int32_t)row_tiles;
   a.group_m = 4;
+  a.k_rot = row_tiles_per_b <= 1 ? 1 : 0;
   const hipError_t e =
       c->launch(a, (int)(row_tiles * tiles_n), (hipStream_t)stream, op_of(type), store_of(c_type));
   return e == hipSuccess ? GEMM_OK : hip_fail(e);

@@ -25,7 +25,7 @@ namespace gemm {
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStepBytes = 128;     // bytes of a row in one K-step
-constexpr int kMaxKSteps = 2048;    // K-steps whose B scales fit in LDS
+constexpr int kMaxKSteps = 1024;    // K-steps whose B scales are held in LDS
 constexpr int kScaleBlock = 128;    // rows of B (and columns of C) of one scale
 
 // Operand types.
@@ -53,6 +53,7 @@ struct BlockArgs {
   int32_t k_steps;
   int32_t row_tiles;  // dense: row tiles; experts: an upper bound on them
   int32_t group_m;    // raster group height in tiles
+  int32_t k_rot;      // K-step at which tile column j starts: j * k_rot, wrapped around
 };
 
 // ------------------------------------------------------------- row tiles
@@ -198,38 +199,47 @@ __device__ __forceinline__ void dma4(const u32x4& rsrc, uint32_t lds_addr, uint3
 
 // ----------------------------------------------------------- tile kernel
 
-// BM x BN tiles, WM x WN waves, two LDS slots of 128-byte rows swizzled as in
-// the direct-to-LDS kernel.  Per K-step: wait for the step's loads, barrier
-// (which also frees the other slot), then the wave's MFMAs with the next
-// step's loads spread between them.
-template <int BM, int BN, int WM, int WN, int OP, int OUT>
-__global__ __attribute__((amdgpu_flat_work_group_size(WM * WN * 64, WM * WN * 64),
-                          amdgpu_waves_per_eu(2, 2))) void
+// BM x BN tiles, WM x WN waves, a ring of S LDS slots of 128-byte rows
+// swizzled as in the direct-to-LDS kernel.  Per K-step X: wait until its
+// loads have landed (those of the S - 2 steps after it may be in flight),
+// barrier (which also frees the slot of step X - 1), then the wave's MFMAs
+// with the loads of step X + S - 1 spread between them.  Every step issues
+// the same loads, those past K reading zeros, so the waits count them.
+template <int BM, int BN, int WM, int WN, int WK, int S, int OP, int OUT>
+__global__ __attribute__((amdgpu_flat_work_group_size(WM * WN * WK * 64, WM * WN * WK * 64),
+                          amdgpu_waves_per_eu(2))) void
 block_tile_kernel(BlockArgs a) {
-  using Cfg = TileCfg<BM, BN, 64, WM, WN, 2, 3, 16>;
-  constexpr int T = Cfg::kThreads, W = WM * WN;
+  using Cfg = TileCfg<BM, BN, 64, WM, WN, S, 3, 16>;
+  constexpr int T = Cfg::kThreads, W = WM * WN;  // threads and waves of one K group
   constexpr int FM = Cfg::kFragM, FN = Cfg::kFragN;
   constexpr int LA = Cfg::kLoadsA, LB = Cfg::kLoadsB, L = LA + LB;
   constexpr int RPI = T / 8;  // rows of one load of all threads
   constexpr bool kScaled = OP == kOpE4m3;
+  using St = Step<OP, OUT>;
+  // A widened fragment takes twice the registers, too many for this form,
+  // and a load of all threads has to be half a wave row of A
+  constexpr bool kPipe = S == 2 && (FM == 4 || FM == 8) && RPI * 2 == Cfg::kWaveM && !St::kWide;
   constexpr int NB = (BN + kScaleBlock - 1) / kScaleBlock;  // scale blocks across a tile
+  constexpr int SA = BM < 64 ? 64 : BM;                     // row scales of a slot
+  constexpr int SS = kPipe ? 3 : S;                         // slots of row scales
+  constexpr int kInFlight = (S - 2) * (L + (kScaled ? 1 : 0));
   static_assert(RPI % 16 == 0, "the swizzle repeats every 16 rows");
   static_assert(kScaleBlock % Cfg::kWaveN == 0, "a wave's columns share one scale");
-  static_assert(BM / 64 <= W, "one wave loads 64 row scales");
-  static_assert(L <= FM * FN, "loads fit between the MFMAs");
+  static_assert(SA / 64 <= W, "one wave loads 64 row scales");
+  static_assert(kInFlight < 64, "vmcnt range");
 
-  __shared__ __attribute__((aligned(1024))) uint8_t smem_raw[Cfg::kLdsBytes];
-  __shared__ float sa_lds[kScaled ? 2 * BM : 1];
+  __shared__ __attribute__((aligned(1024))) uint8_t smem_raw[WK * Cfg::kLdsBytes];
+  __shared__ float sa_lds[kScaled ? WK * SS * SA : 1];
   __shared__ float sb_lds[kScaled ? NB * kMaxKSteps : 1];
-  lds_u8* const smem = (lds_u8*)smem_raw;
-  const uint32_t smem_addr = (uint32_t)(uintptr_t)smem;
-  typedef const __attribute__((address_space(3))) float lds_f32;
-  lds_f32* const sa_s = (lds_f32*)sa_lds;
-  lds_f32* const sb_s = (lds_f32*)sb_lds;
-
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x % T;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int kg = WK > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
+  lds_u8* const smem = (lds_u8*)smem_raw + kg * Cfg::kLdsBytes;
+  const uint32_t smem_addr = (uint32_t)(uintptr_t)smem;
+  typedef const __attribute__((address_space(3))) float lds_f32;
+  lds_f32* const sa_s = (lds_f32*)sa_lds + kg * SS * SA;
+  lds_f32* const sb_s = (lds_f32*)sb_lds;
   const int wm = wave / WN, wn = wave % WN;
 
   // ---- which tile --------------------------------------------------------
@@ -243,7 +253,7 @@ block_tile_kernel(BlockArgs a) {
   const int gsz = min(row_tiles - first, a.group_m);
   const int in = logical - gid * span;
   const int rt = first + in % gsz;
-  const int n0 = (in / gsz) * BN;
+  const int tn = in / gsz, n0 = tn * BN;
   RowTile tile;
   if (a.offsets) {
     if (!find_row_tile(a, BM, rt, lane, tile)) return;
@@ -273,9 +283,12 @@ block_tile_kernel(BlockArgs a) {
       voff[i] = row < rows_b ? (uint32_t)(row * (int)a.ldb + chunk * 16) : kOOB;
     }
   }
-  uint32_t voff_s = kOOB;  // this lane's row scale (waves 0 .. BM / 64 - 1)
+  // this lane's row scale; waves past the tile's rows load the same ones
+  // again (to the same place), so that all waves issue as many loads
+  const int srow = wave % (SA / 64) * 64;
+  uint32_t voff_s = kOOB;
   if constexpr (kScaled) {
-    const int row = wave * 64 + lane;
+    const int row = srow + lane;
     if (row < rows_a) {
       const int src = gather ? source_row(a, m0 + row) : m0 + row;
       if (src >= 0) voff_s = (uint32_t)src * 4;
@@ -283,7 +296,7 @@ block_tile_kernel(BlockArgs a) {
     // the tile's B scales of every K-step, once
     const float* sb = a.SB + tile.expert * a.stride_sb;
     const int per = (a.k_steps + 63) / 64;
-    for (int c = wave; c < NB * per; c += W) {
+    for (int c = kg * W + wave; c < NB * per; c += W * WK) {
       const int nb = c / per, k = (c % per) * 64 + lane;
       const int row = n0 / kScaleBlock + nb;
       const u32x4 rs = make_rsrc(sb + (int64_t)row * a.ldsb,
@@ -293,40 +306,43 @@ block_tile_kernel(BlockArgs a) {
     }
   }
   const bool past_k = (a.k_steps - 1) * kStepBytes + chunk * 16 >= a.kbytes;  // in the last step
-  auto load_one = [&](int X, int i) __attribute__((always_inline)) {
-    const uint32_t dst = smem_addr + (X & 1) * Cfg::kStageBytes + (i < LA ? 0 : Cfg::kABytes) +
-                         (((i < LA ? i : i - LA) * T + wave * 64) * 16);
-    // past K, and in the step past the last one, a load reads zeros: no
-    // branch splits the loop body
-    const uint32_t v = X >= a.k_steps - (past_k ? 1 : 0) ? kOOB : voff[i];
-    dma16(i < LA ? rsrc_a : rsrc_b, dst, v, (uint32_t)(X * kStepBytes));
+  // This group's X-th step of K: X * WK + kg, from the tile's starting point
+  // on (k_steps or more: past the last one).
+  const int rot = a.k_steps > 0 ? __builtin_amdgcn_readfirstlane(tn * a.k_rot % a.k_steps) : 0;
+  auto step_of = [&](int X) __attribute__((always_inline)) {
+    const int k = X * WK + kg;
+    const int r = k + rot >= a.k_steps ? k + rot - a.k_steps : k + rot;
+    return k < a.k_steps ? r : k;
   };
-  auto load_scales = [&](int X) __attribute__((always_inline)) {
+  // load i of K-step k into ring slot `slot`
+  auto load_one = [&](int k, int slot, int i) __attribute__((always_inline)) {
+    const uint32_t dst = smem_addr + slot * Cfg::kStageBytes + (i < LA ? 0 : Cfg::kABytes) +
+                         (((i < LA ? i : i - LA) * T + wave * 64) * 16);
+    // past K, and in the steps past the last one, a load reads zeros: no
+    // branch splits the loop body
+    const uint32_t v = k >= a.k_steps - (past_k ? 1 : 0) ? kOOB : voff[i];
+    dma16(i < LA ? rsrc_a : rsrc_b, dst, v, (uint32_t)(k * kStepBytes));
+  };
+  auto load_scales = [&](int k, int slot) __attribute__((always_inline)) {
     if constexpr (kScaled) {
-      if (wave < BM / 64) {
-        const u32x4 rs =
-            make_rsrc(a.SA + X * a.ldsa, X < a.k_steps ? (uint32_t)a.a_rows * 4 : 0u);
-        dma4(rs, (uint32_t)(uintptr_t)sa_s + ((X & 1) * BM + wave * 64) * 4, voff_s, 0u);
-      }
+      const u32x4 rs = make_rsrc(a.SA + k * a.ldsa, k < a.k_steps ? (uint32_t)a.a_rows * 4 : 0u);
+      dma4(rs, (uint32_t)(uintptr_t)sa_s + (slot * SA + srow) * 4, voff_s, 0u);
     }
   };
   // Zero the bytes past K of the 16-byte chunk that straddles it, each
   // thread in the chunks it loaded (their loads have landed).
-  auto trim = [&](int X) __attribute__((always_inline)) {
-    const int keep = a.kbytes - (X * kStepBytes + chunk * 16);
+  auto trim_one = [&](int k, int slot, int i) __attribute__((always_inline)) {
+    const int keep = a.kbytes - (k * kStepBytes + chunk * 16);
     if (keep > 0 && keep < 16) {
+      lds_u32x4* p = (lds_u32x4*)(smem + slot * Cfg::kStageBytes + (i < LA ? 0 : Cfg::kABytes) +
+                                  ((i < LA ? i : i - LA) * T + tid) * 16);
+      u32x4 v = *p;
 #pragma unroll
-      for (int i = 0; i < L; ++i) {
-        lds_u32x4* p = (lds_u32x4*)(smem + (X & 1) * Cfg::kStageBytes + (i < LA ? 0 : Cfg::kABytes) +
-                                    ((i < LA ? i : i - LA) * T + tid) * 16);
-        u32x4 v = *p;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const int left = keep - 4 * w;
-          v[w] &= left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
-        }
-        *p = v;
+      for (int w = 0; w < 4; ++w) {
+        const int left = keep - 4 * w;
+        v[w] &= left >= 4 ? ~0u : left <= 0 ? 0u : (1u << (8 * left)) - 1;
       }
+      *p = v;
     }
   };
 
@@ -336,9 +352,14 @@ block_tile_kernel(BlockArgs a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) acc[i][j] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
 
+  if constexpr (!kPipe) {
 #pragma unroll
-  for (int i = 0; i < L; ++i) load_one(0, i);
-  load_scales(0);
+    for (int p = 0; p < S - 1; ++p) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) load_one(step_of(p), p, i);
+      load_scales(step_of(p), p);
+    }
+  }
 
   // byte address of this lane's first chunk of its row in fragment 0; the
   // second chunk is 64 bytes away before the swizzle, so 64 by XOR after it
@@ -346,7 +367,6 @@ block_tile_kernel(BlockArgs a) {
   const int at = lrow * kStepBytes + (((lane >> 4) ^ swz<3, 8>(lrow)) << 4);
   const lds_u8* const pa = smem + wm * Cfg::kWaveM * kStepBytes;
   const lds_u8* const pb = smem + Cfg::kABytes + wn * Cfg::kWaveN * kStepBytes;
-  using St = Step<OP, OUT>;
   using Frag = typename St::Frag;
   auto read_frag = [&](const lds_u8* base, int f) __attribute__((always_inline)) {
     const u32x4 lo = *(const lds_u32x4*)(base + f * 16 * kStepBytes + at);
@@ -354,63 +374,246 @@ block_tile_kernel(BlockArgs a) {
     return St::make(lo, hi);
   };
 
-  for (int X = 0; X < a.k_steps; ++X) {
-    if (X == a.k_steps - 1 && (a.kbytes & 15) != 0) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      trim(X);
-    }
-    ring_wait_barrier<0>();
-    const uint32_t slot = (X & 1) * Cfg::kStageBytes;
-    Frag fb[FN], fa[2];
+  const int rounds = (a.k_steps + WK - 1) / WK;
+  if constexpr (kPipe) {
+    // Two slots, each refilled in two parts as soon as a part is read, so
+    // that about a whole step's loads are always in flight (with one barrier
+    // a step the loads had to land within the step that issued them: 1.4 us
+    // a step of 64 KB without any MFMA, against 0.9 us).  Part 1 is B and
+    // the A rows of each wave row's first half, part 2 its other half.  Two
+    // barriers a step:
+    //   P1(X), before the last two rows of step X - 1: part 1 of step X has
+    //     landed; step X - 1's last fragments are in registers, so part 2 of
+    //     step X + 1 is issued in its place;
+    //   P2(X), half way through step X: part 2 of step X has landed; B and
+    //     the first half of A are in registers, so part 1 of step X + 2 is
+    //     issued in their place.
+    // Either way two parts are in flight past the one that is awaited.  The
+    // MFMAs of the last two rows cover P1 and the first reads of the next
+    // step, whose B fragments replace the old ones one by one as their last
+    // MFMAs issue.  MFMA q (row by row, in the last two rows column by
+    // column) writes partial sum q % 4, which is added to its accumulator
+    // once MFMA q + 3 has issued.
+    constexpr int NQ = FM * FN, Q0 = (FM - 2) * FN;  // MFMAs of a step, and of its rows before P1
+    constexpr int QP = (FM == 8 ? 3 : 1) * FN;       // the MFMA before which P2 is
+    constexpr int kParts = L + (kScaled ? 1 : 0);    // loads of both parts
+    static_assert(FM == 4 || FM == 8, "the tables below");
+    // Buffer of row i's A fragment, and the row at whose first MFMA it is
+    // read (rows 0 and 1: in the last two rows of the step before; the second
+    // half's not before P2): rows FM - 2, FM - 1 and the next step's 0 are
+    // held at once.  Eight rows make
+    // do with three buffers, each reused once its row's MFMAs have issued.
+    // (Row 2 not before row 1: until then the last additions of the step
+    // before use the scale that its own replaces.)
+    constexpr int NBUF = FM == 8 ? 3 : 4;
+    auto buf_of = [](int i) constexpr {
+      constexpr int b[8] = {2, 0, 1, 0, 1, 2, 0, 1};
+      return FM == 8 ? b[i] : i;
+    };
+    auto read_at = [](int i) constexpr {
+      constexpr int at8[8] = {-1, -1, 1, 2, 3, 4, 4, 5}, at4[4] = {-1, -1, 1, 1};
+      return FM == 8 ? at8[i] : at4[i % 4];
+    };
+    typedef std::integral_constant<int, 0> Zero;
+    auto row_of = [](int q) constexpr { return q < Q0 ? q / FN : FM - 2 + (q - Q0) % 2; };
+    auto col_of = [](int q) constexpr { return q < Q0 ? q % FN : (q - Q0) / 2; };
+    // the loads of a part: in the second, A's odd ones
+    auto second = [](int l) constexpr { return l < LA && l % 2 == 1; };
+    auto load_part = [&](int k, int slot, int sslot, bool two) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[j] = read_frag(pb + slot, j);
-    fa[0] = read_frag(pa + slot, 0);
-    float sb = 0.0f;
-    if constexpr (kScaled)
-      sb = sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + X];
-    f32x4 part[2][FN];
-    float sc[2];
-#pragma unroll
-    for (int i = 0; i < FM + 1; ++i) {
-      if (i < FM) {
-        if constexpr (kScaled)
-          sc[i & 1] = sa_s[(X & 1) * BM + wm * Cfg::kWaveM + i * 16 + lrow] * sb;
-        if (i + 1 < FM) fa[(i + 1) & 1] = read_frag(pa + slot, i + 1);
-#pragma unroll
-        for (int j = 0; j < FN; ++j) {
-          if constexpr (kScaled)
-            part[i & 1][j] =
-                St::mfma(fb[j], fa[i & 1], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
-          else
-            acc[i][j] = St::mfma(fb[j], fa[i & 1], acc[i][j]);
-        }
+      for (int l = 0; l < L; ++l)
+        if (second(l) == two) load_one(k, slot, l);
+      if (!two) load_scales(k, sslot);
+    };
+    // wait for the oldest part in flight, and the barrier
+    auto publish = [&](int k, int slot, bool two) __attribute__((always_inline)) {
+      if (k == a.k_steps - 1 && (a.kbytes & 15) != 0) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
         for (int l = 0; l < L; ++l)
-          if (l * FM / L == i) load_one(X + 1, l);
-        if (i == 0) load_scales(X + 1);
+          if (second(l) == two) trim_one(k, slot, l);
       }
-      if constexpr (kScaled) {
-        if (i > 0) {
+      ring_wait_barrier<kParts>();
+    };
+    load_part(step_of(0), 0, 0, false);
+    load_part(step_of(0), 0, 0, true);
+    load_part(step_of(1), 1, 1, false);
+    publish(step_of(0), 0, false);
+    load_part(step_of(1), 1, 1, true);
+    Frag fb[FN], fa[NBUF];
+    f32x4 part[4];
 #pragma unroll
-          for (int j = 0; j < FN; ++j)
+    for (int p = 0; p < 4; ++p) part[p] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
+    float sc[4] = {};
+    float sb = 0.0f;
+    auto scale_b = [&](int k) __attribute__((always_inline)) {
+      if constexpr (kScaled)
+        sb = sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + (k < a.k_steps ? k : 0)];
+    };
+    auto read_row = [&](int slot, int sslot, auto ic) __attribute__((always_inline)) {
+      constexpr int i = decltype(ic)::value;
+      fa[buf_of(i)] = read_frag(pa + slot * Cfg::kStageBytes, i);
+      if constexpr (kScaled) sc[i % 4] = sa_s[sslot * SA + wm * Cfg::kWaveM + i * 16 + lrow] * sb;
+    };
+    scale_b(step_of(0));
+    read_row(0, 0, Zero{});
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[i - 1][j][r] =
-                  __builtin_fmaf(part[(i - 1) & 1][j][r], sc[(i - 1) & 1], acc[i - 1][j][r]);
+    for (int j = 0; j < FN; ++j) fb[j] = read_frag(pb, j);
+    read_row(0, 0, std::integral_constant<int, 1>{});
+    int ss = 0;  // X % 3: the slot of step X's row scales, read to the step's end
+    for (int X = 0; X < rounds; ++X) {
+      const int slot = X & 1, next = slot ^ 1;
+      const int ss1 = ss == 2 ? 0 : ss + 1, ss2 = ss == 0 ? 2 : ss - 1;
+      const int k_now = step_of(X);
+      const int k_next = step_of(X + 1);
+      const int k_two = step_of(X + 2);
+      constexpr_for<NQ>([&](auto qc) __attribute__((always_inline)) {
+        constexpr int q = decltype(qc)::value;
+        constexpr int i = row_of(q), j = col_of(q);
+        if constexpr (q == QP) publish(k_now, slot, true);
+        if constexpr (q == Q0) {
+          publish(k_next, next, false);
+          scale_b(k_next);
         }
+        if constexpr (kScaled)
+          part[q % 4] = St::mfma(fb[j], fa[buf_of(i)], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+        else
+          acc[i][j] = St::mfma(fb[j], fa[buf_of(i)], acc[i][j]);
+        if constexpr (q < Q0 && j == 0)
+          constexpr_for<FM>([&](auto rc) __attribute__((always_inline)) {
+            if constexpr (read_at(decltype(rc)::value) == i) read_row(slot, ss, rc);
+          });
+        // loads: part 1 of step X + 2 from P2 to P1, part 2 after P1
+        constexpr int L1 = L - LA / 2, L2 = LA / 2;
+        constexpr_for<L>([&](auto lc) __attribute__((always_inline)) {
+          constexpr int l = decltype(lc)::value;
+          constexpr int nth = l < LA ? l / 2 : l - LA / 2;  // place in its part
+          if constexpr (second(l)) {
+            if constexpr (q == Q0 + nth * (NQ - Q0) / L2) load_one(k_two, slot, l);
+          } else {
+            if constexpr (q == QP + nth * (Q0 - QP) / L1) load_one(k_two, slot, l);
+          }
+        });
+        if constexpr (q == Q0 - 1) load_scales(k_two, ss2);
+        if constexpr (q >= Q0) {
+          // the next step's first rows and B fragments
+          if constexpr (q == Q0) read_row(next, ss1, Zero{});
+          if constexpr ((q - Q0) % 2 == 1) fb[j] = read_frag(pb + next * Cfg::kStageBytes, j);
+          if constexpr (q == NQ - 1) read_row(next, ss1, std::integral_constant<int, 1>{});
+        }
+        if constexpr (kScaled) {
+          constexpr int d = q < 3 ? q - 3 + NQ : q - 3;  // MFMA whose sums are added now
+          constexpr int di = row_of(d), dj = col_of(d);
+          // (before the first step there is nothing to add: part is zero)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            acc[di][dj][r] = __builtin_fmaf(part[d % 4][r], sc[di % 4], acc[di][dj][r]);
+          // (keeps the additions here: left free, they gather at the step's
+          // end, where their partial sums do not fit the registers)
+          asm volatile("" : "+v"(acc[di][dj]));
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      });
+      ss = ss1;
+    }
+    if constexpr (kScaled) {
+      constexpr_for<3>([&](auto dc) __attribute__((always_inline)) {
+        constexpr int d = NQ - 3 + decltype(dc)::value;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          acc[row_of(d)][col_of(d)][r] =
+              __builtin_fmaf(part[d % 4][r], sc[row_of(d) % 4], acc[row_of(d)][col_of(d)][r]);
+      });
+    }
+  } else {
+    int at_slot = 0, to_slot = S - 1;  // ring slots of steps X and X + S - 1
+    for (int X = 0; X < rounds; ++X) {
+      const int k = step_of(X), k_ahead = step_of(X + S - 1);
+      if (k == a.k_steps - 1 && (a.kbytes & 15) != 0) {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+  #pragma unroll
+        for (int i = 0; i < L; ++i) trim_one(k, at_slot, i);
       }
-      // (without it the scheduler reads every fragment first, and spills)
-      __builtin_amdgcn_sched_barrier(0);
+      ring_wait_barrier<kInFlight>();
+      const uint32_t slot = at_slot * Cfg::kStageBytes;
+      Frag fb[FN], fa[2];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) fb[j] = read_frag(pb + slot, j);
+      fa[0] = read_frag(pa + slot, 0);
+      float sb = 0.0f;
+      if constexpr (kScaled)
+        sb = sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + (k < a.k_steps ? k : 0)];
+      f32x4 part[2][FN];
+      float sc[2];
+#pragma unroll
+      for (int i = 0; i < FM + 1; ++i) {
+        if (i < FM) {
+          if constexpr (kScaled)
+            sc[i & 1] = sa_s[at_slot * SA + wm * Cfg::kWaveM + i * 16 + lrow] * sb;
+          if (i + 1 < FM) fa[(i + 1) & 1] = read_frag(pa + slot, i + 1);
+#pragma unroll
+          for (int j = 0; j < FN; ++j) {
+            if constexpr (kScaled)
+              part[i & 1][j] =
+                  St::mfma(fb[j], fa[i & 1], (f32x4){0.0f, 0.0f, 0.0f, 0.0f});
+            else
+              acc[i][j] = St::mfma(fb[j], fa[i & 1], acc[i][j]);
+          }
+#pragma unroll
+          for (int l = 0; l < L; ++l)
+            if (l * FM / L == i) load_one(k_ahead, to_slot, l);
+          if (i == 0) load_scales(k_ahead, to_slot);
+        }
+        if constexpr (kScaled) {
+          if (i > 0) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                acc[i - 1][j][r] =
+                    __builtin_fmaf(part[(i - 1) & 1][j][r], sc[(i - 1) & 1], acc[i - 1][j][r]);
+          }
+        }
+        // (without it the scheduler reads every fragment first, and spills)
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      at_slot = at_slot + 1 == S ? 0 : at_slot + 1;
+      to_slot = to_slot + 1 == S ? 0 : to_slot + 1;
     }
   }
 
-  KernelArgs k{};
-  k.C = a.C;
-  k.ldc = a.ldc;
-  k.M = tile.end;
-  k.N = a.N;
-  finish_tile<Cfg, OUT, false>(k, smem, wave, m0, n0, acc, m0 + wm * Cfg::kWaveM,
-                               n0 + wn * Cfg::kWaveN, lane, 0);
+  KernelArgs c{};
+  c.C = a.C;
+  c.ldc = a.ldc;
+  c.M = tile.end;
+  c.N = a.N;
+  if constexpr (WK > 1) {
+    // The groups' sums meet in LDS, added in the order of the groups by the
+    // first one, which stores C.
+    typedef __attribute__((address_space(3))) f32x4 lds_f32x4;
+    static_assert(T * FM * FN * 16 <= Cfg::kLdsBytes, "a group's sums fit its ring");
+    lds_f32x4* const mine = (lds_f32x4*)smem + (wave * FM * FN) * 64 + lane;
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kg > 0) {
+#pragma unroll
+      for (int i = 0; i < FM * FN; ++i) mine[i * 64] = acc[i / FN][i % FN];
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 1; g < WK; ++g)
+#pragma unroll
+      for (int i = 0; i < FM * FN; ++i)
+        acc[i / FN][i % FN] += mine[g * (Cfg::kLdsBytes / 16) + i * 64];
+    // (each wave stages C in its own part of the first group's ring: no
+    // barrier, which the other groups' waves would not reach)
+    finish_tile<Cfg, OUT, false, Cfg::kLdsBytes, false>(c, smem, wave, m0, n0, acc,
+                                                        m0 + wm * Cfg::kWaveM,
+                                                        n0 + wn * Cfg::kWaveN, lane, 0);
+  } else {
+    finish_tile<Cfg, OUT, false>(c, smem, wave, m0, n0, acc, m0 + wm * Cfg::kWaveM,
+                                 n0 + wn * Cfg::kWaveN, lane, 0);
+  }
 }
 
 // ------------------------------------------------------------ row kernel
@@ -468,6 +671,11 @@ block_row_kernel(BlockArgs a) {
   }
   const float* sb_row = a.SB + tile.expert * a.stride_sb + (int64_t)(n0 / kScaleBlock) * a.ldsb;
 
+  const int rot =
+      a.k_steps > 0 ? __builtin_amdgcn_readfirstlane((n0 / BN) * a.k_rot % a.k_steps) : 0;
+  auto step_of = [&](int X) __attribute__((always_inline)) {
+    return X + rot >= a.k_steps ? X + rot - a.k_steps : X + rot;
+  };
   struct Stage {
     u32x4 fa[FM][2], fb[FN][2];
     float sa[FM], sb;
@@ -551,14 +759,14 @@ block_row_kernel(BlockArgs a) {
   };
 #pragma unroll
   for (int u = 0; u < U; ++u)
-    if (wave + u * W < a.k_steps) load(st[u], wave + u * W);
+    if (wave + u * W < a.k_steps) load(st[u], step_of(wave + u * W));
   for (int X = wave; X < a.k_steps; X += U * W) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int Y = X + u * W;
       if (Y < a.k_steps) {
-        multiply(st[u], Y);
-        if (Y + U * W < a.k_steps) load(st[u], Y + U * W);
+        multiply(st[u], step_of(Y));
+        if (Y + U * W < a.k_steps) load(st[u], step_of(Y + U * W));
       }
     }
   }

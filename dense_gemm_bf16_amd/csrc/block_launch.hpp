@@ -22,11 +22,11 @@ hipError_t by_types(int op, int out, Launch&& launch) {
   }
 }
 
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int WK, int S>
 hipError_t launch_block_tile(const BlockArgs& a, int grid, hipStream_t s, int op, int out) {
   return by_types(op, out, [&](auto o, auto t) {
-    hipLaunchKernelGGL((block_tile_kernel<BM, BN, WM, WN, decltype(o)::value, decltype(t)::value>),
-                       dim3(grid), dim3(WM * WN * 64), 0, s, a);
+    hipLaunchKernelGGL((block_tile_kernel<BM, BN, WM, WN, WK, S, decltype(o)::value, decltype(t)::value>),
+                       dim3(grid), dim3(WM * WN * WK * 64), 0, s, a);
     return hipGetLastError();
   });
 }
@@ -41,17 +41,17 @@ hipError_t launch_block_row(const BlockArgs& a, int grid, hipStream_t s, int op,
 }
 
 // Built shapes: X(name, launcher template arguments).
-#define BLOCK_TILES(X)        \
-  X(b256x256, 256, 256, 2, 4) \
-  X(b128x128, 128, 128, 2, 2)
+#define BLOCK_TILES(X)              \
+  X(b256x256, 256, 256, 2, 4, 1, 2) \
+  X(b128x128, 128, 128, 2, 2, 1, 2)
 #define BLOCK_ROWS(X)    \
   X(r16x16, 1, 1, 4, 4)  \
   X(r32x32, 2, 2, 4, 2)  \
   X(r64x32, 4, 2, 4, 2)
 
-#define BLOCK_DECLARE(NAME, A, B, C, D)                                                       \
-  extern template hipError_t launch_block_tile<A, B, C, D>(const BlockArgs&, int, hipStream_t, \
-                                                           int, int);
+#define BLOCK_DECLARE(NAME, A, B, C, D, E, S)                                            \
+  extern template hipError_t launch_block_tile<A, B, C, D, E, S>(const BlockArgs&, int, \
+                                                                 hipStream_t, int, int);
 BLOCK_TILES(BLOCK_DECLARE)
 #undef BLOCK_DECLARE
 #define BLOCK_DECLARE(NAME, A, B, C, D)                                                      \

@@ -305,7 +305,10 @@ hipError_t route_of(const RouteArgs& a, hipStream_t s) {
 // (they stay in L2), first to count the ids below its own, which is where
 // its rows start, then to place its own in their order.  One launch, no
 // atomics, so the order never depends on timing.  Each wave takes a
-// contiguous part of the ids, so the waves meet once.
+// contiguous part of the ids, 256 at a time (four neighbours a lane), so the
+// waves meet once.
+typedef int i32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
 template <int W>
 __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict__ ids, int R, int k,
                                                       int E, int32_t* __restrict__ offsets,
@@ -314,22 +317,37 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
   __shared__ int below_of[W], own_of[W];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int e = blockIdx.x;
-  const int part = ((R + W - 1) / W + 63) / 64 * 64;
+  const uint32_t e = blockIdx.x;
+  const int part = ((R + W - 1) / W + 255) / 256 * 256;
   const int begin = min((int64_t)wave * part, (int64_t)R), end = min((int64_t)begin + part, (int64_t)R);
-  auto expert = [&](int i) __attribute__((always_inline)) {
-    if (i >= end) return E + 1;  // past the part
-    const int id = ids[i];
-    return id >= 0 && id < E ? id : E;
+  // this lane's four ids from i on: an id that names no expert (negative
+  // ones are large unsigned) counts as E, a place past the part as E + 1
+  auto four = [&](int i, uint32_t (&v)[4]) __attribute__((always_inline)) {
+    if (i + 4 <= end) {
+      const i32x4u q = *(const i32x4u*)(ids + i);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) v[u] = min((uint32_t)q[u], (uint32_t)E);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        v[u] = i + u < end ? min((uint32_t)ids[i + u], (uint32_t)E) : (uint32_t)E + 1;
+    }
   };
   int below = 0, own = 0;
+#pragma unroll 4
   for (int i = begin; i < end; i += 256) {
+    uint32_t v[4];
+    four(i + lane * 4, v);
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      const int id = expert(i + u * 64 + lane);
-      below += __popcll(__ballot(id < e));
-      own += __popcll(__ballot(id == e));
+      below += v[u] < e ? 1 : 0;
+      own += v[u] == e ? 1 : 0;
     }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    below += __shfl_xor(below, d, 64);
+    own += __shfl_xor(own, d, 64);
   }
   if (lane == 0) {
     below_of[wave] = below;
@@ -341,15 +359,26 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
   for (int w = 0; w < W; ++w) at += below_of[w] + (w < wave ? own_of[w] : 0);
   if (wave == 0 && lane == 0) offsets[e] = at;
   if (own == 0) return;
-  for (int i = begin; i < end; i += 64) {
-    const int id = expert(i + lane);
-    const uint64_t mine = __ballot(id == e);
-    if (id == e) {
-      const int p = at + __popcll(mine & ((1ull << lane) - 1));
-      rows[p] = e < E ? (i + lane) / k : -1;
-      pos[i + lane] = e < E ? p : -1;
+#pragma unroll 2
+  for (int i = begin; i < end; i += 256) {
+    uint32_t v[4];
+    four(i + lane * 4, v);
+    int p = at;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const uint64_t mine = __ballot(v[u] == e);
+      p += (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mine >> 32),
+                                          __builtin_amdgcn_mbcnt_lo((uint32_t)mine, 0u));
+      at += __popcll(mine);
     }
-    at += __popcll(mine);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (v[u] == e) {
+        const int slot = i + lane * 4 + u;
+        rows[p] = e < (uint32_t)E ? slot / k : -1;
+        pos[slot] = e < (uint32_t)E ? p : -1;
+        ++p;
+      }
   }
 }
 

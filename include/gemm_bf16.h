@@ -258,7 +258,7 @@ int gemm_bf16_ex_noalloc(const char* config,
  *   SB(j,b) = SB[j*ldsb + b], ldsb >= ceil(K / 128), ceil(N / 128) rows
  * A and B 16-byte aligned with lda and ldb multiples of 16; C 16-byte
  * aligned with ldc a multiple of 8; scales 4-byte aligned.  Any M, N, K >= 0
- * up to K = 262144 (GEMM_ERR_UNSUPPORTED past it); K == 0 sets C to zeros.
+ * up to K = 131072 (GEMM_ERR_UNSUPPORTED past it); K == 0 sets C to zeros.
  *
  * Numerics: the 128 products of a block are summed by the matrix core,
  * multiplied by the fp32 product of the two scales and added to an fp32 sum,
