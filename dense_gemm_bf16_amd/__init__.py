@@ -103,9 +103,9 @@ for _name, _args in {
     getattr(_lib, _name).restype = ctypes.c_int
     getattr(_lib, _name).argtypes = _args
 _lib.gemm_fp8_config_name.restype = ctypes.c_char_p
-_lib.gemm_fp8_config_name.argtypes = [_i64, _i64, _i64]
+_lib.gemm_fp8_config_name.argtypes = [_i64, _i64, _i64, _c_int]
 _lib.gemm_moe_config_name.restype = ctypes.c_char_p
-_lib.gemm_moe_config_name.argtypes = [_i64, _i64, _i64, _i64]
+_lib.gemm_moe_config_name.argtypes = [_c_int, _i64, _i64, _i64, _i64, _c_int]
 _lib.gemm_fp8_config_at.restype = ctypes.c_char_p
 _lib.gemm_fp8_config_at.argtypes = [ctypes.c_int]
 
@@ -359,14 +359,14 @@ def gemm_moe_combine(T, k, N, R, Y, ldy, y_type, pos, weights, out, ldo, out_typ
                                  _ptr(out), ldo, out_type, _stream(stream)))
 
 
-def fp8_config_name(M, N, K) -> str:
+def fp8_config_name(M, N, K, c_type=GEMM_TYPE_BF16) -> str:
     """The kernel shape gemm_fp8 chooses."""
-    return _lib.gemm_fp8_config_name(M, N, K).decode()
+    return _lib.gemm_fp8_config_name(M, N, K, c_type).decode()
 
 
-def moe_config_name(R, N, K, E) -> str:
+def moe_config_name(type, R, N, K, E, c_type=GEMM_TYPE_BF16) -> str:
     """The kernel shape gemm_moe chooses."""
-    return _lib.gemm_moe_config_name(R, N, K, E).decode()
+    return _lib.gemm_moe_config_name(type, R, N, K, E, c_type).decode()
 
 
 def fp8_config_names() -> list[str]:

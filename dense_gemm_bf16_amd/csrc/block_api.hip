@@ -42,16 +42,75 @@ int64_t row_tile_bound(int64_t R, int64_t E, bool experts, int64_t bm) {
   return used + (R - used) / bm;
 }
 
-// Shape by the rows that share one B (all of a dense product's, an expert's
-// on average).
-const BlockConfig* choose_block(int64_t R, int64_t N, int64_t E, bool experts) {
-  const int64_t used = R < E ? R : E;
-  const int64_t rows = used > 0 ? (R + used - 1) / used : 0;
-  if (rows <= 16) return block_config("r16x16");
-  if (rows <= 32) return block_config("r32x32");
-  if (rows <= 64) return block_config("r64x32");
-  const int64_t big = row_tile_bound(R, E, experts, 256) * ((N + 255) / 256);
-  return block_config(rows > 128 && big >= 256 ? "b256x256" : "b128x128");
+// ------------------------------------------------------- choice of shape
+// The shape that a model of a launch's time on MI355X makes cheapest, fitted
+// (least squares on log time) to 167 swept products timed in every shape
+// below (dense: M 1-4096, N x K from 600 x 1000 to 28672 x 1024; experts: 8
+// to 128 experts, 1 to 8192 tokens, e4m3 and bf16).  Its choice ran within
+// 0.9 % of the fastest shape timed (geometric mean; 18 % at worst), 1.8 %
+// for e4m3 with fp32 output.
+//
+// A launch of `units` workgroups on CUs that hold `resident` of them each
+// makes passes of 256 * resident; a pass costs steps * step + tile (steps:
+// K-steps of a workgroup's wave group; tile: first loads and epilogue), a
+// last pass with a fraction f of its workgroups part + (1 - part) * f of
+// that.  The whole takes at least as long as reading B at 5.2 TB/s (joined as
+// fourth powers, so near the floor the cheaper compute still counts).
+struct BlockCost {
+  const char* name;
+  int k_groups, resident;
+  struct Fit {
+    float step, tile, part, base;  // us, us, share, us
+  } fit, wide;                     // wide: e4m3 with fp32 output (codes widened to bf16)
+};
+constexpr float kNever = 1e9f;
+constexpr BlockCost kBlockCosts[] = {
+    {"b256x256", 1, 1, {1.586f, 6.15f, 0.69f, 2.19f}, {kNever, 0, 0, 0}},
+    {"b256x128", 1, 1, {0.932f, 4.29f, 0.76f, 1.51f}, {kNever, 0, 0, 0}},
+    {"b128x128", 1, 2, {1.032f, 3.95f, 0.55f, 2.44f}, {1.822f, 4.58f, 0.61f, 0.00f}},
+    {"b128x128k2", 2, 1, {1.172f, 5.23f, 0.83f, 1.37f}, {1.962f, 5.14f, 0.85f, 0.00f}},
+    {"b64x128k2", 2, 1, {0.873f, 3.68f, 0.75f, 1.39f}, {1.299f, 3.53f, 0.86f, 0.73f}},
+    {"b64x64", 1, 2, {0.492f, 3.41f, 0.67f, 1.06f}, {0.774f, 1.59f, 0.56f, 2.97f}},
+    {"b64x64k2", 2, 1, {0.528f, 3.97f, 0.84f, 0.44f}, {0.799f, 3.88f, 0.85f, 0.57f}},
+    {"b32x128", 1, 2, {0.645f, 3.14f, 0.62f, 0.83f}, {1.032f, 0.00f, 0.50f, 2.96f}},
+    {"b32x64k4", 4, 1, {0.678f, 4.52f, 0.88f, 0.00f}, {0.932f, 4.82f, 0.90f, 0.00f}},
+    {"b32x32k4", 4, 1, {0.508f, 3.15f, 0.96f, 1.30f}, {0.663f, 3.46f, 0.92f, 1.12f}},
+    {"r16x16", 8, 4, {2.435f, 1.11f, 0.24f, 3.08f}, {2.435f, 1.11f, 0.24f, 3.08f}}};
+constexpr double kStreamMBPerUs = 5.2, kStreamBaseUs = 2.5;
+
+const BlockConfig* choose_block(int type, int64_t R, int64_t N, int64_t K, int64_t E, bool experts,
+                                int c_type) {
+  const bool wide = type == GEMM_TYPE_E4M3 && c_type == GEMM_TYPE_F32;
+  const double used = (double)(R < E ? R : E);  // experts that may have rows
+  const double k_bytes = (double)K * (type == GEMM_TYPE_E4M3 ? 1 : 2);
+  const double floor_us = used * N * k_bytes * 1e-6 / kStreamMBPerUs + kStreamBaseUs;
+  const BlockCost* best = nullptr;
+  double best_t = 0;
+  for (const BlockCost& c : kBlockCosts) {
+    const BlockConfig* shape = block_config(c.name);
+    const BlockCost::Fit& f = wide ? c.wide : c.fit;
+    // How the rows fall to the experts is known on the device only: each
+    // expert with rows is taken to add half a tile to the full ones.
+    double rows = (double)((R + shape->bm - 1) / shape->bm);
+    if (experts) {
+      rows = (double)R / shape->bm + 0.5 * used;
+      if (rows < used) rows = used;
+    }
+    const double units = rows * (double)((N + shape->bn - 1) / shape->bn);
+    const double pass = 256.0 * c.resident;
+    double passes = (double)(int64_t)(units / pass);
+    const double rest = units / pass - passes;
+    if (rest > 0) passes += f.part + (1 - f.part) * rest;
+    const double k_steps = (double)(int64_t)((k_bytes + kStepBytes - 1) / kStepBytes);
+    const double steps = (double)(int64_t)((k_steps + c.k_groups - 1) / c.k_groups);
+    const double t = passes * (steps * f.step + f.tile) + f.base;
+    const double t4 = t * t * t * t + floor_us * floor_us * floor_us * floor_us;
+    if (!best || t4 < best_t) {
+      best = &c;
+      best_t = t4;
+    }
+  }
+  return block_config(best->name);
 }
 
 int element_bytes(int type) { return type == GEMM_TYPE_E4M3 ? 1 : type == GEMM_TYPE_F32 ? 4 : 2; }
@@ -94,7 +153,9 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   const int64_t step = 16 / es - 1;
   if (((lda | ldb | stride_b) & step) != 0 || (ldc & 7) != 0) return GEMM_ERR_MISALIGNED;
 
-  const BlockConfig* c = config && config[0] ? block_config(config) : choose_block(R, N, E, experts);
+  const BlockConfig* c = config && config[0]
+                             ? block_config(config)
+                             : choose_block(type, R, N, K, E, experts, c_type);
   if (!c) return GEMM_ERR_UNSUPPORTED;
   if (R >= k2G || N >= k2G || K >= k2G / 2 || E >= k2G || a_rows >= k2G / 4 || lda >= k2G ||
       ldb >= k2G)
@@ -107,7 +168,6 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   const int64_t row_tiles = row_tile_bound(R, E, experts, c->bm);
   if (row_tiles * tiles_n >= k2G) return GEMM_ERR_UNSUPPORTED;
 
-  const int64_t row_tiles_per_b = experts ? 1 : row_tiles;
   BlockArgs a{};
   a.A = (const uint8_t*)A;
   a.B = (const uint8_t*)B;
@@ -132,7 +192,13 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   a.k_steps = (int32_t)((K * es + kStepBytes - 1) / kStepBytes);
   a.row_tiles = (int32_t)row_tiles;
   a.group_m = 4;
-  a.k_rot = row_tiles_per_b <= 1 ? 1 : 0;
+  // Where one row tile takes a whole B, tile column j starts 3 j K-steps in:
+  // rows of a power-of-two stride would otherwise send all workgroups to the
+  // same memory channels (M = 1 and 16 at 8192 x 8192 4 % faster, few rows
+  // an expert 3 %; with more row tiles, whose workgroups share B through the
+  // L2, up to 11 % slower).
+  const int64_t used = R < E ? R : E;
+  a.k_rot = (experts ? R <= used * c->bm : row_tiles == 1) ? 3 : 0;
   const hipError_t e =
       c->launch(a, (int)(row_tiles * tiles_n), (hipStream_t)stream, op_of(type), store_of(c_type));
   return e == hipSuccess ? GEMM_OK : hip_fail(e);
@@ -174,14 +240,15 @@ int gemm_moe(int type, int64_t R, int64_t N, int64_t K, int64_t E, int64_t T, co
                      stride_b, SB, ldsb, stride_sb, C, ldc, c_type, stream);
 }
 
-const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K) {
-  if (M < 0 || N < 0 || K < 0) return "invalid";
-  return gemm::choose_block(M, N, 1, false)->name;
+const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K, int c_type) {
+  if (M < 0 || N < 0 || K < 0 || !gemm::is_float_type(c_type)) return "invalid";
+  return gemm::choose_block(GEMM_TYPE_E4M3, M, N, K, 1, false, c_type)->name;
 }
 
-const char* gemm_moe_config_name(int64_t R, int64_t N, int64_t K, int64_t E) {
-  if (R < 0 || N < 0 || K < 0 || E < 0) return "invalid";
-  return gemm::choose_block(R, N, E, true)->name;
+const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int64_t E, int c_type) {
+  if (R < 0 || N < 0 || K < 0 || E < 0 || !gemm::is_float_type(c_type)) return "invalid";
+  if (type != GEMM_TYPE_E4M3 && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return "invalid";
+  return gemm::choose_block(type, R, N, K, E, true, c_type)->name;
 }
 
 const char* gemm_fp8_config_at(int i) {

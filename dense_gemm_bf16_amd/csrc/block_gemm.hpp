@@ -375,6 +375,10 @@ block_tile_kernel(BlockArgs a) {
   };
 
   const int rounds = (a.k_steps + WK - 1) / WK;
+  // A wave whose rows all lie past the tile's last one (an expert's last
+  // tile, C's last rows) only loads: the other waves of its SIMD then have
+  // the matrix core to themselves.
+  const bool idle = wm * Cfg::kWaveM >= rows_a;
   if constexpr (kPipe) {
     // Two slots, each refilled in two parts as soon as a part is read, so
     // that about a whole step's loads are always in flight (with one barrier
@@ -440,6 +444,15 @@ block_tile_kernel(BlockArgs a) {
     load_part(step_of(1), 1, 1, false);
     publish(step_of(0), 0, false);
     load_part(step_of(1), 1, 1, true);
+    if (idle) {
+      for (int X = 0; X < rounds; ++X) {
+        const int slot = X & 1, k_two = step_of(X + 2);
+        publish(step_of(X), slot, true);
+        load_part(k_two, slot, (X + 2) % 3, false);
+        publish(step_of(X + 1), slot ^ 1, false);
+        load_part(k_two, slot, 0, true);
+      }
+    }
     Frag fb[FN], fa[NBUF];
     f32x4 part[4];
 #pragma unroll
@@ -461,7 +474,7 @@ block_tile_kernel(BlockArgs a) {
     for (int j = 0; j < FN; ++j) fb[j] = read_frag(pb, j);
     read_row(0, 0, std::integral_constant<int, 1>{});
     int ss = 0;  // X % 3: the slot of step X's row scales, read to the step's end
-    for (int X = 0; X < rounds; ++X) {
+    for (int X = idle ? rounds : 0; X < rounds; ++X) {
       const int slot = X & 1, next = slot ^ 1;
       const int ss1 = ss == 2 ? 0 : ss + 1, ss2 = ss == 0 ? 2 : ss - 1;
       const int k_now = step_of(X);
@@ -535,6 +548,14 @@ block_tile_kernel(BlockArgs a) {
         for (int i = 0; i < L; ++i) trim_one(k, at_slot, i);
       }
       ring_wait_barrier<kInFlight>();
+      if (idle) {
+#pragma unroll
+        for (int l = 0; l < L; ++l) load_one(k_ahead, to_slot, l);
+        load_scales(k_ahead, to_slot);
+        at_slot = at_slot + 1 == S ? 0 : at_slot + 1;
+        to_slot = to_slot + 1 == S ? 0 : to_slot + 1;
+        continue;
+      }
       const uint32_t slot = at_slot * Cfg::kStageBytes;
       Frag fb[FN], fa[2];
 #pragma unroll

@@ -40,14 +40,20 @@ hipError_t launch_block_row(const BlockArgs& a, int grid, hipStream_t s, int op,
   });
 }
 
-// Built shapes: X(name, launcher template arguments).
-#define BLOCK_TILES(X)              \
-  X(b256x256, 256, 256, 2, 4, 1, 2) \
-  X(b128x128, 128, 128, 2, 2, 1, 2)
-#define BLOCK_ROWS(X)    \
-  X(r16x16, 1, 1, 4, 4)  \
-  X(r32x32, 2, 2, 4, 2)  \
-  X(r64x32, 4, 2, 4, 2)
+// Built shapes: X(name, launcher template arguments).  "k<n>": n groups of
+// waves share K.
+#define BLOCK_TILES(X)                \
+  X(b256x256, 256, 256, 2, 4, 1, 2)   \
+  X(b256x128, 256, 128, 4, 2, 1, 3)   \
+  X(b128x128, 128, 128, 2, 2, 1, 2)   \
+  X(b128x128k2, 128, 128, 2, 2, 2, 2) \
+  X(b64x128k2, 64, 128, 2, 2, 2, 3)   \
+  X(b64x64, 64, 64, 2, 2, 1, 4)       \
+  X(b64x64k2, 64, 64, 2, 2, 2, 4)     \
+  X(b32x128, 32, 128, 1, 4, 1, 3)     \
+  X(b32x64k4, 32, 64, 2, 2, 4, 3)     \
+  X(b32x32k4, 32, 32, 2, 2, 4, 4)
+#define BLOCK_ROWS(X) X(r16x16, 1, 1, 8, 4)
 
 #define BLOCK_DECLARE(NAME, A, B, C, D, E, S)                                            \
   extern template hipError_t launch_block_tile<A, B, C, D, E, S>(const BlockArgs&, int, \

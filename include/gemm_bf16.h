@@ -294,8 +294,9 @@ int gemm_fp8_ex(const char* config, int64_t M, int64_t N, int64_t K,
                 void* C, int64_t ldc, int c_type, void* stream);
 
 /* Name of the kernel shape gemm_fp8 chooses: "b<BM>x<BN>" stages tiles
- * through LDS, "r<BM>x<BN>" streams B into registers.  Static storage. */
-const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K);
+ * through LDS ("k<n>": n groups of waves share K), "r<BM>x<BN>" streams both
+ * operands into registers.  Static storage. */
+const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K, int c_type);
 
 /* The i-th kernel shape (of gemm_fp8 and gemm_moe), or NULL past the end. */
 const char* gemm_fp8_config_at(int i);
@@ -388,7 +389,8 @@ int gemm_moe_ex(const char* config, int type, int64_t R, int64_t N, int64_t K, i
                 void* C, int64_t ldc, int c_type, void* stream);
 
 /* Name of the kernel shape gemm_moe chooses.  Static storage. */
-const char* gemm_moe_config_name(int64_t R, int64_t N, int64_t K, int64_t E);
+const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int64_t E,
+                                 int c_type);
 
 /* out[t] = sum over j = 0 .. k-1 of weights[t*k + j] * Y[pos[t*k + j]], fp32
  * sums in that order, rounded once.  Y: R rows of N (y_type), out: T rows of

@@ -44,9 +44,12 @@ def test_config_names(g):
     assert len(names) == len(set(names)) >= 3
     for M in (0, 1, 16, 17, 64, 65, 300, 8192):
         assert g.fp8_config_name(M, 8192, 8192) in names
-        assert g.moe_config_name(M, 4096, 4096, 32) in names
-    assert g.fp8_config_name(-1, 1, 1) == "invalid"
-    assert g.moe_config_name(1, 1, 1, -1) == "invalid"
+        assert g.fp8_config_name(M, 8192, 8192, F32) in names
+        for type in (BF16, F16, E4M3):
+            assert g.moe_config_name(type, M, 4096, 4096, 32) in names
+    assert g.fp8_config_name(1, 8192, 1024) != g.fp8_config_name(8192, 8192, 1024) == "b256x256"
+    assert g.fp8_config_name(-1, 1, 1) == g.fp8_config_name(1, 1, 1, E4M3) == "invalid"
+    assert g.moe_config_name(E4M3, 1, 1, 1, -1) == g.moe_config_name(F32, 1, 1, 1, 1) == "invalid"
 
 
 def fp8(g, M=8, N=8, K=256, A=P, lda=256, SA=P, ldsa=8, B=P, ldb=256, SB=P, ldsb=2, C=P, ldc=8,
@@ -61,7 +64,7 @@ def fp8(g, M=8, N=8, K=256, A=P, lda=256, SA=P, ldsa=8, B=P, ldb=256, SB=P, ldsb
     (dict(C=NUL), 1), (dict(SA=NUL), 1), (dict(SB=NUL), 1), (dict(c_type=E4M3), 1),
     (dict(c_type=9), 1), (dict(A=ODD), 2), (dict(B=ODD), 2), (dict(C=ODD), 2),
     (dict(SA=ctypes.c_void_p(0x10002)), 2), (dict(lda=264), 2), (dict(ldb=264), 2),
-    (dict(ldc=12), 2), (dict(config=b"nope"), 3), (dict(K=262144 + 1, lda=262160, ldb=262160,
+    (dict(ldc=12), 2), (dict(config=b"nope"), 3), (dict(K=131072 + 1, lda=131088, ldb=131088,
                                                         ldsb=4000), 3),
     (dict(M=1 << 31, ldsa=1 << 31), 3), (dict(N=1 << 31, ldc=1 << 31), 3),
     (dict(ldb=1 << 28), 3), (dict(lda=1 << 28, M=300, ldsa=300, config=b"b256x256"), 3)])

@@ -8,7 +8,8 @@ from block_ref import HALF_STEP, block_product, check_rounded, dtype, padded
 
 pytestmark = pytest.mark.gpu
 
-CONFIGS = ["b256x256", "b128x128", "r16x16", "r32x32", "r64x32"]
+CONFIGS = ["b256x256", "b256x128", "b128x128", "b128x128k2", "b64x128k2", "b64x64", "b64x64k2",
+           "b32x128", "b32x64k4", "b32x32k4", "r16x16"]
 
 
 def small_ints(rng, shape):
@@ -61,7 +62,7 @@ def test_every_shape_is_exact_on_integers(config, out):
 
 
 @pytest.mark.parametrize("K", [1, 15, 16, 17, 64, 100, 127, 128, 129, 143, 255, 257, 1000])
-@pytest.mark.parametrize("config", ["b256x256", "b128x128", "r16x16", "r64x32"])
+@pytest.mark.parametrize("config", CONFIGS)
 def test_every_end_of_k(config, K):
     a, sa, b, sb = exact_case(37, 70, K, K)
     want, _ = block_product(a, sa, b, sb)

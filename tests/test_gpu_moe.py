@@ -8,7 +8,8 @@ from block_ref import block_product, check_rounded, dtype, padded
 
 pytestmark = pytest.mark.gpu
 
-CONFIGS = ["b256x256", "b128x128", "r16x16", "r32x32", "r64x32"]
+CONFIGS = ["b256x256", "b256x128", "b128x128", "b128x128k2", "b64x128k2", "b64x64", "b64x64k2",
+           "b32x128", "b32x64k4", "b32x32k4", "r16x16"]
 
 
 # ------------------------------------------------------------------ routing
@@ -235,7 +236,7 @@ def test_every_shape_of_experts_is_exact_on_integers(config, type):
 
 @pytest.mark.parametrize("type", ["e4m3", "bf16", "f16"])
 @pytest.mark.parametrize("K", [1, 7, 8, 63, 64, 65, 127, 130, 260])
-@pytest.mark.parametrize("config", ["b256x256", "b128x128", "r16x16"])
+@pytest.mark.parametrize("config", ["b256x256", "b256x128", "b128x128k2", "b64x64", "b32x32k4", "r16x16"])
 def test_experts_every_end_of_k(config, K, type):
     counts = [3, 0, 20]
     a, b, sa, sb, rows = experts_case(counts, 9, 33, K, type, K, True)
