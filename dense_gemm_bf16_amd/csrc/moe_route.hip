@@ -24,15 +24,50 @@
 namespace gemm {
 namespace {
 
-template <int TYPE>
-__device__ __forceinline__ float logit(const void* p, int64_t i) {
-  float v;
-  if constexpr (TYPE == kStoreF32) v = ((const float*)p)[i];
-  else if constexpr (TYPE == kStoreF16) v = (float)((const _Float16*)p)[i];
-  else v = (float)((const __bf16*)p)[i];
-  // NaN counts as -infinity, +infinity as the largest finite number
+// A logit (or bias) as it counts: NaN as -infinity, +infinity as the largest
+// finite number.
+__device__ __forceinline__ float logit(float v) {
   v = v != v ? -INFINITY : v;
   return fminf(v, 3.402823466e38f);
+}
+
+// v of the lane that differs from this one in bit D of its number, within
+// groups whose lanes already agree below that bit (so a mirror serves as the
+// swap of halves): vector operations only, no trip through LDS.
+template <int D>
+__device__ __forceinline__ uint32_t across(uint32_t v) {
+  if constexpr (D == 1) return __builtin_amdgcn_update_dpp(0, (int)v, 0xb1, 0xf, 0xf, true);  // quad 1,0,3,2
+  else if constexpr (D == 2) return __builtin_amdgcn_update_dpp(0, (int)v, 0x4e, 0xf, 0xf, true);  // quad 2,3,0,1
+  else if constexpr (D == 4) return __builtin_amdgcn_update_dpp(0, (int)v, 0x141, 0xf, 0xf, true);  // half mirror
+  else if constexpr (D == 8) return __builtin_amdgcn_update_dpp(0, (int)v, 0x140, 0xf, 0xf, true);  // mirror
+  else if constexpr (D == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return (threadIdx.x & 16) ? r[0] : r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return (threadIdx.x & 32) ? r[0] : r[1];
+  }
+}
+template <int D>
+__device__ __forceinline__ float across(float v) {
+  return __builtin_bit_cast(float, across<D>(__builtin_bit_cast(uint32_t, v)));
+}
+template <int D>
+__device__ __forceinline__ double across(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)across<D>((uint32_t)(b >> 32)) << 32 | across<D>((uint32_t)b));
+}
+
+// Calls f for D = 1, 2, .., below `lanes` (a power of two, the same in all
+// lanes).
+template <typename F>
+__device__ __forceinline__ void butterfly(int lanes, F&& f) {
+  if (lanes > 1) f(std::integral_constant<int, 1>{});
+  if (lanes > 2) f(std::integral_constant<int, 2>{});
+  if (lanes > 4) f(std::integral_constant<int, 4>{});
+  if (lanes > 8) f(std::integral_constant<int, 8>{});
+  if (lanes > 16) f(std::integral_constant<int, 16>{});
+  if (lanes > 32) f(std::integral_constant<int, 32>{});
 }
 
 // Largest value over the wave's lanes (unsigned), by row shifts within 16
@@ -82,24 +117,36 @@ struct Lane {
   __device__ __forceinline__ int expert(int j) const { return group * size + sub + j * per; }
 };
 
+// v of lane n (the same n in all lanes).
+__device__ __forceinline__ float of_lane(float v, int n) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), n));
+}
+__device__ __forceinline__ double of_lane(double v, int n) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, n);
+  const uint32_t hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), n);
+  return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+}
+
 // Whether this lane's group is among the best topk_groups.  F: float or
 // double.  `near` is set where fp32 cannot tell.
 template <typename F>
 __device__ __forceinline__ bool group_stays(const RouteArgs& a, const Lane& l, F best, F second,
                                             bool& near) {
   // the two largest over the group's lanes
-  for (int d = 1; d < l.per; d *= 2) {
-    const F b = __shfl_xor(best, d, 64), s = __shfl_xor(second, d, 64);
+  butterfly(l.per, [&](auto dc) __attribute__((always_inline)) {
+    constexpr int D = decltype(dc)::value;
+    const F b = across<D>(best), s = across<D>(second);
     const F low = best < b ? best : b;
     best = best < b ? b : best;
     second = second < s ? s : second;
     second = second < low ? low : second;
-  }
+  });
   const F g = a.group_top == 2 && l.size > 1 ? best + second : best;
   int rank = 0;
   F next = -INFINITY;  // the largest score of a group ranked below this one
   for (int o = 0; o < a.groups; ++o) {
-    const F v = __shfl(g, o * l.per, 64);
+    const F v = of_lane(g, o * l.per);
     const bool above = o != l.group && (v > g || (v == g && o < l.group));
     rank += above ? 1 : 0;
     if (!above && o != l.group && v > next) next = v;
@@ -168,19 +215,15 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Lane& l, uint32
   return true;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
-  return v;
-}
-__device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) v += __shfl_xor(v, d, 64);
+template <typename F>
+__device__ __forceinline__ F wave_sum(F v) {
+  butterfly(64, [&](auto dc) __attribute__((always_inline)) { v += across<decltype(dc)::value>(v); });
   return v;
 }
 
 template <int TYPE, int VPL>
 __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+  __shared__ float logits[4][VPL * 64];  // a wave's own, by place: lane and j
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= a.T) return;
   Lane l;
@@ -191,17 +234,29 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   l.sub = l.lane - l.group * l.per;
   l.size = a.E / a.groups;
 
-  float x[VPL], b[VPL];
+  // All loads go out before the first is used (places past the group read
+  // expert 0 and are set aside).
+  using X = std::conditional_t<TYPE == kStoreF32, float,
+                               std::conditional_t<TYPE == kStoreF16, _Float16, __bf16>>;
+  const X* row = (const X*)a.x + t * a.ldx;
+  X raw[VPL];
+  float b[VPL], x[VPL];
+#pragma unroll
+  for (int j = 0; j < VPL; ++j) {
+    raw[j] = row[l.has(j, a.groups) ? l.expert(j) : 0];
+    b[j] = 0.0f;
+  }
+  if (a.bias) {
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) b[j] = a.bias[l.has(j, a.groups) ? l.expert(j) : 0];
+  }
   float m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < VPL; ++j) {
-    x[j] = -INFINITY;
-    b[j] = 0.0f;
-    if (l.has(j, a.groups)) {
-      x[j] = logit<TYPE>(a.x, t * a.ldx + l.expert(j));
-      if (a.bias) b[j] = logit<kStoreF32>(a.bias, l.expert(j));
-    }
+    x[j] = l.has(j, a.groups) ? logit((float)raw[j]) : -INFINITY;
+    b[j] = logit(b[j]);
     m = fmaxf(m, x[j]);
+    logits[threadIdx.x >> 6][j * 64 + l.lane] = x[j];
   }
   float z = 1.0f;
   if (!a.sigmoid) {
@@ -213,8 +268,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     z = wave_sum(z);
     z = z > 0.0f ? z : 1.0f;
   }
+  // 1 / (1 + exp(-v)), or exp(v - m) / z
+  const float sign = a.sigmoid ? -1.0f : 1.0f, shift = a.sigmoid ? 0.0f : m;
   auto score = [&](float v) __attribute__((always_inline)) {
-    return a.sigmoid ? 1.0f / (1.0f + expf(-v)) : expf(v - m) / z;
+    const float e = expf(sign * (v - shift));
+    return a.sigmoid ? 1.0f / (1.0f + e) : e / z;
   };
 
   const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
@@ -272,7 +330,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   }
 
   float w = 0.0f;
-  if (l.lane < a.k) w = score(logit<TYPE>(a.x, t * a.ldx + my_id));
+  if (l.lane < a.k) {  // my_id's place: its group's lanes, dealt in turn
+    const int group = my_id / l.size, in = my_id - group * l.size;
+    const int j = in / l.per;
+    w = score(logits[threadIdx.x >> 6][j * 64 + group * l.per + (in - j * l.per)]);
+  }
   if (a.renorm) {
     const float sum = wave_sum(w);
     w = sum > 0.0f ? w / sum : 0.0f;
@@ -300,50 +362,67 @@ hipError_t route_of(const RouteArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// n / k for 0 <= n < 2^30: with 2^s >= k and M = floor(2^(30+s) / k) + 1,
+// n M / 2^(30+s) exceeds n / k by less than 2^-s <= 1 / k.
+struct Divide {
+  uint32_t M;
+  int shift;
+  explicit Divide(uint32_t k) {
+    int s = 0;
+    while ((uint64_t(1) << s) < k) ++s;
+    shift = 30 + s;
+    M = (uint32_t)((uint64_t(1) << shift) / k + 1);
+  }
+  __device__ __forceinline__ int operator()(int n) const {
+    return (int)(((uint64_t)(uint32_t)n * M) >> shift);
+  }
+};
+
 // A stable counting sort of the R = T * k ids, one workgroup per expert and
 // one more for the slots whose id names no expert: each reads every id twice
 // (they stay in L2), first to count the ids below its own, which is where
 // its rows start, then to place its own in their order.  One launch, no
 // atomics, so the order never depends on timing.  Each wave takes a
-// contiguous part of the ids, 256 at a time (four neighbours a lane), so the
-// waves meet once.
-typedef int i32x4u __attribute__((ext_vector_type(4), aligned(4)));
-
+// contiguous part of the ids, so the waves meet once.
+//
+// Bound by instructions, R / 64 vectors of ids for each expert, so a vector
+// costs as few as can be: two comparisons and two additions in the first
+// pass, in the second a comparison and a branch past the vectors without a
+// match; a product and a shift in place of the division by k (40.8 us at
+// 65536 ids and 256 experts with checked loads, ballots in both passes and a
+// division).  kBatch loads wait together.
 template <int W>
-__global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict__ ids, int R, int k,
-                                                      int E, int32_t* __restrict__ offsets,
+__global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict__ ids, int R,
+                                                      Divide by_k, int E,
+                                                      int32_t* __restrict__ offsets,
                                                       int32_t* __restrict__ rows,
                                                       int32_t* __restrict__ pos) {
   __shared__ int below_of[W], own_of[W];
+  constexpr int kBatch = 16;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t e = blockIdx.x;
-  const int part = ((R + W - 1) / W + 255) / 256 * 256;
+  const bool dropped = e == (uint32_t)E;  // the slots of no expert: ids >= E, unsigned
+  const int part = ((R + W - 1) / W + 63) / 64 * 64;
   const int begin = min((int64_t)wave * part, (int64_t)R), end = min((int64_t)begin + part, (int64_t)R);
-  // this lane's four ids from i on: an id that names no expert (negative
-  // ones are large unsigned) counts as E, a place past the part as E + 1
-  auto four = [&](int i, uint32_t (&v)[4]) __attribute__((always_inline)) {
-    if (i + 4 <= end) {
-      const i32x4u q = *(const i32x4u*)(ids + i);
+
+  // use(first slot, ids, lanes that hold one) for each 64 ids of the part
+  auto each = [&](auto&& use) __attribute__((always_inline)) {
+    int i = begin;
+    for (; i + kBatch * 64 <= end; i += kBatch * 64) {
+      uint32_t id[kBatch];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) v[u] = min((uint32_t)q[u], (uint32_t)E);
-    } else {
+      for (int b = 0; b < kBatch; ++b) id[b] = (uint32_t)ids[i + b * 64 + lane];
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
-        v[u] = i + u < end ? min((uint32_t)ids[i + u], (uint32_t)E) : (uint32_t)E + 1;
+      for (int b = 0; b < kBatch; ++b) use(i + b * 64, id[b], true);
     }
+    for (; i < end; i += 64) use(i, (uint32_t)ids[min(i + lane, end - 1)], i + lane < end);
   };
   int below = 0, own = 0;
-#pragma unroll 4
-  for (int i = begin; i < end; i += 256) {
-    uint32_t v[4];
-    four(i + lane * 4, v);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      below += v[u] < e ? 1 : 0;
-      own += v[u] == e ? 1 : 0;
-    }
-  }
+  each([&](int, uint32_t id, bool in) __attribute__((always_inline)) {
+    below += in && id < e ? 1 : 0;
+    own += in && (dropped ? id >= e : id == e) ? 1 : 0;
+  });
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
     below += __shfl_xor(below, d, 64);
@@ -359,27 +438,18 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
   for (int w = 0; w < W; ++w) at += below_of[w] + (w < wave ? own_of[w] : 0);
   if (wave == 0 && lane == 0) offsets[e] = at;
   if (own == 0) return;
-#pragma unroll 2
-  for (int i = begin; i < end; i += 256) {
-    uint32_t v[4];
-    four(i + lane * 4, v);
-    int p = at;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const uint64_t mine = __ballot(v[u] == e);
-      p += (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mine >> 32),
-                                          __builtin_amdgcn_mbcnt_lo((uint32_t)mine, 0u));
-      at += __popcll(mine);
+  each([&](int i, uint32_t id, bool in) __attribute__((always_inline)) {
+    const bool match = in && (dropped ? id >= e : id == e);
+    const uint64_t mine = __ballot(match);
+    if (mine == 0) return;
+    if (match) {
+      const int p = at + (int)__builtin_amdgcn_mbcnt_hi(
+                             (uint32_t)(mine >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mine, 0u));
+      rows[p] = dropped ? -1 : by_k(i + lane);
+      pos[i + lane] = dropped ? -1 : p;
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (v[u] == e) {
-        const int slot = i + lane * 4 + u;
-        rows[p] = e < (uint32_t)E ? slot / k : -1;
-        pos[slot] = e < (uint32_t)E ? p : -1;
-        ++p;
-      }
-  }
+    at += __popcll(mine);
+  });
 }
 
 // out[t] = sum over slots j of w[t,j] Y[pos[t,j]], in fp32 in the order of
@@ -483,10 +553,13 @@ hipError_t launch_route(const RouteArgs& a, int x_type, hipStream_t s) {
 hipError_t launch_plan(const int32_t* ids, int64_t T, int k, int E, int32_t* offsets,
                        int32_t* rows, int32_t* pos, hipStream_t s) {
   const int R = (int)(T * k);
+  const Divide by_k((uint32_t)k);
   if (R <= 4096)
-    hipLaunchKernelGGL(plan_kernel<4>, dim3(E + 1), dim3(256), 0, s, ids, R, k, E, offsets, rows, pos);
+    hipLaunchKernelGGL(plan_kernel<4>, dim3(E + 1), dim3(256), 0, s, ids, R, by_k, E, offsets, rows,
+                       pos);
   else
-    hipLaunchKernelGGL(plan_kernel<16>, dim3(E + 1), dim3(1024), 0, s, ids, R, k, E, offsets, rows, pos);
+    hipLaunchKernelGGL(plan_kernel<16>, dim3(E + 1), dim3(1024), 0, s, ids, R, by_k, E, offsets,
+                       rows, pos);
   return hipGetLastError();
 }
 
