@@ -3,6 +3,8 @@
 // point is stated in include/gemm_bf16.h.  Nothing here allocates or throws.
 #include "../../include/gemm_bf16.h"
 
+#include <math.h>
+#include <stdio.h>
 #include <string.h>
 
 #include "block_launch.hpp"
@@ -56,8 +58,7 @@ int64_t row_tile_bound(int64_t R, int64_t E, bool experts, int64_t bm) {
 // last pass with a fraction f of its workgroups part + (1 - part) * f of
 // that.  The whole takes at least as long as reading B at 5.2 TB/s (joined as
 // fourth powers, so near the floor the cheaper compute still counts).
-struct BlockCost {
-  const char* name;
+struct BlockCost {  // of the shape in the same place of block_configs()
   int k_groups, resident;
   struct Fit {
     float step, tile, part, base;  // us, us, share, us
@@ -65,52 +66,98 @@ struct BlockCost {
 };
 constexpr float kNever = 1e9f;
 constexpr BlockCost kBlockCosts[] = {
-    {"b256x256", 1, 1, {1.586f, 6.15f, 0.69f, 2.19f}, {kNever, 0, 0, 0}},
-    {"b256x128", 1, 1, {0.932f, 4.29f, 0.76f, 1.51f}, {kNever, 0, 0, 0}},
-    {"b128x128", 1, 2, {1.032f, 3.95f, 0.55f, 2.44f}, {1.822f, 4.58f, 0.61f, 0.00f}},
-    {"b128x128k2", 2, 1, {1.172f, 5.23f, 0.83f, 1.37f}, {1.962f, 5.14f, 0.85f, 0.00f}},
-    {"b64x128k2", 2, 1, {0.873f, 3.68f, 0.75f, 1.39f}, {1.299f, 3.53f, 0.86f, 0.73f}},
-    {"b64x64", 1, 2, {0.492f, 3.41f, 0.67f, 1.06f}, {0.774f, 1.59f, 0.56f, 2.97f}},
-    {"b64x64k2", 2, 1, {0.528f, 3.97f, 0.84f, 0.44f}, {0.799f, 3.88f, 0.85f, 0.57f}},
-    {"b32x128", 1, 2, {0.645f, 3.14f, 0.62f, 0.83f}, {1.032f, 0.00f, 0.50f, 2.96f}},
-    {"b32x64k4", 4, 1, {0.678f, 4.52f, 0.88f, 0.00f}, {0.932f, 4.82f, 0.90f, 0.00f}},
-    {"b32x32k4", 4, 1, {0.508f, 3.15f, 0.96f, 1.30f}, {0.663f, 3.46f, 0.92f, 1.12f}},
-    {"r16x16", 8, 4, {2.435f, 1.11f, 0.24f, 3.08f}, {2.435f, 1.11f, 0.24f, 3.08f}}};
+    /* b256x256   */ {1, 1, {1.586f, 6.15f, 0.69f, 2.19f}, {kNever, 0, 0, 0}},
+    /* b256x128   */ {1, 1, {0.932f, 4.29f, 0.76f, 1.51f}, {kNever, 0, 0, 0}},
+    /* b128x128   */ {1, 2, {1.032f, 3.95f, 0.55f, 2.44f}, {1.822f, 4.58f, 0.61f, 0.00f}},
+    /* b128x128k2 */ {2, 1, {1.172f, 5.23f, 0.83f, 1.37f}, {1.962f, 5.14f, 0.85f, 0.00f}},
+    /* b64x128k2  */ {2, 1, {0.873f, 3.68f, 0.75f, 1.39f}, {1.299f, 3.53f, 0.86f, 0.73f}},
+    /* b64x64     */ {1, 2, {0.492f, 3.41f, 0.67f, 1.06f}, {0.774f, 1.59f, 0.56f, 2.97f}},
+    /* b64x64k2   */ {2, 1, {0.528f, 3.97f, 0.84f, 0.44f}, {0.799f, 3.88f, 0.85f, 0.57f}},
+    /* b32x128    */ {1, 2, {0.645f, 3.14f, 0.62f, 0.83f}, {1.032f, 0.00f, 0.50f, 2.96f}},
+    /* b32x64k4   */ {4, 1, {0.678f, 4.52f, 0.88f, 0.00f}, {0.932f, 4.82f, 0.90f, 0.00f}},
+    /* b32x32k4   */ {4, 1, {0.508f, 3.15f, 0.96f, 1.30f}, {0.663f, 3.46f, 0.92f, 1.12f}},
+    /* r16x16     */ {8, 4, {2.435f, 1.11f, 0.24f, 3.08f}, {2.435f, 1.11f, 0.24f, 3.08f}}};
 constexpr double kStreamMBPerUs = 5.2, kStreamBaseUs = 2.5;
 
-const BlockConfig* choose_block(int type, int64_t R, int64_t N, int64_t K, int64_t E, bool experts,
-                                int c_type) {
+// Row tiles as the model counts them.  How the rows fall to the experts is
+// known on the device only: each expert with rows is taken to add half a
+// tile to the full ones.
+double model_row_tiles(const BlockConfig* shape, int64_t R, int64_t E, bool experts) {
+  if (!experts) return (double)((R + shape->bm - 1) / shape->bm);
+  const double used = (double)(R < E ? R : E);
+  const double rows = (double)R / shape->bm + 0.5 * used;
+  return rows < used ? used : rows;
+}
+
+// The fourth power of a launch's time under the model.
+double model_time4(const BlockCost& c, int bn, bool wide, double row_tiles, double b_rows,
+                   int64_t N, double k_bytes) {
+  const BlockCost::Fit& f = wide ? c.wide : c.fit;
+  const double units = row_tiles * (double)((N + bn - 1) / bn);
+  const double pass = 256.0 * c.resident;
+  double passes = (double)(int64_t)(units / pass);
+  const double rest = units / pass - passes;
+  if (rest > 0) passes += f.part + (1 - f.part) * rest;
+  const double k_steps = (double)(int64_t)((k_bytes + kStepBytes - 1) / kStepBytes);
+  const double steps = (double)(int64_t)((k_steps + c.k_groups - 1) / c.k_groups);
+  const double t = passes * (steps * f.step + f.tile) + f.base;
+  const double floor_us = b_rows * (double)N * k_bytes * 1e-6 / kStreamMBPerUs + kStreamBaseUs;
+  return t * t * t * t + floor_us * floor_us * floor_us * floor_us;
+}
+
+// What a call runs: one shape on all of C, or (dense products only) `shape`
+// on columns 0 .. split_n - 1 and `tail` on the rest.
+struct BlockPlan {
+  const BlockConfig* shape;
+  const BlockConfig* tail;
+  int64_t split_n;
+};
+
+BlockPlan choose_block(int type, int64_t R, int64_t N, int64_t K, int64_t E, bool experts,
+                       int c_type) {
   const bool wide = type == GEMM_TYPE_E4M3 && c_type == GEMM_TYPE_F32;
-  const double used = (double)(R < E ? R : E);  // experts that may have rows
+  const double b_rows = experts ? (double)(R < E ? R : E) : 1.0;  // B's, of N rows each
   const double k_bytes = (double)K * (type == GEMM_TYPE_E4M3 ? 1 : 2);
-  const double floor_us = used * N * k_bytes * 1e-6 / kStreamMBPerUs + kStreamBaseUs;
-  const BlockCost* best = nullptr;
-  double best_t = 0;
-  for (const BlockCost& c : kBlockCosts) {
-    const BlockConfig* shape = block_config(c.name);
-    const BlockCost::Fit& f = wide ? c.wide : c.fit;
-    // How the rows fall to the experts is known on the device only: each
-    // expert with rows is taken to add half a tile to the full ones.
-    double rows = (double)((R + shape->bm - 1) / shape->bm);
-    if (experts) {
-      rows = (double)R / shape->bm + 0.5 * used;
-      if (rows < used) rows = used;
+  const BlockConfig* shapes = block_configs();
+  auto cheapest = [&](int64_t n, double* t4) {
+    const BlockConfig* best = nullptr;
+    for (int i = 0; shapes[i].name; ++i) {
+      const BlockConfig* shape = shapes + i;
+      const double t = model_time4(kBlockCosts[i], shape->bn, wide,
+                                   model_row_tiles(shape, R, E, experts), b_rows, n, k_bytes);
+      if (best && t >= *t4) continue;
+      best = shape;
+      *t4 = t;
     }
-    const double units = rows * (double)((N + shape->bn - 1) / shape->bn);
-    const double pass = 256.0 * c.resident;
-    double passes = (double)(int64_t)(units / pass);
-    const double rest = units / pass - passes;
-    if (rest > 0) passes += f.part + (1 - f.part) * rest;
-    const double k_steps = (double)(int64_t)((k_bytes + kStepBytes - 1) / kStepBytes);
-    const double steps = (double)(int64_t)((k_steps + c.k_groups - 1) / c.k_groups);
-    const double t = passes * (steps * f.step + f.tile) + f.base;
-    const double t4 = t * t * t * t + floor_us * floor_us * floor_us * floor_us;
-    if (!best || t4 < best_t) {
-      best = &c;
-      best_t = t4;
-    }
+    return best;
+  };
+  double t4 = 0;
+  BlockPlan plan{cheapest(N, &t4), nullptr, N};
+  if (experts || R < 1) return plan;
+  // Where a shape's last pass over the CUs would be part empty: the columns
+  // that fill its whole passes, then the rest in the shape that is cheapest
+  // for them (777 x 10240 x 4104 with fp32 output 97 -> 82 us, as 511
+  // workgroups of 128 x 128 and 182 of 64 x 64).
+  double best = sqrt(sqrt(t4)) * 0.97;
+  for (int i = 0; shapes[i].name; ++i) {
+    const BlockConfig* shape = shapes + i;
+    const BlockCost& c = kBlockCosts[i];
+    const int64_t rows = (R + shape->bm - 1) / shape->bm, cols = (N + shape->bn - 1) / shape->bn;
+    const int64_t pass = 256 * c.resident;
+    if (rows > pass) continue;
+    const int64_t head = rows * cols / pass * pass / rows * shape->bn / kScaleBlock * kScaleBlock;
+    if (head <= 0 || head >= N) continue;
+    const double t1 =
+        sqrt(sqrt(model_time4(c, shape->bn, wide, (double)rows, b_rows, head, k_bytes)));
+    if (t1 >= best) continue;
+    double tail4 = 0;
+    const BlockConfig* tail = cheapest(N - head, &tail4);
+    const double t = t1 + sqrt(sqrt(tail4));
+    if (t >= best) continue;
+    best = t;
+    plan = BlockPlan{shape, tail, head};
   }
-  return block_config(best->name);
+  return plan;
 }
 
 int element_bytes(int type) { return type == GEMM_TYPE_E4M3 ? 1 : type == GEMM_TYPE_F32 ? 4 : 2; }
@@ -153,20 +200,26 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   const int64_t step = 16 / es - 1;
   if (((lda | ldb | stride_b) & step) != 0 || (ldc & 7) != 0) return GEMM_ERR_MISALIGNED;
 
-  const BlockConfig* c = config && config[0]
-                             ? block_config(config)
-                             : choose_block(type, R, N, K, E, experts, c_type);
-  if (!c) return GEMM_ERR_UNSUPPORTED;
+  BlockPlan plan{nullptr, nullptr, N};
+  if (config && config[0]) {
+    plan.shape = block_config(config);
+    if (!plan.shape) return GEMM_ERR_UNSUPPORTED;
+  } else {
+    plan = choose_block(type, R, N, K, E, experts, c_type);
+  }
   if (R >= k2G || N >= k2G || K >= k2G / 2 || E >= k2G || a_rows >= k2G / 4 || lda >= k2G ||
       ldb >= k2G)
     return GEMM_ERR_UNSUPPORTED;
   if (scaled && kb > kMaxKSteps) return GEMM_ERR_UNSUPPORTED;
-  if (c->bn * ldb * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
-  if ((rows ? a_rows : (int64_t)c->bm) * lda * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
+  const BlockConfig* shapes[2] = {plan.shape, plan.tail};
+  for (const BlockConfig* c : shapes) {
+    if (!c) continue;
+    if (c->bn * ldb * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
+    if ((rows ? a_rows : (int64_t)c->bm) * lda * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
+    if (row_tile_bound(R, E, experts, c->bm) * ((N + c->bn - 1) / c->bn) >= k2G)
+      return GEMM_ERR_UNSUPPORTED;
+  }
   if (!work) return GEMM_OK;
-  const int64_t tiles_n = (N + c->bn - 1) / c->bn;
-  const int64_t row_tiles = row_tile_bound(R, E, experts, c->bm);
-  if (row_tiles * tiles_n >= k2G) return GEMM_ERR_UNSUPPORTED;
 
   BlockArgs a{};
   a.A = (const uint8_t*)A;
@@ -184,25 +237,38 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   a.stride_b = stride_b * es;
   a.stride_sb = stride_sb;
   a.M = (int32_t)R;
-  a.N = (int32_t)N;
   a.kbytes = (int32_t)(K * es);
   a.a_rows = (int32_t)a_rows;
   a.E = (int32_t)E;
-  a.tiles_n = (int32_t)tiles_n;
   a.k_steps = (int32_t)((K * es + kStepBytes - 1) / kStepBytes);
-  a.row_tiles = (int32_t)row_tiles;
   a.group_m = 4;
-  // Where one row tile takes a whole B, tile column j starts 3 j K-steps in:
-  // rows of a power-of-two stride would otherwise send all workgroups to the
-  // same memory channels (M = 1 and 16 at 8192 x 8192 4 % faster, few rows
-  // an expert 3 %; with more row tiles, whose workgroups share B through the
-  // L2, up to 11 % slower).
-  const int64_t used = R < E ? R : E;
-  a.k_rot = (experts ? R <= used * c->bm : row_tiles == 1) ? 3 : 0;
-  const hipError_t e =
-      c->launch(a, (int)(row_tiles * tiles_n), (hipStream_t)stream, op_of(type), store_of(c_type));
+  auto launch = [&](const BlockConfig* c, int64_t n) {
+    const int64_t tiles_n = (n + c->bn - 1) / c->bn;
+    const int64_t row_tiles = row_tile_bound(R, E, experts, c->bm);
+    a.N = (int32_t)n;
+    a.tiles_n = (int32_t)tiles_n;
+    a.row_tiles = (int32_t)row_tiles;
+    // Where one row tile takes a whole B, tile column j starts 3 j K-steps
+    // in: rows of a power-of-two stride would otherwise send all workgroups
+    // to the same memory channels (M = 1 and 16 at 8192 x 8192 4 % faster,
+    // few rows an expert 3 %; with more row tiles, whose workgroups share B
+    // through the L2, up to 11 % slower).
+    const int64_t used = R < E ? R : E;
+    a.k_rot = (experts ? R <= used * c->bm : row_tiles == 1) ? 3 : 0;
+    return c->launch(a, (int)(row_tiles * tiles_n), (hipStream_t)stream, op_of(type),
+                     store_of(c_type));
+  };
+  hipError_t e = launch(plan.shape, plan.split_n);
+  if (e == hipSuccess && plan.tail) {  // (the split lies on a scale block's border)
+    a.B += plan.split_n * a.ldb;
+    if (SB) a.SB += plan.split_n / kScaleBlock * ldsb;
+    a.C = (uint8_t*)C + plan.split_n * element_bytes(c_type);
+    e = launch(plan.tail, N - plan.split_n);
+  }
   return e == hipSuccess ? GEMM_OK : hip_fail(e);
 }
+
+thread_local char g_plan_name[64];
 
 }  // namespace
 }  // namespace gemm
@@ -242,13 +308,16 @@ int gemm_moe(int type, int64_t R, int64_t N, int64_t K, int64_t E, int64_t T, co
 
 const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K, int c_type) {
   if (M < 0 || N < 0 || K < 0 || !gemm::is_float_type(c_type)) return "invalid";
-  return gemm::choose_block(GEMM_TYPE_E4M3, M, N, K, 1, false, c_type)->name;
+  const gemm::BlockPlan p = gemm::choose_block(GEMM_TYPE_E4M3, M, N, K, 1, false, c_type);
+  if (!p.tail) return p.shape->name;
+  snprintf(gemm::g_plan_name, sizeof gemm::g_plan_name, "%s+%s", p.shape->name, p.tail->name);
+  return gemm::g_plan_name;
 }
 
 const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int64_t E, int c_type) {
   if (R < 0 || N < 0 || K < 0 || E < 0 || !gemm::is_float_type(c_type)) return "invalid";
   if (type != GEMM_TYPE_E4M3 && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return "invalid";
-  return gemm::choose_block(type, R, N, K, E, true, c_type)->name;
+  return gemm::choose_block(type, R, N, K, E, true, c_type).shape->name;
 }
 
 const char* gemm_fp8_config_at(int i) {

@@ -295,7 +295,9 @@ int gemm_fp8_ex(const char* config, int64_t M, int64_t N, int64_t K,
 
 /* Name of the kernel shape gemm_fp8 chooses: "b<BM>x<BN>" stages tiles
  * through LDS ("k<n>": n groups of waves share K), "r<BM>x<BN>" streams both
- * operands into registers.  Static storage. */
+ * operands into registers; "<shape>+<shape>": the columns that fill whole
+ * passes over the GPU's compute units in the first, the rest in the second
+ * (two launches).  Per-thread static storage. */
 const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K, int c_type);
 
 /* The i-th kernel shape (of gemm_fp8 and gemm_moe), or NULL past the end. */

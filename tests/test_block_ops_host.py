@@ -43,11 +43,12 @@ def test_config_names(g):
     names = g.fp8_config_names()
     assert len(names) == len(set(names)) >= 3
     for M in (0, 1, 16, 17, 64, 65, 300, 8192):
-        assert g.fp8_config_name(M, 8192, 8192) in names
-        assert g.fp8_config_name(M, 8192, 8192, F32) in names
+        for c_type in (BF16, F16, F32):
+            assert all(n in names for n in g.fp8_config_name(M, 8192, 8192, c_type).split("+"))
         for type in (BF16, F16, E4M3):
             assert g.moe_config_name(type, M, 4096, 4096, 32) in names
     assert g.fp8_config_name(1, 8192, 1024) != g.fp8_config_name(8192, 8192, 1024) == "b256x256"
+    assert "+" in g.fp8_config_name(777, 10240, 4104, F32)  # a part-empty last pass
     assert g.fp8_config_name(-1, 1, 1) == g.fp8_config_name(1, 1, 1, E4M3) == "invalid"
     assert g.moe_config_name(E4M3, 1, 1, 1, -1) == g.moe_config_name(F32, 1, 1, 1, 1) == "invalid"
 

@@ -86,6 +86,30 @@ def test_automatic_shapes_on_normal_values(M, N, K):
         check_rounded(product(a, sa, b, sb, out), want, err, out)
 
 
+@pytest.mark.parametrize("M, N, K, out", [(260, 10000, 300, "f32"), (777, 10240, 400, "f32"),
+                                          (650, 14336, 256, "bf16"), (1100, 9001, 1000, "f16")])
+def test_two_launches_cover_c(M, N, K, out):
+    """Products whose columns go to two shapes, on integers: every element of
+    C once, with its own columns' scales.  (f16: sums stay below 65504.)"""
+    import torch
+
+    a, sa, b, sb = exact_case(M, N, K, M)
+    sa /= 16
+    want, _ = block_product(a, sa, b, sb)
+    got = product(a, sa, b, sb, out)
+    assert np.array_equal(got, torch.from_numpy(want.astype(np.float32)).to(dtype(out)).double().numpy())
+
+
+def test_two_launch_plans_are_reached():
+    import dense_gemm_bf16_amd as g
+
+    codes = {"bf16": g.GEMM_TYPE_BF16, "f16": g.GEMM_TYPE_F16, "f32": g.GEMM_TYPE_F32}
+    plans = [g.fp8_config_name(M, N, K, codes[o]) for M, N, K, o in
+             [(260, 10000, 300, "f32"), (777, 10240, 400, "f32"), (650, 14336, 256, "bf16"),
+              (1100, 9001, 1000, "f16")]]
+    assert any("+" in p for p in plans), plans
+
+
 def test_special_codes_and_scales():
     """Every finite e4m3 code, large scales, zero scales; a NaN code or scale
     reaches only the sums it enters.  (Codes from 256 = 2^8 on, times 2^120,
