@@ -368,7 +368,8 @@ int gemm_moe_route(int64_t T, int64_t E, int64_t k, const void* X, int64_t ldx, 
   if (gemm::misaligned(X, gemm::element_bytes(x_type)) || gemm::misaligned(bias, 4) ||
       gemm::misaligned(ids, 4) || gemm::misaligned(weights, 4))
     return GEMM_ERR_MISALIGNED;
-  if (E > 1024 || k > 64 || groups > 64 || T * k >= gemm::k2G / 2) return GEMM_ERR_UNSUPPORTED;
+  // (64 threads a token: a grid holds fewer than 2^32)
+  if (E > 1024 || k > 64 || groups > 64 || T >= (int64_t(1) << 26)) return GEMM_ERR_UNSUPPORTED;
   if (T == 0) return GEMM_OK;
   const gemm::RouteArgs a{X,        bias,     ids,      weights,          T,
                           ldx,      (int)E,   (int)k,   (int)groups,      (int)topk_groups,
@@ -404,7 +405,7 @@ int gemm_moe_combine(int64_t T, int64_t k, int64_t N, int64_t R, const void* Y, 
       gemm::misaligned(pos, 4) || gemm::misaligned(weights, 4) || (ldo & 7) != 0)
     return GEMM_ERR_MISALIGNED;
   if (T >= gemm::k2G || N >= gemm::k2G || R >= gemm::k2G || k >= gemm::k2G ||
-      T * ((N + 7) / 8) >= gemm::k2G * 256 - 256)
+      T * ((N + 7) / 8) >= 2 * gemm::k2G - 256)  // (a grid holds fewer than 2^32 threads)
     return GEMM_ERR_UNSUPPORTED;
   if (T == 0 || N == 0) return GEMM_OK;
   const gemm::CombineArgs a{Y, pos, weights, out, T, N, R, ldy, ldo, (int)k};

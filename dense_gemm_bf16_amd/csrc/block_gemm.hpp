@@ -67,12 +67,13 @@ __device__ __forceinline__ void expert_rows(const BlockArgs& a, int e, int& begi
   if (end < begin) end = begin;
 }
 
-// Inclusive sum over the wave's lanes.
+// Inclusive sum over the wave's lanes, held below 2^30 (ranges that overlap
+// could add up to more than an int holds; those that do not stay below it).
 __device__ __forceinline__ int wave_scan(int v, int lane) {
 #pragma unroll
   for (int d = 1; d < 64; d *= 2) {
     const int o = __shfl_up(v, d, 64);
-    if (lane >= d) v += o;
+    if (lane >= d) v = min(v + o, (1 << 30) - 1);
   }
   return v;
 }
@@ -81,13 +82,15 @@ struct RowTile {
   int expert, begin, end;  // rows [begin, end) of C, at most BM of them used
 };
 
-// Row tiles (of BM rows) of all experts: expert e has ceil(rows / BM).
+// Row tiles (of BM rows) of all experts: expert e has ceil(rows / BM).  At
+// most the bound that the grid is made for.
 __device__ __forceinline__ int count_row_tiles(const BlockArgs& a, int BM, int lane) {
   int total = 0;
   for (int e0 = 0; e0 < a.E; e0 += 64) {
     int b = 0, n = 0;
     if (e0 + lane < a.E) expert_rows(a, e0 + lane, b, n);
     total += __shfl(wave_scan((n - b + BM - 1) / BM, lane), 63, 64);
+    total = min(total, a.row_tiles);
   }
   return __builtin_amdgcn_readfirstlane(total);
 }
@@ -100,7 +103,7 @@ __device__ __forceinline__ bool find_row_tile(const BlockArgs& a, int BM, int t,
     int b = 0, n = 0;
     if (e0 + lane < a.E) expert_rows(a, e0 + lane, b, n);
     const int tiles = (n - b + BM - 1) / BM;
-    const int upto = before + wave_scan(tiles, lane);
+    const int upto = min(before, 1 << 30) + wave_scan(tiles, lane);
     const uint64_t hit = __ballot(t < upto);
     if (hit != 0) {
       const int l = __builtin_ctzll(hit);  // the first expert whose tiles pass t
@@ -461,7 +464,7 @@ block_tile_kernel(BlockArgs a) {
     float sb = 0.0f;
     auto scale_b = [&](int k) __attribute__((always_inline)) {
       if constexpr (kScaled)
-        sb = sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + (k < a.k_steps ? k : 0)];
+        sb = k < a.k_steps ? sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + k] : 0.0f;
     };
     auto read_row = [&](int slot, int sslot, auto ic) __attribute__((always_inline)) {
       constexpr int i = decltype(ic)::value;
@@ -563,7 +566,7 @@ block_tile_kernel(BlockArgs a) {
       fa[0] = read_frag(pa + slot, 0);
       float sb = 0.0f;
       if constexpr (kScaled)
-        sb = sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + (k < a.k_steps ? k : 0)];
+        sb = k < a.k_steps ? sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + k] : 0.0f;
       f32x4 part[2][FN];
       float sc[2];
 #pragma unroll

@@ -332,7 +332,7 @@ int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_ty
 #define GEMM_SCORE_SOFTMAX 0
 #define GEMM_SCORE_SIGMOID 1
 
-/* Route T tokens over E experts (E <= 1024), k each (k <= 64).  X: T rows of
+/* Route T tokens (T < 2^26) over E experts (E <= 1024), k each (k <= 64).  X: T rows of
  * E logits (x_type BF16, F16 or F32, row stride ldx, any alignment of the
  * type).  Per token:
  *   s = softmax or sigmoid of the logits
@@ -398,7 +398,8 @@ const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int6
  * sums in that order, rounded once.  Y: R rows of N (y_type), out: T rows of
  * N (out_type; BF16, F16 or F32 each).  Y's rows may start at any element;
  * out is 16-byte aligned with ldo a multiple of 8.  A pos outside 0 .. R-1 adds nothing; a token whose pairs
- * were all dropped gets zeros.  Returns a status. */
+ * were all dropped gets zeros.  out must not overlap Y.  T * ceil(N / 8) is
+ * limited to 2^32 - 256.  Returns a status. */
 int gemm_moe_combine(int64_t T, int64_t k, int64_t N, int64_t R, const void* Y, int64_t ldy,
                      int y_type, const int32_t* pos, const float* weights, void* out,
                      int64_t ldo, int out_type, void* stream);

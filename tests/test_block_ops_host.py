@@ -129,7 +129,7 @@ def route(g, T=4, E=64, k=8, X=P, ldx=64, x_type=F32, bias=NUL, score=0, groups=
     (dict(score=2), 1), (dict(top=3), 1), (dict(x_type=E4M3), 1), (dict(X=NUL), 1),
     (dict(ids=NUL), 1), (dict(w=NUL), 1), (dict(X=ctypes.c_void_p(0x10002)), 2),
     (dict(E=2048, ldx=2048), 3), (dict(E=128, ldx=128, groups=128, topk_groups=64), 3),
-    (dict(E=256, ldx=256, k=65, topk_groups=8), 3), (dict(T=1 << 28), 3)])
+    (dict(E=256, ldx=256, k=65, topk_groups=8), 3), (dict(T=1 << 26), 3)])
 def test_route_refusals(g, bad, code):
     assert route(g, **bad) == code
 
@@ -151,7 +151,7 @@ def combine(g, T=4, k=2, N=64, R=8, Y=P, ldy=64, y_type=BF16, pos=P, w=P, out=P,
     (dict(T=-1), 1), (dict(k=-1), 1), (dict(N=-1), 1), (dict(R=-1), 1), (dict(ldy=56), 1),
     (dict(ldo=56), 1), (dict(y_type=E4M3), 1), (dict(out_type=E4M3), 1), (dict(Y=NUL), 1),
     (dict(pos=NUL), 1), (dict(w=NUL), 1), (dict(out=NUL), 1), (dict(Y=ctypes.c_void_p(0x10001)), 2),
-    (dict(out=ODD), 2), (dict(ldo=68), 2), (dict(T=1 << 31), 3)])
+    (dict(out=ODD), 2), (dict(ldo=68), 2), (dict(T=1 << 31), 3), (dict(T=1 << 29), 3)])
 def test_combine_refusals(g, bad, code):
     assert combine(g, **bad) == code
 

@@ -136,6 +136,21 @@ def test_special_codes_and_scales():
         assert np.isfinite(got[[0, 2], :128]).all()
 
 
+def test_infinite_scale_stays_in_its_columns_and_signs():
+    """Three K-steps, which leaves wave groups that share K steps past the
+    last one: an infinite scale of the first block gives infinities, not NaN."""
+    for config in CONFIGS:
+        a, b = np.ones((40, 384), np.float32), np.ones((200, 384), np.float32)
+        a[3] = -1
+        sb = np.ones((2, 3), np.float32)
+        sb[0, 0] = np.inf
+        got = product(a, np.ones((3, 40), np.float32), b, sb, "f32", config)
+        want = np.full((40, 200), 384.0)
+        want[:, :128] = np.inf
+        want[3] *= -1
+        assert np.array_equal(got, want), config
+
+
 def test_c_outside_its_range_is_left_alone():
     import torch
 

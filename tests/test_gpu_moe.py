@@ -294,6 +294,19 @@ def test_rows_and_offsets_outside_are_cut(config, type):
     assert bool((c == 7.0).all())
 
 
+@pytest.mark.parametrize("config", CONFIGS)
+def test_overlapping_ranges_stay_inside(config):
+    """Ranges that overlap give unspecified rows, but touch nothing else."""
+    import torch
+
+    a, b, sa, sb, rows = experts_case([22] * 70, 9, 40, 136, "e4m3", 3, True)
+    offsets = np.tile(np.array([0, 22], np.int32), 36)[:71]
+    buf = torch.full((24, 64), 7.0, device="cuda")
+    run_experts(a, b, sa, sb, offsets, rows[:22], "f32", config, c=buf[1:23, 8:48])
+    buf[1:23, 8:48] = 7.0
+    assert bool((buf == 7.0).all())
+
+
 def test_experts_without_rows_or_columns():
     import torch
 
