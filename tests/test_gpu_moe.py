@@ -481,3 +481,37 @@ def test_layer_in_a_graph_and_on_two_streams():
     torch.cuda.synchronize()
     for o in got:
         assert torch.equal(o, want)
+
+
+def test_offsets_past_32_bits():
+    """Experts 3 GB apart, rows of C and Y 126 MB apart, rows of logits and
+    of what is quantised 10 GB apart: the addresses are 64-bit."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    a, b, sa, sb, rows = experts_case([20, 0, 30], 25, 130, 200, "e4m3", 8, True)
+    offsets = offsets_of([20, 0, 30])
+    want, _ = want_experts(a, b, sa, sb, offsets, rows, 50)
+    gap = 3 << 30
+    big = torch.empty(2 * gap + 130 * 208, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+    B = big.as_strided((3, 130, 200), (gap, 208, 1))
+    B.copy_(b.cuda())
+    wide = torch.empty(50 * (30 << 20), device="cuda")
+    C = wide.as_strided((50, 130), (30 << 20, 1))
+    A = torch.zeros((25, 208), device="cuda").to(torch.float8_e4m3fn)[:, :200]
+    A.copy_(a.cuda())
+    args = [torch.from_numpy(x).cuda() for x in (offsets, rows, sa, sb)]
+    for config in (None, "b256x256", "b32x128", "r16x16"):
+        C.zero_()
+        g.moe_matmul(A, B, args[0], rows=args[1], SA=args[2], SB=args[3], out=C, config=config)
+        assert np.array_equal(C.double().cpu().numpy(), want), config
+    pos = torch.arange(50, device="cuda", dtype=torch.int32).flip(0).view(25, 2)
+    w = torch.rand((25, 2), device="cuda")
+    assert torch.equal(g.moe_combine(C, pos, w), g.moe_combine(C.contiguous(), pos, w))
+    del big, B, C
+    far = torch.empty((5 << 30) + 256, device="cuda", dtype=torch.bfloat16)  # rows 5 Gi elements apart
+    two = far.as_strided((2, 256), (5 << 30, 1))
+    two.copy_(torch.randn((2, 256), device="cuda"))
+    assert torch.equal(g.quantize_fp8(two)[1], g.quantize_fp8(two.contiguous())[1])
+    assert torch.equal(g.moe_route(two, 4)[0], g.moe_route(two.contiguous(), 4)[0])
