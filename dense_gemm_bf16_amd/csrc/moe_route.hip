@@ -403,6 +403,7 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t e = blockIdx.x;
   const bool dropped = e == (uint32_t)E;  // the slots of no expert: ids >= E, unsigned
+  const uint32_t span = dropped ? 0u - e : 1u;  // own ids: e .. e + span - 1
   const int part = ((R + W - 1) / W + 63) / 64 * 64;
   const int begin = min((int64_t)wave * part, (int64_t)R), end = min((int64_t)begin + part, (int64_t)R);
 
@@ -421,13 +422,10 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
   int below = 0, own = 0;
   each([&](int, uint32_t id, bool in) __attribute__((always_inline)) {
     below += in && id < e ? 1 : 0;
-    own += in && (dropped ? id >= e : id == e) ? 1 : 0;
+    own += __popcll(__ballot(in && id - e < span));
   });
 #pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    below += __shfl_xor(below, d, 64);
-    own += __shfl_xor(own, d, 64);
-  }
+  for (int d = 1; d < 64; d *= 2) below += __shfl_xor(below, d, 64);
   if (lane == 0) {
     below_of[wave] = below;
     own_of[wave] = own;
@@ -439,7 +437,7 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
   if (wave == 0 && lane == 0) offsets[e] = at;
   if (own == 0) return;
   each([&](int i, uint32_t id, bool in) __attribute__((always_inline)) {
-    const bool match = in && (dropped ? id >= e : id == e);
+    const bool match = in && id - e < span;
     const uint64_t mine = __ballot(match);
     if (mine == 0) return;
     if (match) {
