@@ -18,7 +18,9 @@
 // One wave per token.  A group's experts are dealt over 64 / (groups rounded
 // up to a power of two) neighbouring lanes, so a group's best two and its
 // score stay within those lanes, and the k rounds of a maximum over the wave
-// cost six DPP steps each.
+// cost six DPP steps each.  Bound by instructions (about 85 a round): 18 us
+// for 8192 tokens of 256 experts, k = 8, against 2 us for the bytes; a wave
+// by itself takes 4 us.
 #include "block_internal.h"
 
 namespace gemm {
@@ -386,11 +388,11 @@ struct Divide {
 // contiguous part of the ids, so the waves meet once.
 //
 // Bound by instructions, R / 64 vectors of ids for each expert, so a vector
-// costs as few as can be: two comparisons and two additions in the first
+// costs as few as can be: two comparisons and one addition in the first
 // pass, in the second a comparison and a branch past the vectors without a
-// match; a product and a shift in place of the division by k (40.8 us at
-// 65536 ids and 256 experts with checked loads, ballots in both passes and a
-// division).  kBatch loads wait together.
+// match; a product and a shift in place of the division by k (10 us at 65536
+// ids and 256 experts, launched back to back; 41 us with checked loads,
+// ballots in both passes and a division).  kBatch loads wait together.
 template <int W>
 __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict__ ids, int R,
                                                       Divide by_k, int E,
@@ -453,7 +455,8 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
 // out[t] = sum over slots j of w[t,j] Y[pos[t,j]], in fp32 in the order of
 // the slots.  Eight columns a thread, Y's rows
 // starting at any element; a slot whose pos lies outside Y
-// (dropped) adds nothing.
+// (dropped) adds nothing.  Bound by memory: 604 MB (8192 tokens, k = 8, rows
+// of 4096 bf16) in 126 us, 4.8 TB/s.
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef _Float16 f16x8u __attribute__((ext_vector_type(8), aligned(2)));
 typedef __bf16 bf16x8u __attribute__((ext_vector_type(8), aligned(2)));
