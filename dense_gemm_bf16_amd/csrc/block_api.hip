@@ -342,8 +342,7 @@ int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_ty
   if (gemm::misaligned(X, gemm::element_bytes(x_type)) || gemm::misaligned(Q, 16) ||
       gemm::misaligned(S, 4) || (ldq & 15) != 0)
     return GEMM_ERR_MISALIGNED;
-  if ((M + 15) / 16 > 65535 || (block_rows == 128 && (M + 127) / 128 > 65535))
-    return GEMM_ERR_UNSUPPORTED;
+  if (block_rows == 128 && (M + 127) / 128 > 65535) return GEMM_ERR_UNSUPPORTED;
   if (M == 0 || K == 0) return GEMM_OK;
   const gemm::QuantArgs a{X, (uint8_t*)Q, S, M, K, ldx, ldq, lds};
   const int t = gemm::store_of(x_type);

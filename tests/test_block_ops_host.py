@@ -112,7 +112,8 @@ def quantize(g, M=8, K=256, X=P, ldx=512, x_type=BF16, act=0, block=1, Q=P, ldq=
     (dict(ldx=248), 1), (dict(ldx=504, act=1), 1), (dict(ldq=240), 1), (dict(lds=7), 1),
     (dict(block=128, lds=1), 1), (dict(X=NUL), 1), (dict(Q=NUL), 1), (dict(S=NUL), 1),
     (dict(X=ctypes.c_void_p(0x10001)), 2), (dict(Q=ODD), 2), (dict(ldq=264), 2),
-    (dict(block=128, act=1), 3), (dict(M=1 << 21, lds=1 << 21), 3)])
+    (dict(block=128, act=1), 3), (dict(M=1 << 31, lds=1 << 31), 3),
+    (dict(block=128, M=8388481), 3)])
 def test_quantize_refusals(g, bad, code):
     assert quantize(g, **bad) == code
 

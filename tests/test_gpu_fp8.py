@@ -280,6 +280,20 @@ def test_quantize_rows_from_any_element(x_type):
     assert torch.equal(a[0][:, :256].float(), b[0][:, :256].float()) and torch.equal(a[1][:2], b[1][:2])
 
 
+def test_quantize_many_rows():
+    """More rows than a grid's second dimension holds workgroups of four."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    x = torch.randn((300001, 130), device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    q, S = g.quantize_fp8(x)
+    at = torch.tensor([0, 5, 262143, 262144, 299999, 300000], device="cuda")
+    r, T = g.quantize_fp8(x[at])
+    assert torch.equal(S[:, at], T)
+    assert torch.equal(q.view(torch.uint8)[at], r.view(torch.uint8))
+
+
 def test_quantize_special_values():
     import torch
 
