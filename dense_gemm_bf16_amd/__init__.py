@@ -388,7 +388,8 @@ def gemm_fp8_config_at(i: int):
 
 
 # The same on torch tensors.  These run on the tensors' device and on torch's
-# current stream there; an output that is not given is allocated on it.
+# current stream there; an output that is not given is allocated on it.  They
+# record no gradients.
 
 _TYPES = {} if torch is None else {
     torch.bfloat16: GEMM_TYPE_BF16, torch.float16: GEMM_TYPE_F16,

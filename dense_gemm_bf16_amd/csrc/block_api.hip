@@ -185,7 +185,7 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   if (!is_float_type(c_type)) return GEMM_ERR_INVALID_ARG;
   const bool scaled = type == GEMM_TYPE_E4M3;
   const int es = element_bytes(type);
-  const int64_t kb = (K + 127) / 128;
+  const int64_t kb = K / 128 + (K % 128 != 0);
   if (lda < K || ldb < K || ldc < N || stride_b < 0 || stride_sb < 0) return GEMM_ERR_INVALID_ARG;
   if (scaled && (ldsa < a_rows || ldsb < kb)) return GEMM_ERR_INVALID_ARG;
   const bool work = R > 0 && N > 0 && E > 0;
@@ -200,6 +200,10 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   const int64_t step = 16 / es - 1;
   if (((lda | ldb | stride_b) & step) != 0 || (ldc & 7) != 0) return GEMM_ERR_MISALIGNED;
 
+  if (R >= k2G || N >= k2G || K >= k2G / 2 || E >= k2G || a_rows >= k2G / 4 || lda >= k2G ||
+      ldb >= k2G)
+    return GEMM_ERR_UNSUPPORTED;
+  if (scaled && kb > kMaxKSteps) return GEMM_ERR_UNSUPPORTED;
   BlockPlan plan{nullptr, nullptr, N};
   if (config && config[0]) {
     plan.shape = block_config(config);
@@ -207,10 +211,6 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
   } else {
     plan = choose_block(type, R, N, K, E, experts, c_type);
   }
-  if (R >= k2G || N >= k2G || K >= k2G / 2 || E >= k2G || a_rows >= k2G / 4 || lda >= k2G ||
-      ldb >= k2G)
-    return GEMM_ERR_UNSUPPORTED;
-  if (scaled && kb > kMaxKSteps) return GEMM_ERR_UNSUPPORTED;
   const BlockConfig* shapes[2] = {plan.shape, plan.tail};
   for (const BlockConfig* c : shapes) {
     if (!c) continue;
@@ -307,7 +307,9 @@ int gemm_moe(int type, int64_t R, int64_t N, int64_t K, int64_t E, int64_t T, co
 }
 
 const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K, int c_type) {
-  if (M < 0 || N < 0 || K < 0 || !gemm::is_float_type(c_type)) return "invalid";
+  if (M < 0 || N < 0 || K < 0 || M >= gemm::k2G || N >= gemm::k2G || K >= gemm::k2G / 2)
+    return "invalid";
+  if (!gemm::is_float_type(c_type)) return "invalid";
   const gemm::BlockPlan p = gemm::choose_block(GEMM_TYPE_E4M3, M, N, K, 1, false, c_type);
   if (!p.tail) return p.shape->name;
   snprintf(gemm::g_plan_name, sizeof gemm::g_plan_name, "%s+%s", p.shape->name, p.tail->name);
@@ -315,7 +317,10 @@ const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K, int c_type) {
 }
 
 const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int64_t E, int c_type) {
-  if (R < 0 || N < 0 || K < 0 || E < 0 || !gemm::is_float_type(c_type)) return "invalid";
+  if (R < 0 || N < 0 || K < 0 || E < 0 || R >= gemm::k2G || N >= gemm::k2G ||
+      K >= gemm::k2G / 2 || E >= gemm::k2G)
+    return "invalid";
+  if (!gemm::is_float_type(c_type)) return "invalid";
   if (type != GEMM_TYPE_E4M3 && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return "invalid";
   return gemm::choose_block(type, R, N, K, E, true, c_type).shape->name;
 }

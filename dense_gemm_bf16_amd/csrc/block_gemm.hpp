@@ -413,8 +413,8 @@ block_tile_kernel(BlockArgs a) {
     // Buffer of row i's A fragment, and the row at whose first MFMA it is
     // read (rows 0 and 1: in the last two rows of the step before; the second
     // half's not before P2): rows FM - 2, FM - 1 and the next step's 0 are
-    // held at once.  Eight rows make
-    // do with three buffers, each reused once its row's MFMAs have issued.
+    // held at once.  Eight rows make do with three buffers, each reused once
+    // its row's MFMAs have issued.
     // (Row 2 not before row 1: until then the last additions of the step
     // before use the scale that its own replaces.)
     constexpr int NBUF = FM == 8 ? 3 : 4;
@@ -552,7 +552,7 @@ block_tile_kernel(BlockArgs a) {
       const int k = step_of(X), k_ahead = step_of(X + S - 1);
       if (k == a.k_steps - 1 && (a.kbytes & 15) != 0) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < L; ++i) trim_one(k, at_slot, i);
       }
       ring_wait_barrier<kInFlight>();

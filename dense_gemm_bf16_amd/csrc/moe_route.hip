@@ -352,15 +352,14 @@ hipError_t route_of(const RouteArgs& a, hipStream_t s) {
   int g2 = 1;
   while (g2 < a.groups) g2 *= 2;
   const int per = 64 / g2, size = a.E / a.groups;
-  const int vpl = (size + per - 1) / per;
+  const int vpl = (size + per - 1) / per;  // at most 32: size <= 1024 / groups, per > 32 / groups
   const dim3 grid((unsigned)((a.T + 3) / 4)), block(256);
   if (vpl <= 1) hipLaunchKernelGGL((route_kernel<TYPE, 1>), grid, block, 0, s, a);
   else if (vpl <= 2) hipLaunchKernelGGL((route_kernel<TYPE, 2>), grid, block, 0, s, a);
   else if (vpl <= 4) hipLaunchKernelGGL((route_kernel<TYPE, 4>), grid, block, 0, s, a);
   else if (vpl <= 8) hipLaunchKernelGGL((route_kernel<TYPE, 8>), grid, block, 0, s, a);
   else if (vpl <= 16) hipLaunchKernelGGL((route_kernel<TYPE, 16>), grid, block, 0, s, a);
-  else if (vpl <= 32) hipLaunchKernelGGL((route_kernel<TYPE, 32>), grid, block, 0, s, a);
-  else return hipErrorInvalidValue;
+  else hipLaunchKernelGGL((route_kernel<TYPE, 32>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
@@ -453,10 +452,9 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
 }
 
 // out[t] = sum over slots j of w[t,j] Y[pos[t,j]], in fp32 in the order of
-// the slots.  Eight columns a thread, Y's rows
-// starting at any element; a slot whose pos lies outside Y
-// (dropped) adds nothing.  Bound by memory: 604 MB (8192 tokens, k = 8, rows
-// of 4096 bf16) in 126 us, 4.8 TB/s.
+// the slots.  Eight columns a thread, Y's rows starting at any element; a slot
+// whose pos lies outside Y (dropped) adds nothing.  Bound by memory: 604 MB
+// (8192 tokens, k = 8, rows of 4096 bf16) in 126 us, 4.8 TB/s.
 typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 typedef _Float16 f16x8u __attribute__((ext_vector_type(8), aligned(2)));
 typedef __bf16 bf16x8u __attribute__((ext_vector_type(8), aligned(2)));
@@ -531,7 +529,6 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
 template <int YT>
 hipError_t combine_of(const CombineArgs& a, int out_type, hipStream_t s) {
   const int64_t blocks = (a.T * ((a.N + 7) / 8) + 255) / 256;
-  if (blocks >= (int64_t(1) << 31)) return hipErrorInvalidValue;
   const dim3 grid((unsigned)blocks), block(256);
   switch (out_type) {
     case kStoreBf16: hipLaunchKernelGGL((combine_kernel<YT, kStoreBf16>), grid, block, 0, s, a); break;

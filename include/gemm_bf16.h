@@ -266,9 +266,9 @@ int gemm_bf16_ex_noalloc(const char* config,
  * type.  For 16-bit C the block's sum is the 8-bit matrix instruction's,
  * which drops what lies below about 2^-17 of the block's largest product
  * (1.5e-5 of C in norm, measured); for fp32 C the codes are widened to bf16
- * first, exactly, and the block's sum is a whole fp32 one, at half the rate.  Scales may be any fp32 value; a NaN code or scale makes
- * the sums it enters NaN.  Elements past K in a row (up to lda) are not used
- * whatever they hold.
+ * first, exactly, and the block's sum is a whole fp32 one, at half the rate.
+ * Scales may be any fp32 value; a NaN code or scale makes the sums it enters
+ * NaN.  Elements past K in a row (up to lda) are not used whatever they hold.
  *
  * Streams and errors as above.  These calls need no workspace: nothing is
  * allocated, calls on different streams may overlap, and all may be
@@ -332,9 +332,9 @@ int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_ty
 #define GEMM_SCORE_SOFTMAX 0
 #define GEMM_SCORE_SIGMOID 1
 
-/* Route T tokens (T < 2^26) over E experts (E <= 1024), k each (k <= 64).  X: T rows of
- * E logits (x_type BF16, F16 or F32, row stride ldx, any alignment of the
- * type).  Per token:
+/* Route T tokens (T < 2^26) over E experts (E <= 1024), k each (k <= 64).
+ * X: T rows of E logits (x_type BF16, F16 or F32, row stride ldx, any
+ * alignment of the type).  Per token:
  *   s = softmax or sigmoid of the logits
  *   c = s + bias            (bias: E fp32 values, or NULL for none)
  *   the experts form `groups` equal groups (<= 64, dividing E); a group's
@@ -397,9 +397,9 @@ const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int6
 /* out[t] = sum over j = 0 .. k-1 of weights[t*k + j] * Y[pos[t*k + j]], fp32
  * sums in that order, rounded once.  Y: R rows of N (y_type), out: T rows of
  * N (out_type; BF16, F16 or F32 each).  Y's rows may start at any element;
- * out is 16-byte aligned with ldo a multiple of 8.  A pos outside 0 .. R-1 adds nothing; a token whose pairs
- * were all dropped gets zeros.  out must not overlap Y.  T * ceil(N / 8) is
- * limited to 2^32 - 256.  Returns a status. */
+ * out is 16-byte aligned with ldo a multiple of 8.  A pos outside 0 .. R-1
+ * adds nothing; a token whose pairs were all dropped gets zeros.  out must not
+ * overlap Y.  T * ceil(N / 8) is limited to 2^32 - 256.  Returns a status. */
 int gemm_moe_combine(int64_t T, int64_t k, int64_t N, int64_t R, const void* Y, int64_t ldy,
                      int y_type, const int32_t* pos, const float* weights, void* out,
                      int64_t ldo, int out_type, void* stream);

@@ -53,6 +53,18 @@ def test_config_names(g):
     assert g.moe_config_name(E4M3, 1, 1, 1, -1) == g.moe_config_name(F32, 1, 1, 1, 1) == "invalid"
 
 
+def test_sizes_past_the_limits_are_refused(g):
+    """Before any of them enters a product that could overflow."""
+    for v in (1 << 31, (1 << 63) - 16):
+        ld = dict(lda=v, ldb=v, ldc=v, ldsa=v, ldsb=v)
+        for M, N, K in ((v, 5, 5), (5, v, 5), (5, 5, v)):
+            assert g.fp8_config_name(M, N, K) == g.moe_config_name(BF16, M, N, K, 4) == "invalid"
+            assert fp8(g, M=M, N=N, K=K, **ld) == 3
+            assert moe(g, type=BF16, R=M, N=N, K=K, T=M, **ld) == 3
+        assert g.moe_config_name(BF16, 5, 5, 5, v) == "invalid"
+        assert moe(g, E=v) == 3
+
+
 def fp8(g, M=8, N=8, K=256, A=P, lda=256, SA=P, ldsa=8, B=P, ldb=256, SB=P, ldsb=2, C=P, ldc=8,
         c_type=BF16, config=None):
     return g._lib.gemm_fp8_ex(config, M, N, K, A, lda, SA, ldsa, B, ldb, SB, ldsb, C, ldc, c_type,
