@@ -162,41 +162,72 @@ __device__ __forceinline__ bool group_stays(const RouteArgs& a, const Lane& l, F
 }
 
 // Rounds of the largest key among the wave's lanes.  WIDE: 64-bit keys, else
-// only the high words.  Returns false (fp32 keys, CHECK) if two neighbours
-// in the order are closer than their bound.
+// only the high words.  Up to kSortedVpl keys a lane are sorted first, so that
+// a round looks at each lane's first one only and a taken key moves the rest
+// up; more are searched again each round (sorting 16 and moving them costs as
+// much).  Returns false (fp32 keys, CHECK) if two neighbours in the order are
+// closer than their bound.
+constexpr int kSortedVpl = 8;
 template <int VPL, bool WIDE, bool CHECK>
 __device__ __forceinline__ bool choose(const RouteArgs& a, const Lane& l, uint32_t (&hi)[VPL],
                                        uint32_t (&lo)[VPL], int& my_id) {
-  auto local = [&](uint32_t& bh, uint32_t& bl, int& be) __attribute__((always_inline)) {
-    bh = hi[0];
-    bl = WIDE ? lo[0] : 0;
-    be = l.expert(0);
+  constexpr bool kSorted = VPL <= kSortedVpl;
+  int id[VPL];  // (of sorted keys)
+  if constexpr (kSorted) {
 #pragma unroll
-    for (int j = 1; j < VPL; ++j) {
-      const bool more = hi[j] > bh || (WIDE && hi[j] == bh && lo[j] > bl);
-      bh = more ? hi[j] : bh;
-      if constexpr (WIDE) bl = more ? lo[j] : bl;
-      be = more ? l.expert(j) : be;
-    }
-  };
-  uint32_t bh, bl;
-  int be;
-  local(bh, bl, be);
-  float before = 0.0f;
+    for (int j = 0; j < VPL; ++j) id[j] = l.expert(j);
+    // Batcher's odd-even merges; equal keys by lowest expert
+#pragma unroll
+    for (int p = 1; p < VPL; p *= 2)
+#pragma unroll
+      for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+        for (int j = q % p; j + q < VPL; j += 2 * q)
+#pragma unroll
+          for (int i = 0; i < q; ++i) {
+            const int x = i + j, y = i + j + q;
+            if (y >= VPL || x / (2 * p) != y / (2 * p)) continue;
+            bool swap;
+            if constexpr (WIDE)
+              swap = hi[y] > hi[x] || (hi[y] == hi[x] && (lo[y] > lo[x] || (lo[y] == lo[x] && id[y] < id[x])));
+            else
+              swap = ((uint64_t)hi[y] << 32 | ~(uint32_t)id[y]) > ((uint64_t)hi[x] << 32 | ~(uint32_t)id[x]);
+            const uint32_t h = hi[x];
+            hi[x] = swap ? hi[y] : h;
+            hi[y] = swap ? h : hi[y];
+            const int e = id[x];
+            id[x] = swap ? id[y] : e;
+            id[y] = swap ? e : id[y];
+            if constexpr (WIDE) {
+              const uint32_t w = lo[x];
+              lo[x] = swap ? lo[y] : w;
+              lo[y] = swap ? w : lo[y];
+            }
+          }
+  }
+  uint32_t my_key = 0, last = 0;
   const int rounds = CHECK ? a.k + 1 : a.k;
   for (int r = 0; r < rounds; ++r) {
+    uint32_t bh = hi[0], bl = WIDE ? lo[0] : 0;
+    int be = kSorted ? id[0] : l.expert(0);
+    if constexpr (!kSorted) {
+#pragma unroll
+      for (int j = 1; j < VPL; ++j) {
+        const bool more = hi[j] > bh || (WIDE && hi[j] == bh && lo[j] > bl);
+        bh = more ? hi[j] : bh;
+        if constexpr (WIDE) bl = more ? lo[j] : bl;
+        be = more ? l.expert(j) : be;
+      }
+    }
     const uint32_t mh = wave_max(bh);
+    if (CHECK && r == a.k) {
+      last = mh;
+      break;
+    }
     uint64_t tied = __ballot(bh == mh);
     if constexpr (WIDE) {
       const uint32_t ml = wave_max(bh == mh ? bl : 0u);
       tied = __ballot(bh == mh && bl == ml);
-    }
-    if constexpr (CHECK) {
-      if (mh == 0) return true;  // every candidate is taken
-      const float c = of_key(mh);
-      if (r > 0 && !(before - c > choice_bound(before))) return false;
-      before = c;
-      if (r == a.k) return true;
     }
     int w = __builtin_ctzll(tied);
     if ((tied & (tied - 1)) != 0) {  // equal values: the lowest expert
@@ -204,15 +235,30 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Lane& l, uint32
       const uint32_t least = ~wave_max(in ? ~(uint32_t)be : 0u);
       w = __builtin_ctzll(__ballot(in && (uint32_t)be == least));
     }
-    const int id = __builtin_amdgcn_readlane(be, w);
-    if (l.lane == r) my_id = id;
+    const int taken = __builtin_amdgcn_readlane(be, w);
+    if (l.lane == r) {
+      my_id = taken;
+      my_key = mh;
+    }
+    const bool mine = l.lane == w;
 #pragma unroll
-    for (int j = 0; j < VPL; ++j)
-      if (l.lane == w && l.expert(j) == id) {
+    for (int j = 0; j < VPL; ++j) {
+      if constexpr (kSorted) {
+        hi[j] = mine ? (j + 1 < VPL ? hi[j + 1 < VPL ? j + 1 : j] : 0u) : hi[j];
+        id[j] = mine && j + 1 < VPL ? id[j + 1 < VPL ? j + 1 : j] : id[j];
+        if constexpr (WIDE) lo[j] = mine ? (j + 1 < VPL ? lo[j + 1 < VPL ? j + 1 : j] : 0u) : lo[j];
+      } else if (mine && l.expert(j) == taken) {
         hi[j] = 0;
         if constexpr (WIDE) lo[j] = 0;
       }
-    local(bh, bl, be);
+    }
+  }
+  if constexpr (CHECK) {
+    // all neighbours at once; key 0: every candidate is taken
+    const uint32_t below = __shfl_down(my_key, 1, 64);
+    const uint32_t next = l.lane == a.k - 1 ? last : below;
+    const float c = of_key(my_key);
+    return !__any(l.lane < a.k && next != 0 && !(c - of_key(next) > choice_bound(c)));
   }
   return true;
 }
