@@ -377,7 +377,8 @@ int gemm_moe_route(int64_t T, int64_t E, int64_t k, const void* X, int64_t ldx, 
   if (T == 0) return GEMM_OK;
   const gemm::RouteArgs a{X,        bias,     ids,      weights,          T,
                           ldx,      (int)E,   (int)k,   (int)groups,      (int)topk_groups,
-                          group_top, score == GEMM_SCORE_SIGMOID, renorm != 0, scale};
+                          group_top, score == GEMM_SCORE_SIGMOID, renorm != 0, scale,
+                          (int)(E / groups), 1.0f / (float)(E / groups)};
   const hipError_t e = gemm::launch_route(a, gemm::store_of(x_type), (hipStream_t)stream);
   return e == hipSuccess ? GEMM_OK : gemm::hip_fail(e);
 }

@@ -30,6 +30,8 @@ struct RouteArgs {
   int E, k, groups, topk_groups, group_top;
   bool sigmoid, renorm;
   float scale;
+  int size;        // experts of a group
+  float inv_size;  // 1 / size
 };
 hipError_t launch_route(const RouteArgs& a, int x_type, hipStream_t s);
 

@@ -149,9 +149,11 @@ __device__ __forceinline__ bool group_stays(const RouteArgs& a, const Lane& l, F
   F next = -INFINITY;  // the largest score of a group ranked below this one
   for (int o = 0; o < a.groups; ++o) {
     const F v = of_lane(g, o * l.per);
-    const bool above = o != l.group && (v > g || (v == g && o < l.group));
+    // (& and |: no branches)
+    const bool above = (v > g) | ((v == g) & (o < l.group));
     rank += above ? 1 : 0;
-    if (!above && o != l.group && v > next) next = v;
+    const bool below = !above & (o != l.group) & (v > next);
+    next = below ? v : next;
   }
   const bool stays = l.group < a.groups && rank < a.topk_groups;
   if constexpr (sizeof(F) == 4) {
@@ -276,11 +278,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
   if (t >= a.T) return;
   Lane l;
   l.lane = threadIdx.x & 63;
-  const int g2 = a.groups <= 1 ? 1 : 1 << (32 - __builtin_clz(a.groups - 1));
-  l.per = 64 / g2;
-  l.group = l.lane / l.per;
-  l.sub = l.lane - l.group * l.per;
-  l.size = a.E / a.groups;
+  const int log_per = a.groups <= 1 ? 6 : 6 - (32 - __builtin_clz(a.groups - 1));
+  l.per = 1 << log_per;
+  l.group = l.lane >> log_per;
+  l.sub = l.lane & (l.per - 1);
+  l.size = a.size;
 
   // All loads go out before the first is used (places past the group read
   // expert 0 and are set aside).
@@ -379,9 +381,11 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 
   float w = 0.0f;
   if (l.lane < a.k) {  // my_id's place: its group's lanes, dealt in turn
-    const int group = my_id / l.size, in = my_id - group * l.size;
-    const int j = in / l.per;
-    w = score(logits[threadIdx.x >> 6][j * 64 + group * l.per + (in - j * l.per)]);
+    // (my_id / size: the product is off by less than 2^-13 / size, and the
+    // quotient at least 1 / (2 size) from a whole number)
+    const int group = (int)(((float)my_id + 0.5f) * a.inv_size), in = my_id - group * l.size;
+    const int j = in >> log_per;
+    w = score(logits[threadIdx.x >> 6][j * 64 + group * l.per + (in & (l.per - 1))]);
   }
   if (a.renorm) {
     const float sum = wave_sum(w);
@@ -397,7 +401,7 @@ template <int TYPE>
 hipError_t route_of(const RouteArgs& a, hipStream_t s) {
   int g2 = 1;
   while (g2 < a.groups) g2 *= 2;
-  const int per = 64 / g2, size = a.E / a.groups;
+  const int per = 64 / g2, size = a.size;
   const int vpl = (size + per - 1) / per;  // at most 32: size <= 1024 / groups, per > 32 / groups
   const dim3 grid((unsigned)((a.T + 3) / 4)), block(256);
   if (vpl <= 1) hipLaunchKernelGGL((route_kernel<TYPE, 1>), grid, block, 0, s, a);
