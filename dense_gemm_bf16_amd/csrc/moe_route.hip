@@ -18,9 +18,10 @@
 // One wave per token.  A group's experts are dealt over 64 / (groups rounded
 // up to a power of two) neighbouring lanes, so a group's best two and its
 // score stay within those lanes, and the k rounds of a maximum over the wave
-// cost six DPP steps each.  Bound by instructions (about 85 a round): 18 us
-// for 8192 tokens of 256 experts, k = 8, against 2 us for the bytes; a wave
-// by itself takes 4 us.
+// cost six DPP steps each.  Bound by instructions (about 35 a round, and as
+// many again for the scores, the groups and the weights): 15 us for 8192
+// tokens of 256 experts, k = 8, against 2 us for the bytes; a wave by itself
+// takes 4 us.
 #include "block_internal.h"
 
 namespace gemm {
@@ -441,7 +442,9 @@ struct Divide {
 // pass, in the second a comparison and a branch past the vectors without a
 // match; a product and a shift in place of the division by k (10 us at 65536
 // ids and 256 experts, launched back to back; 41 us with checked loads,
-// ballots in both passes and a division).  kBatch loads wait together.
+// ballots in both passes and a division).  Sixteen loads wait together, the
+// last few in fours (12800 ids: 5.1 us, 7.6 one by one).  Four ids a lane and
+// load: no faster.
 template <int W>
 __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict__ ids, int R,
                                                       Divide by_k, int E,
@@ -449,7 +452,6 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
                                                       int32_t* __restrict__ rows,
                                                       int32_t* __restrict__ pos) {
   __shared__ int below_of[W], own_of[W];
-  constexpr int kBatch = 16;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t e = blockIdx.x;
@@ -461,13 +463,18 @@ __global__ __launch_bounds__(W * 64) void plan_kernel(const int32_t* __restrict_
   // use(first slot, ids, lanes that hold one) for each 64 ids of the part
   auto each = [&](auto&& use) __attribute__((always_inline)) {
     int i = begin;
-    for (; i + kBatch * 64 <= end; i += kBatch * 64) {
-      uint32_t id[kBatch];
+    auto batches = [&](auto bc) __attribute__((always_inline)) {
+      constexpr int B = decltype(bc)::value;
+      for (; i + B * 64 <= end; i += B * 64) {
+        uint32_t id[B];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) id[b] = (uint32_t)ids[i + b * 64 + lane];
+        for (int b = 0; b < B; ++b) id[b] = (uint32_t)ids[i + b * 64 + lane];
 #pragma unroll
-      for (int b = 0; b < kBatch; ++b) use(i + b * 64, id[b], true);
-    }
+        for (int b = 0; b < B; ++b) use(i + b * 64, id[b], true);
+      }
+    };
+    batches(std::integral_constant<int, 16>{});
+    batches(std::integral_constant<int, 4>{});
     for (; i < end; i += 64) use(i, (uint32_t)ids[min(i + lane, end - 1)], i + lane < end);
   };
   int below = 0, own = 0;
