@@ -95,6 +95,39 @@ def test_route_order_is_finer_than_fp32():
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E, groups, topk", [(100, 1, 1), (240, 1, 1), (240, 4, 3), (480, 1, 1),
+                                             (480, 32, 9), (1000, 1, 1)])
+def test_route_many_near_and_equal_scores(E, groups, topk, score):
+    """One to sixteen experts a lane whose scores agree to fp32's last bits,
+    or whole."""
+    import torch
+
+    rng = np.random.default_rng(E + groups)
+    x = torch.from_numpy(rng.normal(0, 1, E)).float()
+    e = np.exp(x.double().numpy())
+    s = e / e.sum() if score == "softmax" else e / (1 + e)
+    rows = x + torch.from_numpy(rng.choice([0, 1e-7, -1e-7], (60, E))).float()
+    check_route(rows, 24, (0.75 - s).astype(np.float32), score=score, groups=groups,
+                topk_groups=topk)
+    equal = torch.from_numpy(rng.integers(0, 2, (60, E)).astype(np.float32))
+    for bias in (None, np.zeros(E), rng.integers(0, 2, E) * 0.5):
+        check_route(equal, 24, bias, score=score, groups=groups, topk_groups=topk)
+
+
+@pytest.mark.parametrize("T, k, E", [(125, 8, 256), (300, 4, 16), (1100, 8, 5), (1600, 8, 40),
+                                     (2049, 8, 9), (5000, 5, 12)])
+def test_plan_parts_that_end_anywhere(T, k, E):
+    """Parts of every length past whole batches of loads."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    ids = np.random.default_rng(T).integers(-1, E + 1, (T, k)).astype(np.int32)
+    for a, b in zip(g.moe_plan(torch.from_numpy(ids).cuda(), E), ref.plan(ids, E)):
+        assert np.array_equal(a.cpu().numpy(), b)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_route_special_logits(score):
     import torch
 
