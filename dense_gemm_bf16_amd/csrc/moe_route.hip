@@ -167,8 +167,9 @@ __device__ __forceinline__ bool group_stays(const RouteArgs& a, const Lane& l, F
 // Rounds of the largest key among the wave's lanes.  WIDE: 64-bit keys, else
 // only the high words.  Up to kSortedVpl keys a lane are sorted first, so that
 // a round looks at each lane's first one only and a taken key moves the rest
-// up; more are searched again each round (sorting 16 and moving them costs as
-// much).  Returns false (fp32 keys, CHECK) if two neighbours in the order are
+// up; more are searched again each round (k = 8, 8192 tokens, sorted against
+// searched: 10.7 and 12.4 us at 256 experts, 4 a lane; 18.5 and 19.9 at 512;
+// 39.4 and 34.6 at 1024, 16 a lane).  Returns false (fp32 keys, CHECK) if two neighbours in the order are
 // closer than their bound.
 constexpr int kSortedVpl = 8;
 template <int VPL, bool WIDE, bool CHECK>
