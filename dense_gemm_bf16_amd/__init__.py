@@ -516,8 +516,8 @@ def moe_route(logits, k, bias=None, score="softmax", groups=1, topk_groups=None,
     (ids, weights), T x k each, int32 and float32.
 
     score "softmax" or "sigmoid"; bias (E, float32) is added to the scores for
-    the choice only; of `groups` equal groups of experts the topk_groups best
-    stay, by the sum of their group_top (1 or 2) best; weights are the scores
+    the choice only; a logit of -inf (or NaN) masks its expert, whatever its
+    bias; of `groups` equal groups of experts the topk_groups best stay, by the sum of their group_top (1 or 2) best; weights are the scores
     of the chosen, divided by their sum if renormalize, times scale.  Ties go
     to the lowest index."""
     _need(logits, "logits")

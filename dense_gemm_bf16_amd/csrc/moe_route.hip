@@ -3,7 +3,8 @@
 //
 // Routing, per token with logits x:
 //   s  = softmax(x) or sigmoid(x)
-//   c  = s + bias                      (the order of choice)
+//   c  = s + bias                      (the order of choice; -infinity for a
+//                                       masked expert, whatever its bias)
 //   a group's score = its largest c, or the sum of its two largest; the
 //   topk_groups best groups stay
 //   ids = the k largest c of those groups, equal values by lowest index
@@ -145,7 +146,8 @@ __device__ __forceinline__ bool group_stays(const RouteArgs& a, const Lane& l, F
     second = second < s ? s : second;
     second = second < low ? low : second;
   });
-  const F g = a.group_top == 2 && l.size > 1 ? best + second : best;
+  // (a second one that is masked, or not there, does not count)
+  const F g = a.group_top == 2 && second > -INFINITY ? best + second : best;
   int rank = 0;
   F next = -INFINITY;  // the largest score of a group ranked below this one
   for (int o = 0; o < a.groups; ++o) {
@@ -337,7 +339,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       c[j] = by_logit ? x[j] : score(x[j]) + b[j];
-      if (!l.has(j, a.groups)) c[j] = -INFINITY;
+      if (x[j] == -INFINITY) c[j] = -INFINITY;  // masked, whatever its bias, or no expert here
       second = fmaxf(second, fminf(best, c[j]));
       best = fmaxf(best, c[j]);
     }
@@ -366,7 +368,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     for (int j = 0; j < VPL; ++j) {
       c[j] = (a.sigmoid ? 1.0 / (1.0 + exp(-(double)x[j])) : exp((double)x[j] - (double)m) / zz) +
              (double)b[j];
-      if (!l.has(j, a.groups)) c[j] = -INFINITY;
+      if (x[j] == -INFINITY) c[j] = -INFINITY;
       second = fmax(second, fmin(best, c[j]));
       best = fmax(best, c[j]);
     }

@@ -336,19 +336,22 @@ int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_ty
  * X: T rows of E logits (x_type BF16, F16 or F32, row stride ldx, any
  * alignment of the type).  Per token:
  *   s = softmax or sigmoid of the logits
- *   c = s + bias            (bias: E fp32 values, or NULL for none)
+ *   c = s + bias            (bias: E fp32 values, or NULL for none); an
+ *                           expert whose logit is -infinity is masked: its
+ *                           c is -infinity whatever its bias
  *   the experts form `groups` equal groups (<= 64, dividing E); a group's
  *   score is its largest c (group_top 1) or the sum of its two largest
- *   (group_top 2); only the topk_groups best groups stay
+ *   (group_top 2; of the one that is not masked where there is but one, and
+ *   -infinity where all are); only the topk_groups best groups stay
  *   ids = the k largest c that stay, in descending order
  *   weights = s[ids], divided by their sum if renorm != 0, times scale
  * ids (T x k int32) and weights (T x k fp32) are contiguous.  The order is
  * that of the exact values, ties by lowest index (of groups too): it does
  * not depend on rounding in the scores.  A NaN logit counts as -infinity, a
- * logit of +infinity as the largest finite number; masked (-infinity)
- * experts have score 0 and are taken, at weight 0, only when the others run
- * out; weights that sum to 0 are all 0.  k may not exceed the experts of
- * topk_groups groups.  Returns a status. */
+ * logit of +infinity as the largest finite number, and so do those of the
+ * bias; masked experts have score 0 and are taken, at weight 0, only when
+ * the others of the groups that stay run out; weights that sum to 0 are all
+ * 0.  k may not exceed the experts of topk_groups groups.  Returns a status. */
 int gemm_moe_route(int64_t T, int64_t E, int64_t k, const void* X, int64_t ldx, int x_type,
                    const float* bias, int score, int64_t groups, int64_t topk_groups,
                    int group_top, int renorm, float scale, int32_t* ids, float* weights,

@@ -88,12 +88,14 @@ def route(x, k, bias=None, score="softmax", groups=1, topk_groups=None, group_to
     c = s if bias is None else s + bias.astype(np.float64)
     if bias is None and (groups == 1 or group_top == 1):
         c = x
+    c = np.where(np.isneginf(x), -np.inf, c)  # masked, whatever the bias
     topk_groups = groups if topk_groups is None else topk_groups
     ids = np.zeros((T, k), np.int64)
     size = E // groups
     for t in range(T):
         by = c[t].reshape(groups, size)
-        best = -np.sort(-by, 1)[:, :group_top].sum(1)
+        top = -np.sort(-by, 1)[:, :group_top]
+        best = np.where(np.isneginf(top[:, 0]), -np.inf, np.where(np.isneginf(top), 0, top).sum(1))
         kept = np.argsort(-best, kind="stable")[:topk_groups]
         candidates = np.sort((kept[:, None] * size + np.arange(size)).reshape(-1))
         ids[t] = candidates[np.argsort(-c[t][candidates], kind="stable")[:k]]

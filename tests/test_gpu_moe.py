@@ -168,6 +168,57 @@ def test_route_bias_extremes_and_strides():
     assert np.array_equal(got.cpu().numpy(), ref.route(wide[:, 3:].float().numpy(), 4)[0])
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("mask", [-np.inf, np.nan])
+def test_masked_experts_come_last_whatever_their_bias(mask, score):
+    import torch
+
+    x = torch.full((1, 16), -0.5)
+    x[0, 3] = mask
+    bias = np.where(np.arange(16) == 3, 0.5, 0.0)
+    ids, w = run_route(x, 2, bias, score=score)
+    assert ids.tolist() == [[0, 1]] and np.abs(w - 0.5).max() <= 2.0 ** -17
+    # every count of experts left, in each group and over all of them
+    E = 48
+    rng = np.random.default_rng(7)
+    x = torch.from_numpy(rng.normal(0, 1.5, (E + 1, E))).float()
+    for t in range(E + 1):
+        x[t, torch.from_numpy(rng.permutation(E)[t:])] = mask
+    left = x.numpy() > -np.inf  # (NaN: false)
+    for bias in (np.where(left[20], -0.4, 0.6), rng.normal(0, 0.5, E)):
+        for groups, topk in ((1, 1), (4, 2), (16, 5), (48, 10)):
+            for top in (1, 2):
+                kw = dict(score=score, groups=groups, topk_groups=topk, group_top=top)
+                check_route(x, 6, bias, **kw)
+                check_route(x, 6, None, **kw)
+                ids, w = run_route(x, 6, bias, **kw)
+                taken = np.take_along_axis(left, ids.astype(np.int64), 1)
+                assert (w[~taken] == 0).all() and (w[taken] > 0).all()
+                # those that are left first, and all of them where the groups do not choose
+                assert (np.sort(~taken, 1) == ~taken).all()
+                if topk == groups:
+                    assert (taken.sum(1) == np.minimum(6, left.sum(1))).all()
+                # a group with one comes before the groups without
+                assert (taken[:, 0] == left.any(1)).all()
+
+
+def test_a_masked_experts_row_does_not_reach_the_token():
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    logits = torch.zeros(3, 8, device="cuda")
+    logits[:, 5] = float("-inf")
+    bias = torch.zeros(8, device="cuda")
+    bias[5] = 1.0
+    ids, w = g.moe_route(logits, 2, bias=bias)
+    offsets, rows, pos = g.moe_plan(ids, 8)
+    B = torch.ones(8, 16, 64, device="cuda", dtype=torch.bfloat16)
+    B[5] = float("nan")
+    y = g.moe_matmul(torch.ones(3, 64, device="cuda", dtype=torch.bfloat16), B, offsets, rows=rows)
+    assert bool((g.moe_combine(y, pos, w) == 64).all())
+
+
 # ------------------------------------------------------------------ plan
 
 @pytest.mark.parametrize("T, k, E", [(0, 2, 4), (1, 1, 1), (1, 8, 256), (5, 3, 7), (64, 8, 128),
