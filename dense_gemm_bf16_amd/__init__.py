@@ -517,9 +517,10 @@ def moe_route(logits, k, bias=None, score="softmax", groups=1, topk_groups=None,
 
     score "softmax" or "sigmoid"; bias (E, float32) is added to the scores for
     the choice only; a logit of -inf (or NaN) masks its expert, whatever its
-    bias; of `groups` equal groups of experts the topk_groups best stay, by the sum of their group_top (1 or 2) best; weights are the scores
-    of the chosen, divided by their sum if renormalize, times scale.  Ties go
-    to the lowest index."""
+    bias; of `groups` equal groups of experts the topk_groups best stay, by
+    the sum of their group_top (1 or 2) best; weights are the scores of the
+    chosen, divided by their sum if renormalize, times scale.  Scores that are
+    equal in 64 bits go by logit, equal logits to the lowest index."""
     _need(logits, "logits")
     if logits.dim() != 2:
         raise ValueError("logits must have two dimensions")

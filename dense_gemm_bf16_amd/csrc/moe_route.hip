@@ -10,11 +10,16 @@
 //   ids = the k largest c of those groups, equal values by lowest index
 //   w  = s[ids], divided by their sum if renorm, times scale
 //
-// The order of choice is that of the exact values.  Without a bias it is the
+// Without a bias (and by a group's largest c) the order of choice is the
 // order of the logits (both scores grow with x), which needs no arithmetic.
-// With one, c is computed in fp32 with a bound on its error; where two
-// neighbours that matter lie closer than the bound (a fraction of a percent
-// of the rows of ordinary logits), the wave decides its row again in fp64.
+// Otherwise it is that of c in fp64: c is computed in fp32 with a bound on
+// its error, and where two neighbours that matter lie closer than the bound
+// (a fraction of a percent of the rows of ordinary logits), the wave decides
+// its row again in fp64.  What is equal there too (sigmoids of 40 and 50 are
+// both 1) goes by the logits, and only then by index.  c in fp64 never falls
+// as x grows (exp, the sums and the quotient round the same way for every
+// expert), so experts of equal bias always stand in the order of their
+// logits, and a bias of zeros leaves every choice as it was without one.
 //
 // One wave per token.  A group's experts are dealt over 64 / (groups rounded
 // up to a power of two) neighbouring lanes, so a group's best two and its
@@ -115,6 +120,7 @@ __device__ __forceinline__ float group_bound(float g) { return 0x1p-16f + 0x1p-2
 struct Lane {
   int lane, group, sub, per;  // per: lanes of a group; sub: this lane's place among them
   int size;                   // experts of a group
+  int log_per;                // per = 1 << log_per
   __device__ __forceinline__ bool has(int j, int groups) const {
     return group < groups && sub + j * per < size;
   }
@@ -133,14 +139,20 @@ __device__ __forceinline__ double of_lane(double v, int n) {
 }
 
 // Whether this lane's group is among the best topk_groups.  F: float or
-// double.  `near` is set where fp32 cannot tell.
+// double.  `near` is set where fp32 cannot tell; in fp64 equal scores go by
+// `top`, the logit of the group's best expert, then by index.
 template <typename F>
 __device__ __forceinline__ bool group_stays(const RouteArgs& a, const Lane& l, F best, F second,
-                                            bool& near) {
+                                            float top, bool& near) {
+  constexpr bool kTop = sizeof(F) == 8;
   // the two largest over the group's lanes
   butterfly(l.per, [&](auto dc) __attribute__((always_inline)) {
     constexpr int D = decltype(dc)::value;
     const F b = across<D>(best), s = across<D>(second);
+    if constexpr (kTop) {
+      const float t = across<D>(top);
+      top = (b > best) | ((b == best) & (t > top)) ? t : top;
+    }
     const F low = best < b ? best : b;
     best = best < b ? b : best;
     second = second < s ? s : second;
@@ -153,7 +165,12 @@ __device__ __forceinline__ bool group_stays(const RouteArgs& a, const Lane& l, F
   for (int o = 0; o < a.groups; ++o) {
     const F v = of_lane(g, o * l.per);
     // (& and |: no branches)
-    const bool above = (v > g) | ((v == g) & (o < l.group));
+    bool first = o < l.group;
+    if constexpr (kTop) {
+      const float t = of_lane(top, o * l.per);
+      first = (t > top) | ((t == top) & first);
+    }
+    const bool above = (v > g) | ((v == g) & first);
     rank += above ? 1 : 0;
     const bool below = !above & (o != l.group) & (v > next);
     next = below ? v : next;
@@ -166,18 +183,24 @@ __device__ __forceinline__ bool group_stays(const RouteArgs& a, const Lane& l, F
   return stays;
 }
 
-// Rounds of the largest key among the wave's lanes.  WIDE: 64-bit keys, else
-// only the high words.  Up to kSortedVpl keys a lane are sorted first, so that
-// a round looks at each lane's first one only and a taken key moves the rest
-// up; more are searched again each round (k = 8, 8192 tokens, sorted against
-// searched: 10.7 and 12.4 us at 256 experts, 4 a lane; 18.5 and 19.9 at 512;
-// 39.4 and 34.6 at 1024, 16 a lane).  Returns false (fp32 keys, CHECK) if two neighbours in the order are
-// closer than their bound.
+// Rounds of the largest key among the wave's lanes.  WIDE: 64-bit keys, equal
+// ones by logit (this lane's j-th at own[j * 64], read only where keys are
+// equal), else only the high words.  Up to kSortedVpl keys a lane are sorted
+// first, so that a round looks at each lane's first one only and a taken key
+// moves the rest up; more are searched again each round (k = 8, 8192 tokens,
+// sorted against searched: 10.7 and 12.4 us at 256 experts, 4 a lane; 18.5 and
+// 19.9 at 512; 39.4 and 34.6 at 1024, 16 a lane).  Returns false (fp32 keys,
+// CHECK) if two neighbours in the order are closer than their bound.
 constexpr int kSortedVpl = 8;
 template <int VPL, bool WIDE, bool CHECK>
 __device__ __forceinline__ bool choose(const RouteArgs& a, const Lane& l, uint32_t (&hi)[VPL],
-                                       uint32_t (&lo)[VPL], int& my_id) {
+                                       uint32_t (&lo)[VPL], const float* own, int& my_id) {
   constexpr bool kSorted = VPL <= kSortedVpl;
+  // in the order of this lane's experts of equal key
+  auto tie = [&](int id) __attribute__((always_inline)) {
+    const uint32_t logit = key_of(own[((id - l.expert(0)) >> l.log_per) * 64]);
+    return (uint64_t)logit << 32 | ~(uint32_t)id;
+  };
   int id[VPL];  // (of sorted keys)
   if constexpr (kSorted) {
 #pragma unroll
@@ -194,10 +217,13 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Lane& l, uint32
             const int x = i + j, y = i + j + q;
             if (y >= VPL || x / (2 * p) != y / (2 * p)) continue;
             bool swap;
-            if constexpr (WIDE)
-              swap = hi[y] > hi[x] || (hi[y] == hi[x] && (lo[y] > lo[x] || (lo[y] == lo[x] && id[y] < id[x])));
-            else
-              swap = ((uint64_t)hi[y] << 32 | ~(uint32_t)id[y]) > ((uint64_t)hi[x] << 32 | ~(uint32_t)id[x]);
+            if constexpr (WIDE) {
+              swap = hi[y] > hi[x] || (hi[y] == hi[x] && lo[y] > lo[x]);
+              if (hi[y] == hi[x] && lo[y] == lo[x] && hi[x] != 0) swap = tie(id[y]) > tie(id[x]);
+            } else {
+              swap = ((uint64_t)hi[y] << 32 | ~(uint32_t)id[y]) >
+                     ((uint64_t)hi[x] << 32 | ~(uint32_t)id[x]);
+            }
             const uint32_t h = hi[x];
             hi[x] = swap ? hi[y] : h;
             hi[y] = swap ? h : hi[y];
@@ -233,7 +259,27 @@ __device__ __forceinline__ bool choose(const RouteArgs& a, const Lane& l, uint32
     uint64_t tied = __ballot(bh == mh);
     if constexpr (WIDE) {
       const uint32_t ml = wave_max(bh == mh ? bl : 0u);
-      tied = __ballot(bh == mh && bl == ml);
+      const bool in = bh == mh && bl == ml;
+      tied = __ballot(in);
+      uint64_t once = 0, twice = 0;  // lanes that have the high word so often
+      if constexpr (!kSorted) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+          const uint64_t has = __ballot(hi[j] == mh);
+          twice |= once & has;
+          once |= has;
+        }
+      }
+      if ((tied & (tied - 1)) != 0 || twice != 0) {  // equal values: the largest logit
+        if constexpr (!kSorted) {
+#pragma unroll
+          for (int j = 0; j < VPL; ++j)
+            if (in && hi[j] == mh && lo[j] == ml && tie(l.expert(j)) > tie(be)) be = l.expert(j);
+        }
+        const uint32_t bt = in ? (uint32_t)(tie(be) >> 32) : 0u;
+        const uint32_t mt = wave_max(bt);  // (with all lanes active)
+        tied = __ballot(in && bt == mt);
+      }
     }
     int w = __builtin_ctzll(tied);
     if ((tied & (tied - 1)) != 0) {  // equal values: the lowest expert
@@ -275,16 +321,23 @@ __device__ __forceinline__ F wave_sum(F v) {
   return v;
 }
 
+// Waves of a SIMD that the registers have to leave room for (8192 tokens of
+// 1024 experts, 16 a lane: 37 us with four, 41 with the three that the
+// compiler leaves by itself for one register more).
+constexpr int route_waves(int vpl) { return vpl <= 4 ? 8 : vpl <= 8 ? 6 : vpl <= 16 ? 4 : 2; }
+
 template <int TYPE, int VPL>
-__global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256),
+                          amdgpu_waves_per_eu(route_waves(VPL)))) void
+route_kernel(RouteArgs a) {
   __shared__ float logits[4][VPL * 64];  // a wave's own, by place: lane and j
   const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (t >= a.T) return;
   Lane l;
   l.lane = threadIdx.x & 63;
-  const int log_per = a.groups <= 1 ? 6 : 6 - (32 - __builtin_clz(a.groups - 1));
-  l.per = 1 << log_per;
-  l.group = l.lane >> log_per;
+  l.log_per = a.groups <= 1 ? 6 : 6 - (32 - __builtin_clz(a.groups - 1));
+  l.per = 1 << l.log_per;
+  l.group = l.lane >> l.log_per;
   l.sub = l.lane & (l.per - 1);
   l.size = a.size;
 
@@ -331,6 +384,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
 
   const bool by_logit = !a.bias && (a.groups == 1 || a.group_top == 1);
   uint32_t hi[VPL], lo[VPL];
+  const float* const own = &logits[threadIdx.x >> 6][l.lane];
   int my_id = 0;
   bool done;
   {
@@ -344,19 +398,20 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       best = fmaxf(best, c[j]);
     }
     bool stays = true, near = false;
-    if (a.topk_groups < a.groups) stays = group_stays<float>(a, l, best, second, near);
+    if (a.topk_groups < a.groups) stays = group_stays<float>(a, l, best, second, 0.0f, near);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) hi[j] = stays && l.has(j, a.groups) ? key_of(c[j]) : 0u;
     if (by_logit) {
       // (a tie between groups is one between logits: the lowest index)
-      done = choose<VPL, false, false>(a, l, hi, lo, my_id);
+      done = choose<VPL, false, false>(a, l, hi, lo, own, my_id);
     } else {
-      done = !near && choose<VPL, false, true>(a, l, hi, lo, my_id);
+      done = !near && choose<VPL, false, true>(a, l, hi, lo, own, my_id);
     }
   }
   if (!done) {
     double c[VPL];
     double best = -INFINITY, second = -INFINITY, zz = 1.0;
+    float top = -INFINITY;  // the logit of the best
     if (!a.sigmoid) {
       zz = 0.0;
 #pragma unroll
@@ -369,18 +424,19 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
       c[j] = (a.sigmoid ? 1.0 / (1.0 + exp(-(double)x[j])) : exp((double)x[j] - (double)m) / zz) +
              (double)b[j];
       if (x[j] == -INFINITY) c[j] = -INFINITY;
+      top = (c[j] > best) | ((c[j] == best) & (x[j] > top)) ? x[j] : top;
       second = fmax(second, fmin(best, c[j]));
       best = fmax(best, c[j]);
     }
     bool stays = true, near = false;
-    if (a.topk_groups < a.groups) stays = group_stays<double>(a, l, best, second, near);
+    if (a.topk_groups < a.groups) stays = group_stays<double>(a, l, best, second, top, near);
 #pragma unroll
     for (int j = 0; j < VPL; ++j) {
       const uint64_t k = stays && l.has(j, a.groups) ? key_of(c[j]) : 0ull;
       hi[j] = (uint32_t)(k >> 32);
       lo[j] = (uint32_t)k;
     }
-    choose<VPL, true, false>(a, l, hi, lo, my_id);
+    choose<VPL, true, false>(a, l, hi, lo, own, my_id);
   }
 
   float w = 0.0f;
@@ -388,7 +444,7 @@ __global__ __launch_bounds__(256) void route_kernel(RouteArgs a) {
     // (my_id / size: the product is off by less than 2^-13 / size, and the
     // quotient at least 1 / (2 size) from a whole number)
     const int group = (int)(((float)my_id + 0.5f) * a.inv_size), in = my_id - group * l.size;
-    const int j = in >> log_per;
+    const int j = in >> l.log_per;
     w = score(logits[threadIdx.x >> 6][j * 64 + group * l.per + (in & (l.per - 1))]);
   }
   if (a.renorm) {

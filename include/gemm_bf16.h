@@ -345,9 +345,13 @@ int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_ty
  *   -infinity where all are); only the topk_groups best groups stay
  *   ids = the k largest c that stay, in descending order
  *   weights = s[ids], divided by their sum if renorm != 0, times scale
- * ids (T x k int32) and weights (T x k fp32) are contiguous.  The order is
- * that of the exact values, ties by lowest index (of groups too): it does
- * not depend on rounding in the scores.  A NaN logit counts as -infinity, a
+ * ids (T x k int32) and weights (T x k fp32) are contiguous.  Without a bias
+ * the order is that of the logits, and so is that of the groups with
+ * group_top 1; c of a bias, and sums of two, are compared as fp64 holds them.
+ * Values that are equal there go by logit, groups by that of their best
+ * expert; equal logits, and groups still equal, by lowest index.  So experts
+ * of the same bias stand in the order of their logits also where their scores
+ * round to the same value, and a bias of zeros changes nothing.  A NaN logit counts as -infinity, a
  * logit of +infinity as the largest finite number, and so do those of the
  * bias; masked experts have score 0 and are taken, at weight 0, only when
  * the others of the groups that stay run out; weights that sum to 0 are all

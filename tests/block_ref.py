@@ -71,7 +71,8 @@ def plan(ids, E):
 def route(x, k, bias=None, score="softmax", groups=1, topk_groups=None, group_top=2,
           renormalize=True, scale=1.0):
     """(ids, weights) in 64 bits; the order without a bias is that of the
-    logits."""
+    logits.  Equal scores go by logit (groups by that of their best expert),
+    then by index."""
     x = x.astype(np.float64)
     x = np.where(np.isnan(x), -np.inf, x)
     x = np.minimum(x, float(np.finfo(np.float32).max))
@@ -96,9 +97,10 @@ def route(x, k, bias=None, score="softmax", groups=1, topk_groups=None, group_to
         by = c[t].reshape(groups, size)
         top = -np.sort(-by, 1)[:, :group_top]
         best = np.where(np.isneginf(top[:, 0]), -np.inf, np.where(np.isneginf(top), 0, top).sum(1))
-        kept = np.argsort(-best, kind="stable")[:topk_groups]
-        candidates = np.sort((kept[:, None] * size + np.arange(size)).reshape(-1))
-        ids[t] = candidates[np.argsort(-c[t][candidates], kind="stable")[:k]]
+        order = np.lexsort((np.arange(E), -x[t], -c[t]))  # by c, then logit, then index
+        first = [x[t][order[order // size == b][0]] for b in range(groups)]
+        kept = np.lexsort((np.arange(groups), -np.array(first), -best))[:topk_groups]
+        ids[t] = order[np.isin(order // size, kept)][:k]
     w = np.take_along_axis(s, ids, 1)
     if renormalize:
         total = w.sum(1, keepdims=True)

@@ -202,6 +202,37 @@ def test_masked_experts_come_last_whatever_their_bias(mask, score):
                 assert (taken[:, 0] == left.any(1)).all()
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E, groups, topk, k", [(4, 1, 1, 2), (40, 1, 1, 7), (256, 1, 1, 8), (256, 8, 3, 8),
+                                                (600, 1, 1, 9), (1024, 4, 2, 30)])
+def test_scores_that_are_equal_in_64_bits_go_by_logit(E, groups, topk, k, score):
+    """Saturated sigmoids and softmax scores of 0: a bias of zeros, or the
+    same for all, leaves the choice as it is without one."""
+    import torch
+
+    rng = np.random.default_rng(E)
+    x = torch.from_numpy(rng.normal(0, 300, (30, E))).float()  # most scores are 0 or 1
+    x[1] = 40 + torch.from_numpy(rng.integers(0, 4, E)).float()
+    x[2] = -800 - torch.from_numpy(rng.random(E)).float()
+    x[3] = torch.from_numpy(np.where(np.arange(E) % 3, 1e30, -1e30) * rng.choice([1, 2, 3], E)).float()
+    x[4] = 1e-30 * x[4]
+    x[5] = 37 + x[5] / 3e6  # a step or none below 1
+    if E == 4:
+        x[0] = torch.tensor([40.0, 50.0, 3.0, 1.0])
+    kw = dict(score=score, groups=groups, topk_groups=topk)
+    for top in (1, 2):
+        ids, w = run_route(x, k, None, group_top=top, **kw)
+        again, v = run_route(x, k, np.zeros(E), group_top=top, **kw)
+        assert np.array_equal(ids, again) and np.array_equal(w, v)
+        for bias in (None, np.zeros(E), rng.choice([0.0, 1.0], E)):
+            assert np.array_equal(run_route(x, k, bias, group_top=top, **kw)[0],
+                                  ref.route(x.numpy(), k, bias, group_top=top, **kw)[0])
+    if groups == 1:
+        order = np.argsort(-x.double().numpy(), axis=1, kind="stable")[:, :k]
+        for bias in (0.0, 0.25, -1e9, 3e38):
+            assert np.array_equal(run_route(x, k, np.full(E, bias), **kw)[0], order), bias
+
+
 def test_a_masked_experts_row_does_not_reach_the_token():
     import torch
 
