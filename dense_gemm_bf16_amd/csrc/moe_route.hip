@@ -439,17 +439,28 @@ route_kernel(RouteArgs a) {
     choose<VPL, true, false>(a, l, hi, lo, own, my_id);
   }
 
-  float w = 0.0f;
+  float w = 0.0f, v = -INFINITY;
   if (l.lane < a.k) {  // my_id's place: its group's lanes, dealt in turn
     // (my_id / size: the product is off by less than 2^-13 / size, and the
     // quotient at least 1 / (2 size) from a whole number)
     const int group = (int)(((float)my_id + 0.5f) * a.inv_size), in = my_id - group * l.size;
     const int j = in >> l.log_per;
-    w = score(logits[threadIdx.x >> 6][j * 64 + group * l.per + (in & (l.per - 1))]);
+    v = logits[threadIdx.x >> 6][j * 64 + group * l.per + (in & (l.per - 1))];
+    w = score(v);
   }
   if (a.renorm) {
     const float sum = wave_sum(w);
+    const float each = w;
     w = sum > 0.0f ? w / sum : 0.0f;
+    // Scores near fp32's smallest, or below it, have lost their ratios (and
+    // sigmoid's exp(-v) is infinite from -88.7 down): again in fp64, whose
+    // range goes to a sigmoid of -709 or a softmax score 745 below the largest.
+    if (__any(each < 0x1p-100f && v > -INFINITY)) {
+      const double x = v;
+      const double s = l.lane >= a.k ? 0.0 : a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)m);
+      const double total = wave_sum(s);
+      w = total > 0.0 ? (float)(s / total) : 0.0f;
+    }
   }
   if (l.lane < a.k) {
     a.ids[t * a.k + l.lane] = my_id;

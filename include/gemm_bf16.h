@@ -351,11 +351,14 @@ int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_ty
  * Values that are equal there go by logit, groups by that of their best
  * expert; equal logits, and groups still equal, by lowest index.  So experts
  * of the same bias stand in the order of their logits also where their scores
- * round to the same value, and a bias of zeros changes nothing.  A NaN logit counts as -infinity, a
- * logit of +infinity as the largest finite number, and so do those of the
- * bias; masked experts have score 0 and are taken, at weight 0, only when
- * the others of the groups that stay run out; weights that sum to 0 are all
- * 0.  k may not exceed the experts of topk_groups groups.  Returns a status. */
+ * round to the same value, and a bias of zeros changes nothing.  A NaN logit
+ * counts as -infinity, a logit of +infinity as the largest finite number, and
+ * so do those of the bias; masked experts have score 0 and are taken, at
+ * weight 0, only when the others of the groups that stay run out.  Divided
+ * weights keep their ratios where the scores leave fp32's range, down to a
+ * sigmoid's logit of -709 or a softmax logit 745 below the row's largest,
+ * past which a score is 0; weights whose scores sum to 0 are all 0.  k may
+ * not exceed the experts of topk_groups groups.  Returns a status. */
 int gemm_moe_route(int64_t T, int64_t E, int64_t k, const void* X, int64_t ldx, int x_type,
                    const float* bias, int score, int64_t groups, int64_t topk_groups,
                    int group_top, int renorm, float scale, int32_t* ids, float* weights,

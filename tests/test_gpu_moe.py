@@ -233,6 +233,36 @@ def test_scores_that_are_equal_in_64_bits_go_by_logit(E, groups, topk, k, score)
             assert np.array_equal(run_route(x, k, np.full(E, bias), **kw)[0], order), bias
 
 
+@pytest.mark.parametrize("x_type", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("E, groups, topk, k", [(8, 1, 1, 3), (64, 1, 1, 6), (256, 8, 3, 8), (1024, 1, 1, 20)])
+def test_weights_of_scores_below_fp32(E, groups, topk, k, x_type):
+    """Chosen scores that fp32 holds as 0, or with a few bits, have ordinary
+    weights all the same: rows of logits about one level, rows across fp32's
+    border, and softmax choices far below the largest logit."""
+    import torch
+
+    rng = np.random.default_rng(E)
+    levels = np.array([-60.0, -69.3, -80, -87, -88.7, -89, -95, -100, -104, -300, -600, -700])
+    x = levels[:, None] + rng.normal(0, 2, (len(levels), E))
+    wide = -rng.uniform(40, 140, (8, E))  # chosen ones on both sides of the border
+    rows = torch.from_numpy(np.concatenate([x, wide])).to(dtype(x_type))
+    kw = dict(groups=groups, topk_groups=topk, scale=2.5)
+    for bias in (None, rng.normal(0, 1, E)):
+        check_route(rows, k, bias, score="sigmoid", **kw)
+    if E == 8:
+        ids, w = run_route(torch.linspace(-100, -95, 8)[None], 3, score="sigmoid")
+        assert ids.tolist() == [[7, 6, 5]] and np.abs(w - [[0.578305, 0.283104, 0.138591]]).max() < 1e-5
+    # one expert towers above those that the bias, or the groups, choose
+    towers = rows.float()
+    towers[:, 0] = towers[:, 1:].max(1).values + torch.from_numpy(rng.choice([85, 104, 110, 300, 600], len(rows)))
+    towers = towers.to(dtype(x_type))
+    bias = np.where(np.arange(E) == 0, -10.0, rng.normal(0, 1, E))
+    for renorm in (True, False):
+        check_route(towers, k, bias, renormalize=renorm, **kw)
+    ids, w = run_route(towers, k, bias, **kw)
+    assert (ids != 0).all() and np.abs(w.sum(1) - 2.5).max() < 1e-5
+
+
 def test_a_masked_experts_row_does_not_reach_the_token():
     import torch
 
