@@ -632,6 +632,14 @@ def moe_mlp_fp8(x, logits, k, W1, S1, W2, S2, **route):
     (E x ceil(H/128) x ceil(I/128)).  route: moe_route's keyword arguments.
     Activations are quantised per row and 128 columns before each product;
     the first product is rounded to x's type.  Returns T x H of x's type."""
+    if x.dim() != 2 or logits.dim() != 2 or W1.dim() != 3:
+        raise ValueError("need x (T x H), logits (T x E) and W1 (E x 2I x H)")
+    # (ids past W1's experts would be dropped, and rows past x's read as zeros)
+    if logits.shape[0] != x.shape[0] or logits.shape[1] != W1.shape[0]:
+        raise ValueError(f"logits must have a row for each of x's {x.shape[0]} tokens and a column "
+                         f"for each of W1's {W1.shape[0]} experts, not {tuple(logits.shape)}")
+    if W2.shape[0] != W1.shape[0]:
+        raise ValueError("W1 and W2 must hold as many experts")
     ids, weights = moe_route(logits, k, **route)
     offsets, rows, pos = moe_plan(ids, W1.shape[0])
     q, s = quantize_fp8(x)

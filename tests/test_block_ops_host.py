@@ -179,3 +179,20 @@ def test_tensor_forms_refuse_host_tensors(g):
                  lambda: g.moe_combine(x, torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, 2))):
         with pytest.raises(ValueError, match="GPU"):
             call()
+
+
+def test_layer_refuses_logits_of_other_experts_or_tokens(g):
+    """More experts than W1 holds would lose pairs, more tokens than x has
+    would read zeros, without a word."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(4, 256, dtype=torch.bfloat16)
+    W1, W2 = torch.zeros(8, 256, 256), torch.zeros(8, 256, 128)
+    S = torch.ones(8, 2, 2)
+    for T, E in ((4, 9), (4, 7), (5, 8), (3, 8)):
+        with pytest.raises(ValueError, match=r"4 tokens .* 8 experts, not \(%d, %d\)" % (T, E)):
+            g.moe_mlp_fp8(x, torch.zeros(T, E), 2, W1, S, W2, S[:, :, :1])
+    with pytest.raises(ValueError, match="as many experts"):
+        g.moe_mlp_fp8(x, torch.zeros(4, 8), 2, W1, S, W2[:7], S[:7, :, :1])
+    for bad in ((x[0], torch.zeros(4, 8), W1), (x, torch.zeros(8), W1), (x, torch.zeros(4, 8), W1[0])):
+        with pytest.raises(ValueError, match="need x"):
+            g.moe_mlp_fp8(bad[0], bad[1], 2, bad[2], S, W2, S)
