@@ -14,13 +14,13 @@ namespace gemm {
 
 const BlockConfig* block_configs() {
   static const BlockConfig table[] = {
-#define ROW(NAME, A, B, C, D, E, S) {#NAME, A, B, true, &launch_block_tile<A, B, C, D, E, S>},
+#define ROW(NAME, A, B, C, D, E, S) {#NAME, A, B, (C) * (D) * (E) * 64, &launch_block_tile<A, B, C, D, E, S>},
       BLOCK_TILES(ROW)
 #undef ROW
-#define ROW(NAME, A, B, C, D) {#NAME, 16 * A, 16 * B, false, &launch_block_row<A, B, C, D>},
+#define ROW(NAME, A, B, C, D) {#NAME, 16 * A, 16 * B, (C) * 64, &launch_block_row<A, B, C, D>},
       BLOCK_ROWS(ROW)
 #undef ROW
-      {nullptr, 0, 0, false, nullptr}};
+      {nullptr, 0, 0, 0, nullptr}};
   return table;
 }
 
@@ -216,7 +216,9 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
     if (!c) continue;
     if (c->bn * ldb * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
     if ((rows ? a_rows : (int64_t)c->bm) * lda * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
-    if (row_tile_bound(R, E, experts, c->bm) * ((N + c->bn - 1) / c->bn) >= k2G)
+    // (a grid holds fewer than 2^32 threads; the tiles fit 32 bits, so 64 hold the product)
+    const int64_t tiles_n = (N + c->bn - 1) / c->bn;
+    if (row_tile_bound(R, E, experts, c->bm) * tiles_n >= 2 * k2G / c->threads)
       return GEMM_ERR_UNSUPPORTED;
   }
   if (!work) return GEMM_OK;

@@ -14,7 +14,7 @@ namespace gemm {
 struct BlockConfig {
   const char* name;
   int bm, bn;    // rows and columns of C per workgroup
-  bool staged;   // block_tile_kernel (else block_row_kernel)
+  int threads;   // of a workgroup
   hipError_t (*launch)(const BlockArgs&, int grid, hipStream_t, int op, int out);
 };
 

@@ -85,6 +85,19 @@ def test_fp8_refusals(g, bad, code):
     assert fp8(g, **bad) == code
 
 
+@pytest.mark.parametrize("config, M, N", [
+    (b"b32x32k4", 65536, 65536), (b"b32x64k4", 131072, 65536), (b"r16x16", 32768, 65536),
+    (b"b64x64", 1 << 20, 1 << 16), (b"b256x256", 1 << 22, 1 << 17)])
+def test_grids_past_a_launch_are_refused(g, config, M, N):
+    """Workgroups times their threads reach 2^32.  (Experts without any: the
+    checks run, and nothing is launched.)"""
+    big = dict(N=N, ldc=N, config=config)
+    assert fp8(g, M=M, ldsa=M, **big) == 3
+    assert moe(g, R=M, T=M, ldsa=M, rows=NUL, **big) == 3
+    assert moe(g, R=M, T=M, ldsa=M, rows=NUL, E=0, **big) == 3
+    assert moe(g, R=M - 256, T=M, ldsa=M, rows=NUL, E=0, **big) == 0
+
+
 def test_empty_products_launch_nothing(g):
     assert fp8(g, M=0, A=NUL, SA=NUL, C=NUL) == 0
     assert fp8(g, N=0, B=NUL, SB=NUL, C=NUL) == 0
