@@ -349,7 +349,10 @@ int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_ty
   if (gemm::misaligned(X, gemm::element_bytes(x_type)) || gemm::misaligned(Q, 16) ||
       gemm::misaligned(S, 4) || (ldq & 15) != 0)
     return GEMM_ERR_MISALIGNED;
-  if (block_rows == 128 && (M + 127) / 128 > 65535) return GEMM_ERR_UNSUPPORTED;
+  // (a workgroup of 256 for each block: at most 65535 rows of blocks, and fewer than 2^32 threads
+  // across a row of them)
+  if (block_rows == 128 && ((M + 127) / 128 > 65535 || (K + 127) / 128 >= 2 * gemm::k2G / 256))
+    return GEMM_ERR_UNSUPPORTED;
   if (M == 0 || K == 0) return GEMM_OK;
   const gemm::QuantArgs a{X, (uint8_t*)Q, S, M, K, ldx, ldq, lds};
   const int t = gemm::store_of(x_type);

@@ -319,7 +319,8 @@ const char* gemm_fp8_config_at(int i);
  * block_rows 128: blocks of 128 x 128, S(j,b) = S[j*lds + b] (its SB;
  * without activation only).  NaN gives a NaN code and is left out of amax;
  * a block with an infinity gets an infinite scale.  M and K are below 2^31
- * (M with block_rows 128: at most 8388480).  Returns a status. */
+ * (with block_rows 128: M at most 8388480, K at most 2147483520).  Returns a
+ * status. */
 int gemm_fp8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_type, int act,
                       int block_rows, void* Q, int64_t ldq, float* S, int64_t lds,
                       void* stream);

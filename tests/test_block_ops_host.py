@@ -143,6 +143,14 @@ def test_quantize_refusals(g, bad, code):
     assert quantize(g, **bad) == code
 
 
+def test_blocks_past_a_launch_are_refused(g):
+    """A row of 2^24 blocks, a workgroup of 256 threads each."""
+    wide = dict(block=128, ldx=1 << 31, ldq=1 << 31, lds=1 << 24)
+    for K in ((1 << 31) - 127, (1 << 31) - 1):
+        assert quantize(g, M=1, K=K, **wide) == 3
+    assert quantize(g, M=0, K=(1 << 31) - 128, **wide) == 0
+
+
 def route(g, T=4, E=64, k=8, X=P, ldx=64, x_type=F32, bias=NUL, score=0, groups=8, topk_groups=4,
           top=2, renorm=1, ids=P, w=P):
     return g._lib.gemm_moe_route(T, E, k, X, ldx, x_type, bias, score, groups, topk_groups, top,
