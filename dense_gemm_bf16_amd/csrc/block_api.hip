@@ -106,15 +106,34 @@ double model_time4(const BlockCost& c, int bn, bool wide, double row_tiles, doub
 }
 
 // What a call runs: one shape on all of C, or (dense products only) `shape`
-// on columns 0 .. split_n - 1 and `tail` on the rest.
+// on columns 0 .. split_n - 1 and `tail` on the rest.  No shape: none can.
 struct BlockPlan {
   const BlockConfig* shape;
   const BlockConfig* tail;
   int64_t split_n;
 };
 
+// How far a call's operands reach: bytes from row to row, and for gathered
+// rows how many A has (-1: not gathered).
+struct Reach {
+  int64_t lda, ldb, gathered;
+};
+constexpr Reach kNear = {0, 0, -1};
+
+// Whether a shape can run R rows by N columns: what a workgroup loads from one
+// base (the tile's rows of B, those of A or all of a gathered A) lies within
+// a buffer resource, and the grid holds fewer than 2^32 threads (the tiles fit
+// 32 bits, so 64 hold the product).
+bool block_fits(const BlockConfig* c, int64_t R, int64_t N, int64_t E, bool experts,
+                const Reach& r) {
+  if (c->bn * r.ldb >= kRangeLimit) return false;
+  if ((r.gathered >= 0 ? r.gathered : (int64_t)c->bm) * r.lda >= kRangeLimit) return false;
+  const int64_t tiles_n = (N + c->bn - 1) / c->bn;
+  return row_tile_bound(R, E, experts, c->bm) * tiles_n < 2 * k2G / c->threads;
+}
+
 BlockPlan choose_block(int type, int64_t R, int64_t N, int64_t K, int64_t E, bool experts,
-                       int c_type) {
+                       int c_type, const Reach& reach) {
   const bool wide = type == GEMM_TYPE_E4M3 && c_type == GEMM_TYPE_F32;
   const double b_rows = experts ? (double)(R < E ? R : E) : 1.0;  // B's, of N rows each
   const double k_bytes = (double)K * (type == GEMM_TYPE_E4M3 ? 1 : 2);
@@ -123,6 +142,7 @@ BlockPlan choose_block(int type, int64_t R, int64_t N, int64_t K, int64_t E, boo
     const BlockConfig* best = nullptr;
     for (int i = 0; shapes[i].name; ++i) {
       const BlockConfig* shape = shapes + i;
+      if (!block_fits(shape, R, n, E, experts, reach)) continue;
       const double t = model_time4(kBlockCosts[i], shape->bn, wide,
                                    model_row_tiles(shape, R, E, experts), b_rows, n, k_bytes);
       if (best && t >= *t4) continue;
@@ -133,7 +153,7 @@ BlockPlan choose_block(int type, int64_t R, int64_t N, int64_t K, int64_t E, boo
   };
   double t4 = 0;
   BlockPlan plan{cheapest(N, &t4), nullptr, N};
-  if (experts || R < 1) return plan;
+  if (experts || R < 1 || !plan.shape) return plan;
   // Where a shape's last pass over the CUs would be part empty: the columns
   // that fill its whole passes, then the rest in the shape that is cheapest
   // for them (777 x 10240 x 4104 with fp32 output 97 -> 82 us, as 511
@@ -146,12 +166,13 @@ BlockPlan choose_block(int type, int64_t R, int64_t N, int64_t K, int64_t E, boo
     const int64_t pass = 256 * c.resident;
     if (rows > pass) continue;
     const int64_t head = rows * cols / pass * pass / rows * shape->bn / kScaleBlock * kScaleBlock;
-    if (head <= 0 || head >= N) continue;
+    if (head <= 0 || head >= N || !block_fits(shape, R, head, E, experts, reach)) continue;
     const double t1 =
         sqrt(sqrt(model_time4(c, shape->bn, wide, (double)rows, b_rows, head, k_bytes)));
     if (t1 >= best) continue;
     double tail4 = 0;
     const BlockConfig* tail = cheapest(N - head, &tail4);
+    if (!tail) continue;
     const double t = t1 + sqrt(sqrt(tail4));
     if (t >= best) continue;
     best = t;
@@ -204,23 +225,15 @@ int block_product(const char* config, int type, int64_t R, int64_t N, int64_t K,
       ldb >= k2G)
     return GEMM_ERR_UNSUPPORTED;
   if (scaled && kb > kMaxKSteps) return GEMM_ERR_UNSUPPORTED;
+  const Reach reach{lda * es, ldb * es, rows ? a_rows : -1};
   BlockPlan plan{nullptr, nullptr, N};
   if (config && config[0]) {
     plan.shape = block_config(config);
-    if (!plan.shape) return GEMM_ERR_UNSUPPORTED;
+    if (plan.shape && !block_fits(plan.shape, R, N, E, experts, reach)) plan.shape = nullptr;
   } else {
-    plan = choose_block(type, R, N, K, E, experts, c_type);
+    plan = choose_block(type, R, N, K, E, experts, c_type, reach);
   }
-  const BlockConfig* shapes[2] = {plan.shape, plan.tail};
-  for (const BlockConfig* c : shapes) {
-    if (!c) continue;
-    if (c->bn * ldb * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
-    if ((rows ? a_rows : (int64_t)c->bm) * lda * es >= kRangeLimit) return GEMM_ERR_UNSUPPORTED;
-    // (a grid holds fewer than 2^32 threads; the tiles fit 32 bits, so 64 hold the product)
-    const int64_t tiles_n = (N + c->bn - 1) / c->bn;
-    if (row_tile_bound(R, E, experts, c->bm) * tiles_n >= 2 * k2G / c->threads)
-      return GEMM_ERR_UNSUPPORTED;
-  }
+  if (!plan.shape) return GEMM_ERR_UNSUPPORTED;
   if (!work) return GEMM_OK;
 
   BlockArgs a{};
@@ -312,7 +325,9 @@ const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K, int c_type) {
   if (M < 0 || N < 0 || K < 0 || M >= gemm::k2G || N >= gemm::k2G || K >= gemm::k2G / 2)
     return "invalid";
   if (!gemm::is_float_type(c_type)) return "invalid";
-  const gemm::BlockPlan p = gemm::choose_block(GEMM_TYPE_E4M3, M, N, K, 1, false, c_type);
+  const gemm::BlockPlan p =
+      gemm::choose_block(GEMM_TYPE_E4M3, M, N, K, 1, false, c_type, gemm::kNear);
+  if (!p.shape) return "invalid";
   if (!p.tail) return p.shape->name;
   snprintf(gemm::g_plan_name, sizeof gemm::g_plan_name, "%s+%s", p.shape->name, p.tail->name);
   return gemm::g_plan_name;
@@ -324,7 +339,8 @@ const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int6
     return "invalid";
   if (!gemm::is_float_type(c_type)) return "invalid";
   if (type != GEMM_TYPE_E4M3 && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return "invalid";
-  return gemm::choose_block(type, R, N, K, E, true, c_type).shape->name;
+  const gemm::BlockPlan p = gemm::choose_block(type, R, N, K, E, true, c_type, gemm::kNear);
+  return p.shape ? p.shape->name : "invalid";
 }
 
 const char* gemm_fp8_config_at(int i) {

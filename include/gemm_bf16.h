@@ -259,8 +259,10 @@ int gemm_bf16_ex_noalloc(const char* config,
  * A and B 16-byte aligned with lda and ldb multiples of 16; C 16-byte
  * aligned with ldc a multiple of 8; scales 4-byte aligned.  Any M, N, K >= 0
  * up to K = 131072 (GEMM_ERR_UNSUPPORTED past it); K == 0 sets C to zeros.
- * A named shape whose grid would not hold fewer than 2^32 threads (a small
- * tile on a C of 2^31 elements and more) is refused as well.
+ * Refused as well: rows so far apart that 16 of A or of B span 2^31 - 4096
+ * bytes or more, and grids of 2^32 threads and more.  A named shape counts
+ * with its own BM and BN rows (256 of "b256x256") and tiles (a small one on a
+ * C of 2^31 elements); the automatic choice takes one that runs.
  *
  * Numerics: the 128 products of a block are summed by the matrix core,
  * multiplied by the fp32 product of the two scales and added to an fp32 sum,

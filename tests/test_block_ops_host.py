@@ -98,6 +98,25 @@ def test_grids_past_a_launch_are_refused(g, config, M, N):
     assert moe(g, R=M - 256, T=M, ldsa=M, rows=NUL, E=0, **big) == 0
 
 
+def test_row_strides_are_refused_only_where_no_shape_runs_them(g):
+    """(Experts without any: shapes are chosen, nothing is launched.)  The
+    shape that fits sizes of 8192 best loads 256 rows from one base, the
+    smallest 16."""
+    big = dict(R=8192, N=8192, K=4096, E=0, T=8192, lda=4096, ldsa=8192, rows=NUL, ldb=4096,
+               ldsb=32, ldc=8192)
+    assert g.moe_config_name(E4M3, 8192, 8192, 4096, 0) == "b256x256"
+    for ld in ("lda", "ldb"):
+        for stride, code in ((1 << 22, 0), (1 << 23, 0), (1 << 26, 0), ((1 << 27) - 4096, 0), (1 << 27, 3)):
+            assert moe(g, **{**big, ld: stride}) == code, (ld, stride)
+        assert moe(g, config=b"b256x256", **{**big, ld: 1 << 23}) == 3
+        assert moe(g, config=b"b128x128", **{**big, ld: 1 << 23}) == 0
+        assert moe(g, type=BF16, **{**big, ld: 1 << 25}) == 0
+        assert moe(g, type=BF16, **{**big, ld: 1 << 26}) == 3
+    gathered = {**big, "rows": P}
+    assert moe(g, **{**gathered, "lda": 1 << 18}) == 3  # all of A from one base
+    assert moe(g, **{**gathered, "lda": (1 << 18) - 16}) == 0
+
+
 def test_empty_products_launch_nothing(g):
     assert fp8(g, M=0, A=NUL, SA=NUL, C=NUL) == 0
     assert fp8(g, N=0, B=NUL, SB=NUL, C=NUL) == 0

@@ -410,3 +410,32 @@ def test_other_stream_and_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, layer()), i
+
+
+@pytest.mark.parametrize("M, N, K, far", [(650, 14336, 256, "A"), (40000, 256, 1024, "B")])
+def test_rows_far_apart_take_a_shape_that_reaches_them(M, N, K, far):
+    """Rows 8 MiB apart: 256 of them, the best shape's, span too much for one
+    base, so a smaller shape runs."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    assert g.fp8_config_name(M, N, K) == "b256x256"
+    rng = torch.Generator(device="cuda").manual_seed(M)
+    draw = lambda n: torch.randint(-4, 5, (n, K), device="cuda", generator=rng).float().to(torch.float8_e4m3fn)  # noqa: E731
+    A, B = draw(M), draw(N)
+    SA = 2.0 ** torch.randint(-2, 3, (K // 128, M), device="cuda", generator=rng).float()
+    SB = 2.0 ** torch.randint(-2, 3, (N // 128, K // 128), device="cuda", generator=rng).float()
+    want = g.matmul_fp8(A, SA, B, SB, out_dtype=torch.float32)
+    rows = M if far == "A" else N
+    wide = torch.empty(rows << 23, device="cuda", dtype=torch.uint8).view(torch.float8_e4m3fn)
+    apart = wide.as_strided((rows, K), (1 << 23, 1))
+    apart.copy_(A if far == "A" else B)
+    if far == "A":
+        A = apart
+    else:
+        B = apart
+    for out in (torch.float32, torch.bfloat16):
+        assert torch.equal(g.matmul_fp8(A, SA, B, SB, out_dtype=out), want.to(out))
+    with pytest.raises(g.GemmError):
+        g.matmul_fp8(A, SA, B, SB, config="b256x256")
