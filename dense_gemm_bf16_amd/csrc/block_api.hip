@@ -324,7 +324,7 @@ int gemm_moe(int type, int64_t R, int64_t N, int64_t K, int64_t E, int64_t T, co
 const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K, int c_type) {
   if (M < 0 || N < 0 || K < 0 || M >= gemm::k2G || N >= gemm::k2G || K >= gemm::k2G / 2)
     return "invalid";
-  if (!gemm::is_float_type(c_type)) return "invalid";
+  if (!gemm::is_float_type(c_type) || K > gemm::kScaleBlock * gemm::kMaxKSteps) return "invalid";
   const gemm::BlockPlan p =
       gemm::choose_block(GEMM_TYPE_E4M3, M, N, K, 1, false, c_type, gemm::kNear);
   if (!p.shape) return "invalid";
@@ -339,6 +339,7 @@ const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int6
     return "invalid";
   if (!gemm::is_float_type(c_type)) return "invalid";
   if (type != GEMM_TYPE_E4M3 && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return "invalid";
+  if (type == GEMM_TYPE_E4M3 && K > gemm::kScaleBlock * gemm::kMaxKSteps) return "invalid";
   const gemm::BlockPlan p = gemm::choose_block(type, R, N, K, E, true, c_type, gemm::kNear);
   return p.shape ? p.shape->name : "invalid";
 }

@@ -301,7 +301,8 @@ int gemm_fp8_ex(const char* config, int64_t M, int64_t N, int64_t K,
  * through LDS ("k<n>": n groups of waves share K), "r<BM>x<BN>" streams both
  * operands into registers; "<shape>+<shape>": the columns that fill whole
  * passes over the GPU's compute units in the first, the rest in the second
- * (two launches).  Per-thread static storage. */
+ * (two launches).  "invalid": gemm_fp8 refuses these sizes.  Per-thread static
+ * storage. */
 const char* gemm_fp8_config_name(int64_t M, int64_t N, int64_t K, int c_type);
 
 /* The i-th kernel shape (of gemm_fp8 and gemm_moe), or NULL past the end. */
@@ -405,7 +406,8 @@ int gemm_moe_ex(const char* config, int type, int64_t R, int64_t N, int64_t K, i
                 const float* SB, int64_t ldsb, int64_t stride_sb,
                 void* C, int64_t ldc, int c_type, void* stream);
 
-/* Name of the kernel shape gemm_moe chooses.  Static storage. */
+/* Name of the kernel shape gemm_moe chooses ("invalid": it refuses these
+ * sizes).  Static storage. */
 const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int64_t E,
                                  int c_type);
 

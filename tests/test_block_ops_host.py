@@ -53,6 +53,17 @@ def test_config_names(g):
     assert g.moe_config_name(E4M3, 1, 1, 1, -1) == g.moe_config_name(F32, 1, 1, 1, 1) == "invalid"
 
 
+def test_sizes_that_are_refused_have_no_shape(g):
+    for M, N in ((1, 8), (300, 8192)):
+        for c_type in (BF16, F16, F32):
+            assert g.fp8_config_name(M, N, 131072, c_type) != "invalid"
+            assert g.fp8_config_name(M, N, 131073, c_type) == "invalid"
+        assert g.moe_config_name(E4M3, M, N, 131073, 4) == "invalid"
+        assert g.moe_config_name(BF16, M, N, 131073, 4) != "invalid"
+    assert g.fp8_config_name((1 << 31) - 1, (1 << 31) - 1, 128) == "invalid"
+    assert moe(g, R=(1 << 31) - 1, N=(1 << 31) - 1, E=0, T=8, ldc=1 << 31) == 3
+
+
 def test_sizes_past_the_limits_are_refused(g):
     """Before any of them enters a product that could overflow."""
     for v in (1 << 31, (1 << 63) - 16):
