@@ -59,6 +59,7 @@ int64_t row_tile_bound(int64_t R, int64_t E, bool experts, int64_t bm) {
 // that.  The whole takes at least as long as reading B at 5.2 TB/s (joined as
 // fourth powers, so near the floor the cheaper compute still counts).
 struct BlockCost {  // of the shape in the same place of block_configs()
+  const char* name;
   int k_groups, resident;
   struct Fit {
     float step, tile, part, base;  // us, us, share, us
@@ -66,17 +67,42 @@ struct BlockCost {  // of the shape in the same place of block_configs()
 };
 constexpr float kNever = 1e9f;
 constexpr BlockCost kBlockCosts[] = {
-    /* b256x256   */ {1, 1, {1.586f, 6.15f, 0.69f, 2.19f}, {kNever, 0, 0, 0}},
-    /* b256x128   */ {1, 1, {0.932f, 4.29f, 0.76f, 1.51f}, {kNever, 0, 0, 0}},
-    /* b128x128   */ {1, 2, {1.032f, 3.95f, 0.55f, 2.44f}, {1.822f, 4.58f, 0.61f, 0.00f}},
-    /* b128x128k2 */ {2, 1, {1.172f, 5.23f, 0.83f, 1.37f}, {1.962f, 5.14f, 0.85f, 0.00f}},
-    /* b64x128k2  */ {2, 1, {0.873f, 3.68f, 0.75f, 1.39f}, {1.299f, 3.53f, 0.86f, 0.73f}},
-    /* b64x64     */ {1, 2, {0.492f, 3.41f, 0.67f, 1.06f}, {0.774f, 1.59f, 0.56f, 2.97f}},
-    /* b64x64k2   */ {2, 1, {0.528f, 3.97f, 0.84f, 0.44f}, {0.799f, 3.88f, 0.85f, 0.57f}},
-    /* b32x128    */ {1, 2, {0.645f, 3.14f, 0.62f, 0.83f}, {1.032f, 0.00f, 0.50f, 2.96f}},
-    /* b32x64k4   */ {4, 1, {0.678f, 4.52f, 0.88f, 0.00f}, {0.932f, 4.82f, 0.90f, 0.00f}},
-    /* b32x32k4   */ {4, 1, {0.508f, 3.15f, 0.96f, 1.30f}, {0.663f, 3.46f, 0.92f, 1.12f}},
-    /* r16x16     */ {8, 4, {2.435f, 1.11f, 0.24f, 3.08f}, {2.435f, 1.11f, 0.24f, 3.08f}}};
+    {"b256x256", 1, 1, {1.586f, 6.15f, 0.69f, 2.19f}, {kNever, 0, 0, 0}},
+    {"b256x128", 1, 1, {0.932f, 4.29f, 0.76f, 1.51f}, {kNever, 0, 0, 0}},
+    {"b128x128", 1, 2, {1.032f, 3.95f, 0.55f, 2.44f}, {1.822f, 4.58f, 0.61f, 0.00f}},
+    {"b128x128k2", 2, 1, {1.172f, 5.23f, 0.83f, 1.37f}, {1.962f, 5.14f, 0.85f, 0.00f}},
+    {"b64x128k2", 2, 1, {0.873f, 3.68f, 0.75f, 1.39f}, {1.299f, 3.53f, 0.86f, 0.73f}},
+    {"b64x64", 1, 2, {0.492f, 3.41f, 0.67f, 1.06f}, {0.774f, 1.59f, 0.56f, 2.97f}},
+    {"b64x64k2", 2, 1, {0.528f, 3.97f, 0.84f, 0.44f}, {0.799f, 3.88f, 0.85f, 0.57f}},
+    {"b32x128", 1, 2, {0.645f, 3.14f, 0.62f, 0.83f}, {1.032f, 0.00f, 0.50f, 2.96f}},
+    {"b32x64k4", 4, 1, {0.678f, 4.52f, 0.88f, 0.00f}, {0.932f, 4.82f, 0.90f, 0.00f}},
+    {"b32x32k4", 4, 1, {0.508f, 3.15f, 0.96f, 1.30f}, {0.663f, 3.46f, 0.92f, 1.12f}},
+    {"r16x16", 8, 4, {2.435f, 1.11f, 0.24f, 3.08f}, {2.435f, 1.11f, 0.24f, 3.08f}}};
+
+// The table is read by place: the same shapes in the same order, with as many
+// groups of waves along K as they are built with.
+constexpr struct {
+  const char* name;
+  int k_groups;
+} kBuiltShapes[] = {
+#define ROW(NAME, A, B, C, D, E, S) {#NAME, E},
+    BLOCK_TILES(ROW)
+#undef ROW
+#define ROW(NAME, A, B, C, D) {#NAME, C},
+    BLOCK_ROWS(ROW)
+#undef ROW
+};
+constexpr bool costs_match_shapes() {
+  constexpr size_t n = sizeof kBuiltShapes / sizeof *kBuiltShapes;
+  if (n != sizeof kBlockCosts / sizeof *kBlockCosts) return false;
+  for (size_t i = 0; i < n; ++i) {
+    const char *a = kBuiltShapes[i].name, *b = kBlockCosts[i].name;
+    while (*a && *a == *b) ++a, ++b;
+    if (*a != *b || kBuiltShapes[i].k_groups != kBlockCosts[i].k_groups) return false;
+  }
+  return true;
+}
+static_assert(costs_match_shapes(), "a line of kBlockCosts for each built shape, in their order");
 constexpr double kStreamMBPerUs = 5.2, kStreamBaseUs = 2.5;
 
 // Row tiles as the model counts them.  How the rows fall to the experts is
