@@ -14,7 +14,8 @@ namespace gemm {
 
 const BlockConfig* block_configs() {
   static const BlockConfig table[] = {
-#define ROW(NAME, A, B, C, D, E, S) {#NAME, A, B, (C) * (D) * (E) * 64, &launch_block_tile<A, B, C, D, E, S>},
+#define ROW(NAME, A, B, C, D, E, S) \
+  {#NAME, A, B, (C) * (D) * (E) * 64, &launch_block_tile<A, B, C, D, E, S>},
       BLOCK_TILES(ROW)
 #undef ROW
 #define ROW(NAME, A, B, C, D) {#NAME, 16 * A, 16 * B, (C) * 64, &launch_block_row<A, B, C, D>},
@@ -49,8 +50,9 @@ int64_t row_tile_bound(int64_t R, int64_t E, bool experts, int64_t bm) {
 // (least squares on log time) to 167 swept products timed in every shape
 // below (dense: M 1-4096, N x K from 600 x 1000 to 28672 x 1024; experts: 8
 // to 128 experts, 1 to 8192 tokens, e4m3 and bf16).  Its choice ran within
-// 0.9 % of the fastest shape timed (geometric mean; 18 % at worst), 1.8 %
-// for e4m3 with fp32 output.
+// 0.9 % of the fastest shape timed (geometric mean; 18 % at worst), 2.0 % (24
+// %) for e4m3 with fp32 output.  block_model.py holds the same model, the
+// sweep, its times and the fit, which gives these constants.
 //
 // A launch of `units` workgroups on CUs that hold `resident` of them each
 // makes passes of 256 * resident; a pass costs steps * step + tile (steps:
@@ -65,6 +67,12 @@ struct BlockCost {  // of the shape in the same place of block_configs()
     float step, tile, part, base;  // us, us, share, us
   } fit, wide;                     // wide: e4m3 with fp32 output (codes widened to bf16)
 };
+// Two shapes are not chosen for e4m3 with fp32 output.  256 x 256 spills its
+// widened fragments: 4.9 us a K-step, where four 128 x 128 tiles on two CUs
+// take 3.6.  256 x 128 was the fastest of all for one of the 24 products (2048
+// x 4096 x 4096: 60.0 us, 128 x 128 65.6) and slower on the others, up to 15 %
+// where it counts (777 x 10240 x 4104: 114.6 us, 128 x 128 99.7), and the
+// model misjudges it (13 % rms) and would take it there.
 constexpr float kNever = 1e9f;
 constexpr BlockCost kBlockCosts[] = {
     {"b256x256", 1, 1, {1.586f, 6.15f, 0.69f, 2.19f}, {kNever, 0, 0, 0}},
