@@ -439,3 +439,29 @@ def test_rows_far_apart_take_a_shape_that_reaches_them(M, N, K, far):
         assert torch.equal(g.matmul_fp8(A, SA, B, SB, out_dtype=out), want.to(out))
     with pytest.raises(g.GemmError):
         g.matmul_fp8(A, SA, B, SB, config="b256x256")
+
+
+@pytest.mark.parametrize("M, N, K, out", [
+    (M, N, K, out) for M, N, K in ((641, 21768, 70), (694, 24955, 272), (2869, 6675, 275),
+                                   (1007, 16422, 444), (1252, 6536, 973)) for out in ("bf16", "f16")] +
+    [(291, 26435, 267, "f32"), (1052, 7171, 274, "f32"), (2084, 4784, 402, "f32")])
+def test_each_two_launch_plan_covers_c(M, N, K, out):
+    """Each of these runs as two launches, for both 16-bit types and fp32: on
+    integers every element of C once, with its own columns' scales, and
+    nothing beside C.  (f16: sums stay below 65504.)"""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    code = {"bf16": g.GEMM_TYPE_BF16, "f16": g.GEMM_TYPE_F16, "f32": g.GEMM_TYPE_F32}[out]
+    assert "+" in g.fp8_config_name(M, N, K, code)
+    a, sa, b, sb = exact_case(M, N, K, M)
+    sa /= 16
+    want, _ = block_product(a, sa, b, sb)
+    ld = -(-N // 8) * 8 + 16
+    buf = torch.full((M + 2, ld), 7.0, device="cuda", dtype=dtype(out))
+    product(a, sa, b, sb, out, c=buf[1:M + 1, 8:8 + N])
+    got = buf.float().cpu()
+    assert torch.equal(got[1:M + 1, 8:8 + N], torch.from_numpy(want.astype(np.float32)).to(dtype(out)).float())
+    got[1:M + 1, 8:8 + N] = 7.0
+    assert bool((got == 7.0).all())
