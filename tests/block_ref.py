@@ -45,6 +45,24 @@ def block_product(A, SA, B, SB):
     return C, 2 * U * sums * mag
 
 
+def cut_bound(A, SA, B, SB):
+    """What a 16-bit C of e4m3 operands may miss beside its fp32 error: of
+    eight products at a time all but the largest are cut by less than 2^-13 of
+    its codes' powers of two (2^-6 for subnormal codes), times the scales."""
+    def power(x):
+        x = np.maximum(np.abs(x.astype(np.float64)), 2.0 ** -6)
+        x = np.pad(x, ((0, 0), (0, -x.shape[1] % 128)), constant_values=2.0 ** -6)
+        return 2.0 ** np.floor(np.log2(x)).reshape(len(x), -1, 8)
+
+    pa, pb = power(A), power(B)
+    cut = np.zeros((len(pa), len(pb)))
+    for i in range(pa.shape[1]):  # eights; 16 to a block
+        largest = (pa[:, i][:, None] * pb[:, i][None]).max(2)
+        scale = np.abs(SA[i // 16][:, None] * np.repeat(SB[:, i // 16], 128)[:len(pb)][None])
+        cut += 7 * 2.0 ** -13 * largest * scale
+    return cut
+
+
 def check_rounded(got, want, err, out):
     """got (float64) is `want`, known to `err`, rounded once to type `out`."""
     tol = err + HALF_STEP[out] * (np.abs(want) + err) + TINY[out]

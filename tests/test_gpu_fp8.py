@@ -4,7 +4,7 @@ from the roundings."""
 import numpy as np
 import pytest
 
-from block_ref import HALF_STEP, block_product, check_rounded, dtype, padded
+from block_ref import HALF_STEP, block_product, check_rounded, cut_bound, dtype, padded
 
 pytestmark = pytest.mark.gpu
 
@@ -465,3 +465,45 @@ def test_each_two_launch_plan_covers_c(M, N, K, out):
     assert torch.equal(got[1:M + 1, 8:8 + N], torch.from_numpy(want.astype(np.float32)).to(dtype(out)).float())
     got[1:M + 1, 8:8 + N] = 7.0
     assert bool((got == 7.0).all())
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("config", CONFIGS)
+def test_products_that_cancel(config, out):
+    """Outliers, products that cancel to nothing beside small ones, and
+    subnormal codes: a 16-bit C within what the matrix instruction cuts off,
+    fp32 C as if nothing were large."""
+    import torch
+
+    rng = np.random.default_rng(11)
+    M, N, K = 40, 70, 400
+    codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).float().numpy()
+    codes = codes[np.isfinite(codes)]
+    a, b = rng.choice(codes, (M, K)), rng.choice(codes, (N, K))  # every exponent alike
+    a[8:16], b[8:16] = rng.choice([-1, 1], (8, K)), rng.choice([1, 2], (8, K))
+    a[16:24] *= rng.choice([0, 1], (8, K), p=[0.9, 0.1])
+    for i, (p, q) in enumerate(((0, 1), (0, 127), (5, 9), (128, 399), (130, 135), (3, 260))):
+        a[8 + i, p], a[8 + i, q] = 448, -448  # sums of small products beside +-448 * 448
+        b[8:16, p] = b[8:16, q] = 448
+    a, b = a.astype(np.float32), b.astype(np.float32)
+    kb, nb = 4, 1
+    sa, sb = np.full((kb, M), 2.0 ** -5, np.float32), np.full((nb, kb), 2.0 ** -6, np.float32)
+    want, err = block_product(a, sa, b, sb)
+    got = product(a, sa, b, sb, out, config)
+    check_rounded(got, want, err if out == "f32" else err + cut_bound(a, sa, b, sb), out)
+
+
+def test_small_products_beside_a_cancelled_one():
+    """Where the eights' borders lie, and that fp32 C loses nothing."""
+    a, b = np.zeros((3, 128), np.float32), np.zeros((1, 128), np.float32)
+    b[0, [0, 9]] = 448
+    b[0, 10:127] = 1
+    a[:, 10:127] = 1                  # 117 products of 1
+    a[1, 0], a[1, 9] = 448, -448      # 0 .. 7 and 8 .. 15: six ones beside the second
+    a[2, 0], a[2, 9] = 1, 1
+    one = np.ones((1, 3), np.float32)
+    for config in CONFIGS:
+        got = product(a, one, b, one[:, :1], "f32", config)
+        assert got.tolist() == [[117], [117], [117 + 2 * 448]]
+        got = product(a, one, b, one[:, :1], "bf16", config)
+        assert got[0] == 117 and 117 - 6 <= got[1] <= 117
