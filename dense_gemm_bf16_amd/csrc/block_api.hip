@@ -47,11 +47,14 @@ int64_t row_tile_bound(int64_t R, int64_t E, bool experts, int64_t bm) {
 
 // ------------------------------------------------------- choice of shape
 // The shape that a model of a launch's time on MI355X makes cheapest, fitted
-// (least squares on log time) to 167 swept products timed in every shape
-// below (dense: M 1-4096, N x K from 600 x 1000 to 28672 x 1024; experts: 8
-// to 128 experts, 1 to 8192 tokens, e4m3 and bf16).  Its choice ran within
+// (least squares on log time) to 167 swept products timed in the shapes below
+// that were in question (dense: M 1-4096, N x K from 600 x 1000 to 28672 x
+// 1024; experts: 8 to 128 experts, 1 to 8192 tokens, e4m3 and bf16; r16x16
+// with dense products only).  Its choice ran within
 // 0.9 % of the fastest shape timed (geometric mean; 18 % at worst), 2.0 % (24
-// %) for e4m3 with fp32 output.  block_model.py holds the same model, the
+// %) for e4m3 with fp32 output, and within 3.7 % over 70 products of 1 to 16
+// tokens with experts of 512 x 512 to 4096 x 4096 timed afterwards in every
+// shape (33 % at worst: 5.3 us where r16x16 takes 4.0).  block_model.py holds the same model, the
 // sweep, its times and the fit, which gives these constants.
 //
 // A launch of `units` workgroups on CUs that hold `resident` of them each

@@ -17,10 +17,10 @@
 // one FMA each with SA * SB: 4 FMAs (16 cycles of the SIMD's vector unit)
 // per MFMA of 32 cycles, issued while the next MFMA runs.
 //
-// Measured (MI355X): 8192 x 10240 x 8192 bf16 out 575 us, 2390 TFLOP/s, the
-// matrix cores 58 % busy; 1 x 8192 x 8192 12-15 us (memory); 64, 128, 256
-// rows by 8192 x 8192 19.5, 23.5, 32 us (the L2: tile traffic of 13-15 TB/s
-// when the lines come in from the fabric, whatever the ring's depth).
+// Measured (MI355X): 8192 x 10240 x 8192 bf16 out 571-608 us, 2260-2410
+// TFLOP/s, the matrix cores 58 % busy; 1 x 8192 x 8192 12-13 us (memory); 64,
+// 128, 256 rows by 8192 x 8192 15, 20.5, 29 us (the L2: tile traffic of 13-15
+// TB/s when the lines come in from the fabric, whatever the ring's depth).
 #pragma once
 
 #include "gemm_kernel.hpp"
