@@ -31,8 +31,8 @@ GEMM_ERR_HIP = 4
 GEMM_ERR_CAPTURE = 5
 GEMM_ERR_SCRATCH = 6
 GEMM_NOALLOC_SCRATCH_BYTES = 64 << 20
-GEMM_TYPE_BF16, GEMM_TYPE_F16, GEMM_TYPE_F32, GEMM_TYPE_E4M3 = 0, 1, 2, 3
-GEMM_ACT_NONE, GEMM_ACT_SWIGLU = 0, 1
+GEMM_TYPE_BF16, GEMM_TYPE_F16, GEMM_TYPE_F32, GEMM_TYPE_E4M3, GEMM_TYPE_I8 = 0, 1, 2, 3, 4
+GEMM_ACT_NONE, GEMM_ACT_SWIGLU, GEMM_ACT_GEGLU = 0, 1, 2
 GEMM_SCORE_SOFTMAX, GEMM_SCORE_SIGMOID = 0, 1
 
 if not os.path.exists(LIB_PATH):
@@ -89,7 +89,17 @@ _c_int = ctypes.c_int
 _fp8_args = [_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _c_int, _p]
 _moe_args = [_c_int, _i64, _i64, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _p, _i64, _i64,
              _p, _i64, _i64, _p, _i64, _c_int, _p]
+_i8_args = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _p, _i64, _c_int, _p]
+_i8_gated_args = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _c_int, _p, _i64, _c_int, _p]
+_gated_args = [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _c_int, _p, _i64, _p, _i64, _p]
 for _name, _args in {
+    "gemm_i8": _i8_args,
+    "gemm_i8_ex": [ctypes.c_char_p, *_i8_args],
+    "gemm_i8_quantize": [_i64, _i64, _p, _i64, _c_int, _p, _i64, _p, _p],
+    "gemm_i8_gated": _i8_gated_args,
+    "gemm_i8_gated_ex": [ctypes.c_char_p, *_i8_gated_args],
+    "gemm_gated": _gated_args,
+    "gemm_gated_ex": [ctypes.c_char_p, *_gated_args],
     "gemm_fp8": _fp8_args,
     "gemm_fp8_ex": [ctypes.c_char_p, *_fp8_args],
     "gemm_fp8_quantize": [_i64, _i64, _p, _i64, _c_int, _c_int, _c_int, _p, _i64, _p, _i64, _p],
@@ -106,6 +116,10 @@ _lib.gemm_fp8_config_name.restype = ctypes.c_char_p
 _lib.gemm_fp8_config_name.argtypes = [_i64, _i64, _i64, _c_int]
 _lib.gemm_moe_config_name.restype = ctypes.c_char_p
 _lib.gemm_moe_config_name.argtypes = [_c_int, _i64, _i64, _i64, _i64, _c_int]
+_lib.gemm_i8_config_name.restype = ctypes.c_char_p
+_lib.gemm_i8_config_name.argtypes = [_i64, _i64, _i64]
+_lib.gemm_gated_config_name.restype = ctypes.c_char_p
+_lib.gemm_gated_config_name.argtypes = [_c_int, _i64, _i64, _i64]
 _lib.gemm_fp8_config_at.restype = ctypes.c_char_p
 _lib.gemm_fp8_config_at.argtypes = [ctypes.c_int]
 
@@ -387,6 +401,67 @@ def gemm_fp8_config_at(i: int):
     return None if n is None else n.decode()
 
 
+# ------------------------------------------------- 8-bit integers and gated products
+# The C calls, argument for argument.
+
+def gemm_i8(M, N, K, A, lda, SA, B, ldb, SB, C, ldc, c_type, stream=None) -> None:
+    """C = A . B^T over 8-bit integers, a scale for each row of A and of B."""
+    gemm_i8_ex(None, M, N, K, A, lda, SA, B, ldb, SB, C, ldc, c_type, stream)
+
+
+def gemm_i8_ex(config, M, N, K, A, lda, SA, B, ldb, SB, C, ldc, c_type, stream=None) -> None:
+    """As gemm_i8 with the kernel shape named (None = automatic)."""
+    cfg = None if config is None else config.encode()
+    _check(_lib.gemm_i8_ex(cfg, M, N, K, _ptr(A), lda, _ptr(SA), _ptr(B), ldb, _ptr(SB), _ptr(C),
+                           ldc, c_type, _stream(stream)))
+
+
+def gemm_i8_quantize(M, K, X, ldx, x_type, Q, ldq, S, stream=None) -> None:
+    """X to 8-bit integers Q with a scale for each row, S."""
+    _check(_lib.gemm_i8_quantize(M, K, _ptr(X), ldx, x_type, _ptr(Q), ldq, _ptr(S),
+                                 _stream(stream)))
+
+
+def gemm_i8_gated(M, F, K, A, lda, SA, W, ldw, SW, act, H, ldh, h_type, stream=None) -> None:
+    """H = act(A . Wg^T) * (A . Wu^T) over 8-bit integers, scaled as gemm_i8."""
+    gemm_i8_gated_ex(None, M, F, K, A, lda, SA, W, ldw, SW, act, H, ldh, h_type, stream)
+
+
+def gemm_i8_gated_ex(config, M, F, K, A, lda, SA, W, ldw, SW, act, H, ldh, h_type,
+                     stream=None) -> None:
+    """As gemm_i8_gated with the kernel shape named (None = automatic)."""
+    cfg = None if config is None else config.encode()
+    _check(_lib.gemm_i8_gated_ex(cfg, M, F, K, _ptr(A), lda, _ptr(SA), _ptr(W), ldw, _ptr(SW), act,
+                                 _ptr(H), ldh, h_type, _stream(stream)))
+
+
+def gemm_gated(type, M, F, K, X, ldx, W, ldw, act, H, ldh, GU=None, ldgu=0, stream=None) -> None:
+    """H = act(X . Wg^T) * (X . Wu^T), bf16 or fp16; G and U to GU as well."""
+    gemm_gated_ex(None, type, M, F, K, X, ldx, W, ldw, act, H, ldh, GU, ldgu, stream)
+
+
+def gemm_gated_ex(config, type, M, F, K, X, ldx, W, ldw, act, H, ldh, GU=None, ldgu=0,
+                  stream=None) -> None:
+    """As gemm_gated with the kernel shape named (None = automatic)."""
+    cfg = None if config is None else config.encode()
+    _check(_lib.gemm_gated_ex(cfg, type, M, F, K, _ptr(X), ldx, _ptr(W), ldw, act, _ptr(H), ldh,
+                              _ptr(GU), ldgu, _stream(stream)))
+
+
+def i8_config_name(M, N, K) -> str:
+    """The kernel shape gemm_i8 chooses."""
+    return _lib.gemm_i8_config_name(M, N, K).decode()
+
+
+def gated_config_name(type, M, F, K) -> str:
+    """The kernel shape the gated product of a type chooses."""
+    return _lib.gemm_gated_config_name(type, M, F, K).decode()
+
+
+gemm_i8_config_name = i8_config_name
+gemm_gated_config_name = gated_config_name
+
+
 # The same on torch tensors.  These run on the tensors' device and on torch's
 # current stream there; an output that is not given is allocated on it.  They
 # record no gradients.
@@ -647,3 +722,96 @@ def moe_mlp_fp8(x, logits, k, W1, S1, W2, S2, **route):
     q, s = quantize_fp8(h, act="swiglu")
     y = moe_matmul(q, W2, offsets, SA=s, SB=S2, out_dtype=x.dtype)
     return moe_combine(y, pos, weights)
+
+
+_ACTS = {"swiglu": GEMM_ACT_SWIGLU, "geglu": GEMM_ACT_GEGLU}
+
+
+def _act(act):
+    code = _ACTS.get(act)
+    if code is None:
+        raise ValueError("act must be 'swiglu' or 'geglu'")
+    return code
+
+
+def quantize_int8(x):
+    """8-bit integers and fp32 scales of x (M x K, bfloat16, float16 or
+    float32), one scale for each row: (q, S), S of M entries, as matmul_int8
+    takes them for tokens and, of a weight's rows, for channels.  q's rows are
+    padded to 16 bytes."""
+    _need(x, "x")
+    if x.dim() != 2:
+        raise ValueError("x must have two dimensions")
+    M, K = x.shape
+    q = torch.empty(M, max(16, -(-K // 16) * 16), device=x.device, dtype=torch.int8)
+    S = torch.empty(M, device=x.device, dtype=torch.float32)
+    _call(_lib.gemm_i8_quantize, x.device, M, K, x.data_ptr(), _ld(x, 1),
+          _type(x.dtype, "x", _FLOATS), q.data_ptr(), q.shape[1], S.data_ptr())
+    return (q if q.shape[1] == K else q[:, :K]), S
+
+
+def _scales_of(S, name, device, n):
+    _need(S, name, device, torch.float32, (n,))
+    return S.data_ptr()
+
+
+def matmul_int8(A, SA, B, SB, out=None, out_dtype=None, config=None):
+    """C (M x N) = A . B^T of int8 tensors A (M x K) and B (N x K) with scales
+    SA (M) and SB (N), as quantize_int8 returns them.  The sums are exact
+    integers.  out_dtype: bfloat16 (default), float16 or float32."""
+    _need(A, "A", None, torch.int8)
+    dev = A.device
+    _need(B, "B", dev, torch.int8)
+    if A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+        raise ValueError("need A (M x K) and B (N x K)")
+    (M, K), N = A.shape, B.shape[0]
+    sa, sb = _scales_of(SA, "SA", dev, M), _scales_of(SB, "SB", dev, N)
+    out = _out(out, (M, N), out_dtype or (torch.bfloat16 if out is None else out.dtype), dev)
+    _call(_lib.gemm_i8_ex, dev, None if config is None else config.encode(), M, N, K,
+          A.data_ptr(), _ld(A, 16), sa, B.data_ptr(), _ld(B, 16), sb, out.data_ptr(), _ld(out, 8),
+          _type(out.dtype, "out", _FLOATS))
+    return out
+
+
+def gated_matmul_int8(A, SA, W, SW, act="swiglu", out=None, out_dtype=None, config=None):
+    """H (M x F) = act(A . Wg^T) * (A . Wu^T) of int8 tensors A (M x K) and W (2F
+    x K: Wg's rows, then Wu's) with scales SA (M) and SW (2F).  act: "swiglu"
+    (silu) or "geglu" (gelu, tanh form).  out_dtype: bfloat16 (default), float16
+    or float32."""
+    _need(A, "A", None, torch.int8)
+    dev = A.device
+    _need(W, "W", dev, torch.int8)
+    if A.dim() != 2 or W.dim() != 2 or A.shape[1] != W.shape[1] or W.shape[0] % 2:
+        raise ValueError("need A (M x K) and W (2F x K)")
+    (M, K), F = A.shape, W.shape[0] // 2
+    sa, sw = _scales_of(SA, "SA", dev, M), _scales_of(SW, "SW", dev, 2 * F)
+    out = _out(out, (M, F), out_dtype or (torch.bfloat16 if out is None else out.dtype), dev)
+    _call(_lib.gemm_i8_gated_ex, dev, None if config is None else config.encode(), M, F, K,
+          A.data_ptr(), _ld(A, 16), sa, W.data_ptr(), _ld(W, 16), sw, _act(act), out.data_ptr(),
+          _ld(out, 8), _type(out.dtype, "out", _FLOATS))
+    return out
+
+
+def gated_matmul(x, W, act="swiglu", out=None, save=False, config=None):
+    """h (M x F) = act(g) * u with g = x . Wg^T and u = x . Wu^T: x (M x K) and W
+    (2F x K: Wg's rows, then Wu's) both bfloat16 or both float16.  act: "swiglu"
+    (silu) or "geglu" (gelu, tanh form).  save: also return gu (M x 2 x F), g and
+    u rounded to x's type, for gated_matmul_backward."""
+    _need(x, "x")
+    dev, code = x.device, _type(x.dtype, "x", (GEMM_TYPE_BF16, GEMM_TYPE_F16))
+    _need(W, "W", dev, x.dtype)
+    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1] or W.shape[0] % 2:
+        raise ValueError("need x (M x K) and W (2F x K)")
+    (M, K), F = x.shape, W.shape[0] // 2
+    out = _out(out, (M, F), x.dtype, dev)
+    gu, ldgu = None, 0
+    if save:
+        Fp = -(-F // 8) * 8
+        ldgu = max(16, 2 * Fp)
+        gu = torch.empty(M, ldgu, device=dev, dtype=x.dtype)
+    _call(_lib.gemm_gated_ex, dev, None if config is None else config.encode(), code, M, F, K,
+          x.data_ptr(), _ld(x, 8), W.data_ptr(), _ld(W, 8), _act(act), out.data_ptr(), _ld(out, 8),
+          None if gu is None else gu.data_ptr(), ldgu)
+    if not save:
+        return out
+    return out, gu.as_strided((M, 2, F), (ldgu, ldgu // 2, 1))

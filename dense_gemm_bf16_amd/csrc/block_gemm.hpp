@@ -5,6 +5,9 @@
 //   experts   the same for every row p of expert e's range
 //             [offsets[e], offsets[e+1]), with A's row rows[p] (or p) and
 //             expert e's B and SB; bf16 and fp16 operands carry no scales
+//   integer   C[m,n] = SA[m] SB[n] sum_k A[m,k] B[n,k] over 8-bit integers
+//   gated     H[m,f] = act(G[m,f]) U[m,f] with [G | U] a product over bf16,
+//             fp16 or 8-bit integers, B's rows f for G and F + f for U
 //
 // Two kernels.  block_tile_kernel stages BM x BN tiles through LDS for many
 // rows; block_row_kernel streams B straight into registers for few rows.
@@ -15,7 +18,9 @@
 // powers of two), so each K-step's partial sums of a 16 x 16 block start
 // from zero in one 16x16x128 MFMA and are added to the fp32 accumulators by
 // one FMA each with SA * SB: 4 FMAs (16 cycles of the SIMD's vector unit)
-// per MFMA of 32 cycles, issued while the next MFMA runs.
+// per MFMA of 32 cycles, issued while the next MFMA runs.  Sums of 8-bit
+// integers stay integers (in the same registers) over all of K and meet their
+// scales once, after the last step.
 //
 // Measured (MI355X): 8192 x 10240 x 8192 bf16 out 571-608 us, 2260-2410
 // TFLOP/s, the matrix cores 58 % busy; 1 x 8192 x 8192 12-13 us (memory); 64,
@@ -28,20 +33,24 @@
 namespace gemm {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kStepBytes = 128;     // bytes of a row in one K-step
 constexpr int kMaxKSteps = 1024;    // K-steps whose B scales are held in LDS
 constexpr int kScaleBlock = 128;    // rows of B (and columns of C) of one scale
 
 // Operand types.
-enum : int { kOpE4m3 = 0, kOpBf16 = 1, kOpF16 = 2 };
+enum : int { kOpE4m3 = 0, kOpBf16 = 1, kOpF16 = 2, kOpI8 = 3 };
+
+// What becomes of the sums: C, or (kGated) act(g) * u of paired columns.
+enum : int { kPlain = 0, kGated = 1 };
 
 struct BlockArgs {
   const uint8_t* A;
   const uint8_t* B;
   void* C;
-  const float* SA;         // SA[b * ldsa + row of A]
-  const float* SB;         // SB[(n / 128) * ldsb + b]
+  const float* SA;         // SA[b * ldsa + row of A]; integers: SA[row of A]
+  const float* SB;         // SB[(n / 128) * ldsb + b]; integers: SB[n]
   const int32_t* offsets;  // experts: E + 1 row offsets; null: dense
   const int32_t* rows;     // experts: A's row of each row of C, or null
   int64_t lda, ldb;        // bytes
@@ -59,6 +68,13 @@ struct BlockArgs {
   int32_t row_tiles;  // dense: row tiles; experts: an upper bound on them
   int32_t group_m;    // raster group height in tiles
   int32_t k_rot;      // K-step at which tile column j starts: j * k_rot, wrapped around
+  // gated: N counts the columns of H (in C), and
+  int64_t up_b;       // bytes from B's row f (gate) to its row F + f (up)
+  int64_t up_sb;      // floats from SB's entry f to its entry F + f
+  void* GU;           // where g and u go as well, or null
+  int64_t ldgu;       // elements from row to row of GU
+  int64_t up_gu;      // elements from g to u in a row of GU
+  int32_t geglu;      // act: 1: gelu (tanh form), 0: silu
 };
 
 // ------------------------------------------------------------- row tiles
@@ -182,6 +198,14 @@ struct Step {
       const i32x8 va = {(int)a.v[0][0], (int)a.v[0][1], (int)a.v[0][2], (int)a.v[0][3],
                         (int)a.v[1][0], (int)a.v[1][1], (int)a.v[1][2], (int)a.v[1][3]};
       return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(vb, va, c, 0, 0, 0, 0, 0, 0);
+    } else if constexpr (OP == kOpI8) {
+      // exact 32-bit integer sums, held as their bits
+      i32x4 d = __builtin_bit_cast(i32x4, c);
+#pragma unroll
+      for (int h = 0; h < kRegs; ++h)
+        d = __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b.v[h]),
+                                                  __builtin_bit_cast(i32x4, a.v[h]), d, 0, 0, 0);
+      return __builtin_bit_cast(f32x4, d);
     } else {
 #pragma unroll
       for (int h = 0; h < kRegs; ++h) {
@@ -197,6 +221,15 @@ struct Step {
   }
 };
 
+// The sum of two partial sums (of integers: of the integers they hold).
+template <int OP>
+__device__ __forceinline__ f32x4 add_sums(f32x4 x, f32x4 y) {
+  if constexpr (OP == kOpI8)
+    return __builtin_bit_cast(f32x4, __builtin_bit_cast(i32x4, x) + __builtin_bit_cast(i32x4, y));
+  else
+    return x + y;
+}
+
 // One LDS-DMA load of 4 bytes per lane (see dma16).
 __device__ __forceinline__ void dma4(const u32x4& rsrc, uint32_t lds_addr, uint32_t voff,
                                      uint32_t soff) {
@@ -208,6 +241,202 @@ __device__ __forceinline__ void dma4(const u32x4& rsrc, uint32_t lds_addr, uint3
       : "memory");
 }
 
+// ---------------------------------------------------------------- epilogue
+
+// SB of columns n .. n+3 (0 past the last one).
+__device__ __forceinline__ f32x4 column_scales(const float* sb, int n, int N) {
+  f32x4 v;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) v[r] = n + r < N ? sb[n + r] : 0.0f;
+  return v;
+}
+
+// Integer sums to (fp32(sum) * SA[m]) * SB[n], three roundings; other types'
+// are left.  acc[i][j]: row i * 16 + lane % 16 from m_base on, columns j * 16
+// + 4 (lane / 16) .. + 3 from n_base on.
+template <int OP, int FM, int FN>
+__device__ __forceinline__ void scale_sums(const BlockArgs& a, f32x4 (&acc)[FM][FN], int m_end,
+                                           int m_base, int n_base, int lane) {
+  if constexpr (OP == kOpI8) {
+    f32x4 sb[FN];
+#pragma unroll
+    for (int j = 0; j < FN; ++j) sb[j] = column_scales(a.SB, n_base + j * 16 + 4 * (lane >> 4), a.N);
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int m = m_base + i * 16 + (lane & 15);
+      const float sa = m < m_end ? a.SA[m] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const i32x4 sum = __builtin_bit_cast(i32x4, acc[i][j]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = (float)sum[r] * sa * sb[j][r];
+      }
+    }
+  }
+}
+
+// act(g) * u, with act(g) = g sigmoid(z): z = g for silu; for gelu in its tanh
+// form, g (1 + tanh(y)) / 2 = g sigmoid(2 y) with y = sqrt(2 / pi) (g +
+// 0.044715 g^3).  For a 16-bit H, sigmoid(z) = 1 / (1 + 2^(-z log2 e)) by the
+// vector unit's 2^x and 1/x (1 ulp each); the exponent's rounding is |z| 2^-24
+// relative, 2^-17 where the result nears fp32's smallest, against the 2^-9 or
+// 2^-12 of H's own rounding.  An fp32 H shows it, so there the exponent's
+// rounding error is made up for and the power is of -|z|, which neither
+// overflows nor cancels: a few ulp for every z (results below 2^-120 may be
+// zero).  Six and fourteen operations: with the longer form everywhere the
+// activation would take 5 % of a bf16 product's time and 9 % of an integer
+// one's at 8192 x 14336 x 4096.
+constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.69314718f;
+
+__device__ __forceinline__ float gate_argument(float g, bool geglu) {
+  const float y = g * __builtin_fmaf(0.0713548163f, g * g, 1.59576912f);
+  return geglu ? y : g;
+}
+
+// exp(-x) for x >= 0 (x is cut at 200, past which it is zero).
+__device__ __forceinline__ float exp_of_minus(float x) {
+  x = fminf(x, 200.0f);
+  const float t = x * -kLog2e;
+  const float low = __builtin_fmaf(x, -kLog2e, -t) - x * kLog2eLow;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, low * kLn2, e);
+}
+
+template <int OUT>
+__device__ __forceinline__ float gate(float g, float u, bool geglu) {
+  const float z = gate_argument(g, geglu);
+  if constexpr (OUT == kStoreF32) {
+    const float e = exp_of_minus(fabsf(z));
+    const float r = 1.0f / (1.0f + e);
+    return g * (z >= 0.0f ? r : e * r) * u;
+  } else {
+    return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -kLog2e)) * u;
+  }
+}
+
+// A workgroup's BM x COLS values, staged in LDS by rows and stored in whole
+// 16-byte pieces, COLS * size bytes of a row by consecutive lanes.  Waves with
+// `mine` write v[i][j]: row wm * WAVE_M + i * 16 + lane % 16, columns (wn * FN +
+// j) * 16 + 4 (lane / 16) .. + 3.  Every wave of the workgroup calls it; the
+// LDS region is free when it is called and in use when it returns.
+template <int BM, int COLS, int THREADS, int OUT, int FM, int FN>
+__device__ __forceinline__ void store_staged(lds_u8* region, const f32x4 (&v)[FM][FN], bool mine,
+                                             int wm, int wn, int lane, void* out, int64_t ld,
+                                             int m0, int m_end, int n0, int N) {
+  constexpr int kE = OUT == kStoreF32 ? 4 : 2, kPer = 16 / kE;
+  constexpr int kRB = COLS * kE, kChunks = kRB / 16;
+  constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
+  static_assert(kChunks >= 4 && (kChunks & (kChunks - 1)) == 0, "a power of two");
+  static_assert(THREADS % kChunks == 0, "whole rows a pass");
+  // rows of 64 and 128 bytes: the bits of the row that tell rows of one
+  // 256-byte stretch of banks from another
+  auto at = [](int r, int c) {
+    const int sw = kChunks >= 16 ? r : kChunks == 8 ? r >> 1 : r >> 2;
+    return (uint32_t)(r * kRB + ((c ^ (sw & kMask)) << 4));
+  };
+  if (mine) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = (wm * FM + i) * 16 + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int q = (wn * FN + j) * 4 + (lane >> 4);  // column / 4
+        if constexpr (kE == 4)
+          *(__attribute__((address_space(3))) f32x4*)(region + at(r, q)) = v[i][j];
+        else
+          *(__attribute__((address_space(3))) u32x2*)(region + at(r, q >> 1) + ((q & 1) << 3)) =
+              pack_quad<OUT>(v[i][j]);
+      }
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  const int c = (int)threadIdx.x % kChunks, col = n0 + c * kPer;
+#pragma unroll
+  for (int r0 = 0; r0 < BM; r0 += THREADS / kChunks) {
+    const int r = r0 + (int)threadIdx.x / kChunks;
+    if (BM % (THREADS / kChunks) != 0 && r >= BM) break;
+    const u32x4 x = *(const lds_u32x4*)(region + at(r, c));
+    if (m0 + r >= m_end || col >= N) continue;
+    uint8_t* dst = (uint8_t*)out + ((int64_t)(m0 + r) * ld + col) * kE;
+    if (col + kPer <= N) {
+      __builtin_nontemporal_store(x, (u32x4*)dst);
+      continue;
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) {
+      if (col + e >= N) break;
+      if constexpr (kE == 4)
+        ((uint32_t*)dst)[e] = x[e];
+      else
+        ((uint16_t*)dst)[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
+// H = act(g) * u (rounded once, from the unrounded sums) and, where GU is
+// asked for, g and u rounded to H's type.  Waves with `mine` hold the sums,
+// g in the even fragments of their columns and u in the odd ones.
+template <typename Cfg, int OP, int OUT, int THREADS>
+__device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
+                                             f32x4 (&acc)[Cfg::kFragM][Cfg::kFragN], int m0,
+                                             int m_end, int f0, int wm, int wn, int lane,
+                                             bool mine) {
+  constexpr int FM = Cfg::kFragM, FN = Cfg::kFragN / 2, BM = Cfg::kBM, COLS = Cfg::kBN / 2;
+  f32x4 h[FM][FN];
+  if (mine) {
+    if constexpr (OP == kOpI8) {
+      f32x4 sg[FN], su[FN];
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int f = f0 + (wn * FN + j) * 16 + 4 * (lane >> 4);
+        sg[j] = column_scales(a.SB, f, a.N);
+        su[j] = column_scales(a.SB + a.up_sb, f, a.N);
+      }
+#pragma unroll
+      for (int i = 0; i < FM; ++i) {
+        const int m = m0 + (wm * FM + i) * 16 + (lane & 15);
+        const float sa = m < m_end ? a.SA[m] : 0.0f;
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const i32x4 g = __builtin_bit_cast(i32x4, acc[i][2 * j]);
+          const i32x4 u = __builtin_bit_cast(i32x4, acc[i][2 * j + 1]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            acc[i][2 * j][r] = (float)g[r] * sa * sg[j][r];
+            acc[i][2 * j + 1][r] = (float)u[r] * sa * su[j][r];
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          h[i][j][r] = gate<OUT>(acc[i][2 * j][r], acc[i][2 * j + 1][r], a.geglu != 0);
+  }
+  // every wave is done with the ring
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  store_staged<BM, COLS, THREADS, OUT>(region, h, mine, wm, wn, lane, a.C, a.ldc, m0, m_end, f0,
+                                       a.N);
+  if constexpr (OP != kOpI8) {
+    if (a.GU != nullptr) {
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+#pragma unroll
+        for (int i = 0; i < FM; ++i)
+#pragma unroll
+          for (int j = 0; j < FN; ++j) h[i][j] = acc[i][2 * j + p];
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        store_staged<BM, COLS, THREADS, OUT>(region, h, mine, wm, wn, lane,
+                                             (uint16_t*)a.GU + p * a.up_gu, a.ldgu, m0, m_end, f0,
+                                             a.N);
+      }
+    }
+  }
+}
+
 // ----------------------------------------------------------- tile kernel
 
 // BM x BN tiles, WM x WN waves, a ring of S LDS slots of 128-byte rows
@@ -216,7 +445,14 @@ __device__ __forceinline__ void dma4(const u32x4& rsrc, uint32_t lds_addr, uint3
 // barrier (which also frees the slot of step X - 1), then the wave's MFMAs
 // with the loads of step X + S - 1 spread between them.  Every step issues
 // the same loads, those past K reading zeros, so the waits count them.
-template <int BM, int BN, int WM, int WN, int WK, int S, int OP, int OUT>
+//
+// MODE kGated: a tile's BN rows of B are BN / 2 rows of the gate and the BN /
+// 2 of the same columns of the up projection, 16 and 16 in turn, so that a
+// wave holds g and u of one element of H in the same lane and register and
+// the activation costs no exchange.  NT: B's loads non-temporal, for one row
+// of tiles, where no other workgroup reads the same B.
+template <int BM, int BN, int WM, int WN, int WK, int S, int OP, int OUT, int MODE = kPlain,
+          bool NT = false>
 __global__ __attribute__((amdgpu_flat_work_group_size(WM * WN * WK * 64, WM * WN * WK * 64),
                           amdgpu_waves_per_eu(2))) void
 block_tile_kernel(BlockArgs a) {
@@ -264,7 +500,10 @@ block_tile_kernel(BlockArgs a) {
   const int gsz = min(row_tiles - first, a.group_m);
   const int in = logical - gid * span;
   const int rt = first + in % gsz;
-  const int tn = in / gsz, n0 = tn * BN;
+  constexpr bool kPairs = MODE == kGated;
+  constexpr int kCols = kPairs ? BN / 2 : BN;  // columns of C
+  static_assert(!kPairs || (RPI % 32 == 0 && FN % 2 == 0), "16 and 16 rows of B in turn");
+  const int tn = in / gsz, n0 = tn * kCols;
   RowTile tile;
   if (a.offsets) {
     if (!find_row_tile(a, BM, rt, lane, tile)) return;
@@ -273,13 +512,16 @@ block_tile_kernel(BlockArgs a) {
   }
   const int m0 = tile.begin;
   const int rows_a = min(BM, tile.end - m0);
-  const int rows_b = min(BN, a.N - n0);
+  const int rows_b = min(kCols, a.N - n0);
 
   // ---- loads -------------------------------------------------------------
   const bool gather = a.rows != nullptr;
   const u32x4 rsrc_a = gather ? make_rsrc(a.A, (uint32_t)((int64_t)a.a_rows * a.lda))
                               : make_rsrc(a.A + (int64_t)m0 * a.lda, (uint32_t)(rows_a * a.lda));
-  const u32x4 rsrc_b = make_rsrc(a.B + tile.expert * a.stride_b + (int64_t)n0 * a.ldb,
+  // (gated: a wave loads 8 rows at a time, all of the gate or all of the up
+  // projection)
+  const int64_t up = kPairs ? ((wave >> 1) & 1) * a.up_b : 0;
+  const u32x4 rsrc_b = make_rsrc(a.B + tile.expert * a.stride_b + up + (int64_t)n0 * a.ldb,
                                  (uint32_t)(rows_b * a.ldb));
   const int r0 = tid / 8;
   const int chunk = (tid & 7) ^ swz<3, 8>(r0);
@@ -291,7 +533,8 @@ block_tile_kernel(BlockArgs a) {
       const int src = row < rows_a ? (gather ? source_row(a, m0 + row) : row) : -1;
       voff[i] = src >= 0 ? (uint32_t)(src * (int)a.lda + chunk * 16) : kOOB;
     } else {
-      voff[i] = row < rows_b ? (uint32_t)(row * (int)a.ldb + chunk * 16) : kOOB;
+      const int src = kPairs ? row / 32 * 16 + row % 16 : row;
+      voff[i] = src < rows_b ? (uint32_t)(src * (int)a.ldb + chunk * 16) : kOOB;
     }
   }
   // this lane's row scale; waves past the tile's rows load the same ones
@@ -332,7 +575,10 @@ block_tile_kernel(BlockArgs a) {
     // past K, and in the steps past the last one, a load reads zeros: no
     // branch splits the loop body
     const uint32_t v = k >= a.k_steps - (past_k ? 1 : 0) ? kOOB : voff[i];
-    dma16(i < LA ? rsrc_a : rsrc_b, dst, v, (uint32_t)(k * kStepBytes));
+    if (NT && i >= LA)
+      dma16<true>(rsrc_b, dst, v, (uint32_t)(k * kStepBytes));
+    else
+      dma16(i < LA ? rsrc_a : rsrc_b, dst, v, (uint32_t)(k * kStepBytes));
   };
   auto load_scales = [&](int k, int slot) __attribute__((always_inline)) {
     if constexpr (kScaled) {
@@ -631,18 +877,36 @@ block_tile_kernel(BlockArgs a) {
       for (int i = 0; i < FM * FN; ++i) mine[i * 64] = acc[i / FN][i % FN];
     }
     asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if constexpr (kPairs) {
+      if (kg == 0) {
+#pragma unroll
+        for (int g = 1; g < WK; ++g)
+#pragma unroll
+          for (int i = 0; i < FM * FN; ++i)
+            acc[i / FN][i % FN] =
+                add_sums<OP>(acc[i / FN][i % FN], mine[g * (Cfg::kLdsBytes / 16) + i * 64]);
+      }
+      finish_gated<Cfg, OP, OUT, T * WK>(a, (lds_u8*)smem_raw, acc, m0, tile.end, n0, wm, wn, lane,
+                                         kg == 0);
+      return;
+    }
     if (kg > 0) return;
 #pragma unroll
     for (int g = 1; g < WK; ++g)
 #pragma unroll
       for (int i = 0; i < FM * FN; ++i)
-        acc[i / FN][i % FN] += mine[g * (Cfg::kLdsBytes / 16) + i * 64];
+        acc[i / FN][i % FN] =
+            add_sums<OP>(acc[i / FN][i % FN], mine[g * (Cfg::kLdsBytes / 16) + i * 64]);
+    scale_sums<OP, FM, FN>(a, acc, tile.end, m0 + wm * Cfg::kWaveM, n0 + wn * Cfg::kWaveN, lane);
     // (each wave stages C in its own part of the first group's ring: no
     // barrier, which the other groups' waves would not reach)
     finish_tile<Cfg, OUT, false, Cfg::kLdsBytes, false>(c, smem, wave, m0, n0, acc,
                                                         m0 + wm * Cfg::kWaveM,
                                                         n0 + wn * Cfg::kWaveN, lane, 0);
+  } else if constexpr (kPairs) {
+    finish_gated<Cfg, OP, OUT, T>(a, smem, acc, m0, tile.end, n0, wm, wn, lane, true);
   } else {
+    scale_sums<OP, FM, FN>(a, acc, tile.end, m0 + wm * Cfg::kWaveM, n0 + wn * Cfg::kWaveN, lane);
     finish_tile<Cfg, OUT, false>(c, smem, wave, m0, n0, acc, m0 + wm * Cfg::kWaveM,
                                  n0 + wn * Cfg::kWaveN, lane, 0);
   }
@@ -664,11 +928,16 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, ui
 // K-step.  Operands go from global memory into registers in the MFMA's own
 // layout (a lane holds two 16-byte chunks of its row), U steps ahead; the
 // waves' sums meet in LDS and are added in the order of the waves.
-template <int FM, int FN, int W, int U, int OP, int OUT>
+//
+// MODE kGated: fragments of B in turn from the gate's and the up projection's
+// rows (FN = 2: 16 columns of H).
+template <int FM, int FN, int W, int U, int OP, int OUT, int MODE = kPlain>
 __global__ __attribute__((amdgpu_flat_work_group_size(W * 64, W * 64))) void
 block_row_kernel(BlockArgs a) {
   constexpr bool kScaled = OP == kOpE4m3;
-  constexpr int BM = 16 * FM, BN = 16 * FN;
+  constexpr bool kPairs = MODE == kGated;
+  static_assert(!kPairs || FN == 2, "one fragment of the gate, one of the up projection");
+  constexpr int BM = 16 * FM, BN = kPairs ? 16 : 16 * FN;
   static_assert(kScaleBlock % BN == 0, "the tile's columns share one scale");
   __shared__ f32x4 sums[W][FM * FN][64];
 
@@ -693,6 +962,8 @@ block_row_kernel(BlockArgs a) {
              : buffer_of(a.A + (int64_t)m0 * a.lda, (uint32_t)(rows_a * a.lda));
   const __amdgpu_buffer_rsrc_t rsrc_b = buffer_of(a.B + tile.expert * a.stride_b + (int64_t)n0 * a.ldb,
                                  (uint32_t)(rows_b * a.ldb));
+  const __amdgpu_buffer_rsrc_t rsrc_u =
+      kPairs ? buffer_of(a.B + a.up_b + (int64_t)n0 * a.ldb, (uint32_t)(rows_b * a.ldb)) : rsrc_b;
   uint32_t va[FM], vb[FN], vs[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -703,10 +974,10 @@ block_row_kernel(BlockArgs a) {
   }
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    const int row = j * 16 + lrow;
+    const int row = kPairs ? lrow : j * 16 + lrow;
     vb[j] = row < rows_b ? (uint32_t)(row * (int)a.ldb + lchunk) : kOOB;
   }
-  const float* sb_row = a.SB + tile.expert * a.stride_sb + (int64_t)(n0 / kScaleBlock) * a.ldsb;
+  const float* sb_row = !kScaled ? nullptr : a.SB + tile.expert * a.stride_sb + (int64_t)(n0 / kScaleBlock) * a.ldsb;
 
   const int rot =
       a.k_steps > 0 ? __builtin_amdgcn_readfirstlane((n0 / BN) * a.k_rot % a.k_steps) : 0;
@@ -731,8 +1002,8 @@ block_row_kernel(BlockArgs a) {
     const std::false_type keep{};
 #pragma unroll
     for (int j = 0; j < FN; ++j) {
-      s.fb[j][0] = get(rsrc_b, vb[j], in0, 0, nt);
-      s.fb[j][1] = get(rsrc_b, vb[j], in1, 64, nt);
+      s.fb[j][0] = get(kPairs && j ? rsrc_u : rsrc_b, vb[j], in0, 0, nt);
+      s.fb[j][1] = get(kPairs && j ? rsrc_u : rsrc_b, vb[j], in1, 64, nt);
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -813,14 +1084,49 @@ block_row_kernel(BlockArgs a) {
 #pragma unroll
     for (int j = 0; j < FN; ++j) sums[wave][i * FN + j][lane] = acc[i][j];
   __syncthreads();
-  for (int q = tid; q < FM * FN * 64; q += W * 64) {
-    const int f = q >> 6, l = q & 63;
+  auto total = [&](int f, int l) __attribute__((always_inline)) {
     f32x4 v = sums[0][f][l];
 #pragma unroll
-    for (int w = 1; w < W; ++w) v += sums[w][f][l];
-    const int row = (f / FN) * 16 + (l & 15);
-    if (row < rows_a)
-      store_quad<OUT>(a.C, a.ldc, v, m0 + row, n0 + (f % FN) * 16 + 4 * (l >> 4), a.N);
+    for (int w = 1; w < W; ++w) v = add_sums<OP>(v, sums[w][f][l]);
+    return v;
+  };
+  auto scaled = [&](const f32x4& v, const float* sb, int row, int n) __attribute__((always_inline)) {
+    if constexpr (OP == kOpI8) {
+      const i32x4 sum = __builtin_bit_cast(i32x4, v);
+      const f32x4 s = column_scales(sb, n, a.N);
+      const float sa = a.SA[m0 + row];
+      f32x4 x;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) x[r] = (float)sum[r] * sa * s[r];
+      return x;
+    } else {
+      return v;
+    }
+  };
+  if constexpr (kPairs) {
+    for (int q = tid; q < FM * 64; q += W * 64) {
+      const int i = q >> 6, l = q & 63;
+      const int row = i * 16 + (l & 15), n = n0 + 4 * (l >> 4);
+      if (row >= rows_a) continue;
+      const f32x4 g = scaled(total(2 * i, l), a.SB, row, n);
+      const f32x4 u = scaled(total(2 * i + 1, l), a.SB + a.up_sb, row, n);
+      f32x4 h;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) h[r] = gate<OUT>(g[r], u[r], a.geglu != 0);
+      store_quad<OUT>(a.C, a.ldc, h, m0 + row, n, a.N);
+      if constexpr (OP != kOpI8) {
+        if (a.GU != nullptr) {
+          store_quad<OUT>(a.GU, a.ldgu, g, m0 + row, n, a.N);
+          store_quad<OUT>((uint16_t*)a.GU + a.up_gu, a.ldgu, u, m0 + row, n, a.N);
+        }
+      }
+    }
+  } else {
+    for (int q = tid; q < FM * FN * 64; q += W * 64) {
+      const int f = q >> 6, l = q & 63;
+      const int row = (f / FN) * 16 + (l & 15), n = n0 + (f % FN) * 16 + 4 * (l >> 4);
+      if (row < rows_a) store_quad<OUT>(a.C, a.ldc, scaled(total(f, l), a.SB, row, n), m0 + row, n, a.N);
+    }
   }
 }
 

@@ -57,4 +57,12 @@ struct QuantArgs {
 hipError_t launch_quantize_rows(const QuantArgs& a, int x_type, bool swiglu, hipStream_t s);
 hipError_t launch_quantize_blocks(const QuantArgs& a, int x_type, hipStream_t s);
 
+struct Int8QuantArgs {
+  const void* x;
+  uint8_t* q;
+  float* s;
+  int64_t M, K, ldx, ldq;
+};
+hipError_t launch_quantize_int8(const Int8QuantArgs& a, int x_type, hipStream_t s);
+
 }  // namespace gemm

@@ -1,0 +1,315 @@
+// C-ABI front end of the integer products and the gated products: argument
+// checks, the choice of kernel shape, launch.  The contract of every entry
+// point is stated in include/gemm_bf16.h.  Nothing here allocates or throws.
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "../../include/gemm_bf16.h"
+#include "gated_launch.hpp"
+#include "gemm_internal.h"
+
+namespace gemm {
+namespace {
+
+constexpr int64_t k2G = int64_t(1) << 31;
+constexpr int64_t kRangeLimit = k2G - 4096;
+constexpr int64_t kMaxIntK = 131071;  // 2^14 K stays below 2^31
+
+// ------------------------------------------------------- choice of shape
+// As the block products choose theirs: the shape that a model of a launch's
+// time makes cheapest.  `units` workgroups on CUs that hold `resident` of them
+// each make passes of 256 * resident; a pass costs steps * step + tile (steps:
+// K-steps of a workgroup's wave group; tile: first loads and epilogue), a last
+// pass with a fraction f of its workgroups part + (1 - part) * f of that; the
+// whole takes at least as long as reading B.
+struct Cost {
+  float step, tile, part, base;  // us, us, share, us
+};
+struct Shape {
+  GatedConfig built;
+  int k_groups, resident;
+  int gated_rows;  // rows of B of a workgroup with paired columns
+  Cost cost;
+};
+const Shape kShapes[] = {
+#define ROW(NAME, A, B, C, D, E, S, RESIDENT, ...)                                        \
+  {{#NAME, A, B, (C) * (D) * (E) * 64, (B) / (D) / 16 % 2 == 0,                           \
+    &launch_gated_tile<A, B, C, D, E, S>}, E, RESIDENT, B, __VA_ARGS__},
+    ROW(b256x256, 256, 256, 2, 4, 1, 2, 1, {1.586f, 6.15f, 0.69f, 2.19f})
+    ROW(b256x128, 256, 128, 4, 2, 1, 3, 1, {0.932f, 4.29f, 0.76f, 1.51f})
+    ROW(b128x128, 128, 128, 2, 2, 1, 2, 2, {1.032f, 3.95f, 0.55f, 2.44f})
+    ROW(b128x128k2, 128, 128, 2, 2, 2, 2, 1, {1.172f, 5.23f, 0.83f, 1.37f})
+    ROW(b64x128k2, 64, 128, 2, 2, 2, 3, 1, {0.873f, 3.68f, 0.75f, 1.39f})
+    ROW(b64x64, 64, 64, 2, 2, 1, 4, 2, {0.492f, 3.41f, 0.67f, 1.06f})
+    ROW(b64x64k2, 64, 64, 2, 2, 2, 4, 1, {0.528f, 3.97f, 0.84f, 0.44f})
+    ROW(b32x128, 32, 128, 1, 4, 1, 3, 2, {0.645f, 3.14f, 0.62f, 0.83f})
+    ROW(b32x64k4, 32, 64, 2, 2, 4, 3, 1, {0.678f, 4.52f, 0.88f, 0.00f})
+    ROW(b32x32k4, 32, 32, 2, 2, 4, 4, 1, {0.508f, 3.15f, 0.96f, 1.30f})
+#undef ROW
+    {{"r16x16", 16, 16, 512, true, &launch_gated_row<1, 1, 8, 4>}, 8, 4, 32,
+     {2.435f, 1.11f, 0.24f, 3.08f}},
+};
+constexpr double kStreamMBPerUs = 5.2, kStreamBaseUs = 2.5;
+
+// A product as the choice sees it: rows of A and of B, bytes of a row and from
+// row to row, and whether B's rows are paired.
+struct Product {
+  int64_t M, rows_b, k_bytes, lda, ldb;
+  bool gated;
+};
+
+int rows_of_b(const Shape& s, bool gated) { return gated ? s.gated_rows : s.built.bn; }
+
+int64_t tiles_n(const Shape& s, const Product& p, int64_t rows_b) {
+  const int bn = rows_of_b(s, p.gated);
+  return (rows_b + bn - 1) / bn;
+}
+
+// Whether a shape can run rows_b rows of B (see the block products).
+bool fits(const Shape& s, const Product& p, int64_t rows_b) {
+  if (p.gated && !s.built.gated) return false;
+  if (rows_of_b(s, p.gated) * p.ldb >= kRangeLimit || s.built.bm * p.lda >= kRangeLimit) return false;
+  return (p.M + s.built.bm - 1) / s.built.bm * tiles_n(s, p, rows_b) < 2 * k2G / s.built.threads;
+}
+
+double model_time(const Shape& s, const Product& p, int64_t rows_b) {
+  const Cost& c = s.cost;
+  const double units =
+      (double)((p.M + s.built.bm - 1) / s.built.bm) * (double)tiles_n(s, p, rows_b);
+  const double pass = 256.0 * s.resident;
+  double passes = (double)(int64_t)(units / pass);
+  const double rest = units / pass - passes;
+  if (rest > 0) passes += c.part + (1 - c.part) * rest;
+  const int64_t k_steps = (p.k_bytes + kStepBytes - 1) / kStepBytes;
+  const double steps = (double)((k_steps + s.k_groups - 1) / s.k_groups);
+  const double t = passes * (steps * c.step + c.tile) + c.base;
+  const double floor_us =
+      (double)rows_b * (double)p.k_bytes * 1e-6 / kStreamMBPerUs + kStreamBaseUs;
+  return sqrt(sqrt(t * t * t * t + floor_us * floor_us * floor_us * floor_us));
+}
+
+const Shape* cheapest(const Product& p, int64_t rows_b, double* time) {
+  const Shape* best = nullptr;
+  for (const Shape& s : kShapes) {
+    if (!fits(s, p, rows_b)) continue;
+    const double t = model_time(s, p, rows_b);
+    if (best && t >= *time) continue;
+    best = &s;
+    *time = t;
+  }
+  return best;
+}
+
+// `shape` on the first split_b rows of B (all of them, or those that fill its
+// whole passes over the CUs), `tail` on the rest.  No shape: none can.
+struct DensePlan {
+  const Shape* shape;
+  const Shape* tail;
+  int64_t split_b;
+};
+
+DensePlan choose(const Product& p) {
+  double best = 0;
+  DensePlan plan{cheapest(p, p.rows_b, &best), nullptr, p.rows_b};
+  if (p.M < 1 || !plan.shape) return plan;
+  best *= 0.97;
+  for (const Shape& s : kShapes) {
+    const int64_t rows = (p.M + s.built.bm - 1) / s.built.bm, cols = tiles_n(s, p, p.rows_b);
+    const int64_t pass = 256 * s.resident;
+    if (rows > pass) continue;
+    const int64_t head = rows * cols / pass * pass / rows * rows_of_b(s, p.gated) / 128 * 128;
+    if (head <= 0 || head >= p.rows_b || !fits(s, p, head)) continue;
+    const double t1 = model_time(s, p, head);
+    if (t1 >= best) continue;
+    double t2 = 0;
+    const Shape* tail = cheapest(p, p.rows_b - head, &t2);
+    if (!tail || t1 + t2 >= best) continue;
+    best = t1 + t2;
+    plan = DensePlan{&s, tail, head};
+  }
+  return plan;
+}
+
+const Shape* shape_named(const char* name) {
+  for (const Shape& s : kShapes)
+    if (strcmp(s.built.name, name) == 0) return &s;
+  return nullptr;
+}
+
+bool misaligned(const void* p, int bytes) { return ((uintptr_t)p & (bytes - 1)) != 0; }
+bool is_float_type(int type) {
+  return type == GEMM_TYPE_BF16 || type == GEMM_TYPE_F16 || type == GEMM_TYPE_F32;
+}
+int store_of(int type) {
+  return type == GEMM_TYPE_F32 ? kStoreF32 : type == GEMM_TYPE_F16 ? kStoreF16 : kStoreBf16;
+}
+int op_of(int type) {
+  return type == GEMM_TYPE_I8 ? kOpI8 : type == GEMM_TYPE_F16 ? kOpF16 : kOpBf16;
+}
+int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+
+// C (M x N) of A and B's N rows, or with `gated` H (M x N) of B's 2 N rows.
+int dense_product(const char* config, int type, bool gated, int64_t M, int64_t N, int64_t K,
+                  const void* A, int64_t lda, const float* SA, const void* B, int64_t ldb,
+                  const float* SB, int act, void* C, int64_t ldc, int c_type, void* GU,
+                  int64_t ldgu, void* stream) {
+  const bool ints = type == GEMM_TYPE_I8;
+  if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
+  if (!ints && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return GEMM_ERR_INVALID_ARG;
+  if (!is_float_type(c_type) || (!ints && c_type != type)) return GEMM_ERR_INVALID_ARG;
+  if (gated && act != GEMM_ACT_SWIGLU && act != GEMM_ACT_GEGLU) return GEMM_ERR_INVALID_ARG;
+  if (M >= k2G || N >= (gated ? k2G / 2 : k2G) || K >= k2G / 2 || lda >= k2G || ldb >= k2G ||
+      ldc >= (int64_t(1) << 40) || ldgu >= (int64_t(1) << 40) || (ints && K > kMaxIntK))
+    return GEMM_ERR_UNSUPPORTED;
+  if (lda < K || ldb < K || ldc < N || (GU && ldgu < 2 * up8(N))) return GEMM_ERR_INVALID_ARG;
+  const bool work = M > 0 && N > 0;
+  if (work && (!C || (K > 0 && (!A || !B)) || (ints && (!SA || !SB)))) return GEMM_ERR_INVALID_ARG;
+  const int es = ints ? 1 : 2;
+  if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 16) || misaligned(GU, 16) ||
+      misaligned(SA, 4) || misaligned(SB, 4) || ((lda | ldb) & (16 / es - 1)) != 0 ||
+      (ldc & 7) != 0 || (GU && (ldgu & 7) != 0))
+    return GEMM_ERR_MISALIGNED;
+
+  const Product p{M, gated ? 2 * N : N, K * es, lda * es, ldb * es, gated};
+  DensePlan plan{nullptr, nullptr, p.rows_b};
+  if (config && config[0]) {
+    plan.shape = shape_named(config);
+    if (plan.shape && !fits(*plan.shape, p, p.rows_b)) plan.shape = nullptr;
+  } else {
+    plan = choose(p);
+  }
+  if (!plan.shape) return GEMM_ERR_UNSUPPORTED;
+  if (!work) return GEMM_OK;
+
+  BlockArgs a{};
+  a.A = (const uint8_t*)A;
+  a.B = (const uint8_t*)B;
+  a.C = C;
+  a.SA = SA;
+  a.SB = SB;
+  a.lda = p.lda;
+  a.ldb = p.ldb;
+  a.ldc = ldc;
+  a.M = (int32_t)M;
+  a.kbytes = (int32_t)p.k_bytes;
+  a.a_rows = (int32_t)M;
+  a.E = 1;
+  a.k_steps = (int32_t)((p.k_bytes + kStepBytes - 1) / kStepBytes);
+  a.group_m = 4;
+  if (gated) {
+    a.up_b = N * p.ldb;
+    a.up_sb = N;
+    a.GU = GU;
+    a.ldgu = ldgu;
+    a.up_gu = up8(N);
+    a.geglu = act == GEMM_ACT_GEGLU;
+  }
+  auto launch = [&](const Shape& s, int64_t rows_b) {
+    const int64_t row_tiles = (M + s.built.bm - 1) / s.built.bm;
+    a.N = (int32_t)(gated ? rows_b / 2 : rows_b);
+    a.tiles_n = (int32_t)tiles_n(s, p, rows_b);
+    a.row_tiles = (int32_t)row_tiles;
+    // (one row of tiles: see the block products)
+    a.k_rot = row_tiles == 1 ? 3 : 0;
+    return s.built.launch(a, (int)(row_tiles * a.tiles_n), (hipStream_t)stream, op_of(type),
+                          store_of(c_type), gated, row_tiles == 1);
+  };
+  hipError_t e = launch(*plan.shape, plan.split_b);
+  if (e == hipSuccess && plan.tail) {
+    const int64_t col = gated ? plan.split_b / 2 : plan.split_b;
+    a.B += col * p.ldb;
+    if (SB) a.SB += col;
+    a.C = (uint8_t*)C + col * (c_type == GEMM_TYPE_F32 ? 4 : 2);
+    if (GU) a.GU = (uint16_t*)GU + col;
+    e = launch(*plan.tail, p.rows_b - plan.split_b);
+  }
+  return e == hipSuccess ? GEMM_OK : hip_fail(e);
+}
+
+thread_local char g_plan_name[64];
+
+const char* plan_name(int type, bool gated, int64_t M, int64_t N, int64_t K) {
+  const bool ints = type == GEMM_TYPE_I8;
+  if (M < 0 || N < 0 || K < 0 || M >= k2G || N >= (gated ? k2G / 2 : k2G) || K >= k2G / 2 ||
+      (ints && K > kMaxIntK) || (!ints && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16))
+    return "invalid";
+  const DensePlan p = choose(Product{M, gated ? 2 * N : N, ints ? K : 2 * K, 0, 0, gated});
+  if (!p.shape) return "invalid";
+  if (!p.tail) return p.shape->built.name;
+  snprintf(g_plan_name, sizeof g_plan_name, "%s+%s", p.shape->built.name, p.tail->built.name);
+  return g_plan_name;
+}
+
+}  // namespace
+}  // namespace gemm
+
+extern "C" {
+
+int gemm_i8_ex(const char* config, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda,
+               const float* SA, const void* B, int64_t ldb, const float* SB, void* C, int64_t ldc,
+               int c_type, void* stream) {
+  return gemm::dense_product(config, GEMM_TYPE_I8, false, M, N, K, A, lda, SA, B, ldb, SB,
+                             GEMM_ACT_NONE, C, ldc, c_type, nullptr, 0, stream);
+}
+
+int gemm_i8(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const float* SA,
+            const void* B, int64_t ldb, const float* SB, void* C, int64_t ldc, int c_type,
+            void* stream) {
+  return gemm_i8_ex(nullptr, M, N, K, A, lda, SA, B, ldb, SB, C, ldc, c_type, stream);
+}
+
+int gemm_i8_gated_ex(const char* config, int64_t M, int64_t F, int64_t K, const void* A,
+                     int64_t lda, const float* SA, const void* W, int64_t ldw, const float* SW,
+                     int act, void* H, int64_t ldh, int h_type, void* stream) {
+  return gemm::dense_product(config, GEMM_TYPE_I8, true, M, F, K, A, lda, SA, W, ldw, SW, act, H,
+                             ldh, h_type, nullptr, 0, stream);
+}
+
+int gemm_i8_gated(int64_t M, int64_t F, int64_t K, const void* A, int64_t lda, const float* SA,
+                  const void* W, int64_t ldw, const float* SW, int act, void* H, int64_t ldh,
+                  int h_type, void* stream) {
+  return gemm_i8_gated_ex(nullptr, M, F, K, A, lda, SA, W, ldw, SW, act, H, ldh, h_type, stream);
+}
+
+int gemm_gated_ex(const char* config, int type, int64_t M, int64_t F, int64_t K, const void* X,
+                  int64_t ldx, const void* W, int64_t ldw, int act, void* H, int64_t ldh, void* GU,
+                  int64_t ldgu, void* stream) {
+  if (type == GEMM_TYPE_I8) return GEMM_ERR_INVALID_ARG;
+  return gemm::dense_product(config, type, true, M, F, K, X, ldx, nullptr, W, ldw, nullptr, act, H,
+                             ldh, type, GU, ldgu, stream);
+}
+
+int gemm_gated(int type, int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,
+               const void* W, int64_t ldw, int act, void* H, int64_t ldh, void* GU, int64_t ldgu,
+               void* stream) {
+  return gemm_gated_ex(nullptr, type, M, F, K, X, ldx, W, ldw, act, H, ldh, GU, ldgu, stream);
+}
+
+const char* gemm_i8_config_name(int64_t M, int64_t N, int64_t K) {
+  return gemm::plan_name(GEMM_TYPE_I8, false, M, N, K);
+}
+
+const char* gemm_gated_config_name(int type, int64_t M, int64_t F, int64_t K) {
+  return gemm::plan_name(type, true, M, F, K);
+}
+
+int gemm_i8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_type, void* Q,
+                     int64_t ldq, float* S, void* stream) {
+  if (M < 0 || K < 0 || !gemm::is_float_type(x_type)) return GEMM_ERR_INVALID_ARG;
+  // (a workgroup of 256 a row: a grid holds fewer than 2^32 threads)
+  if (K >= gemm::k2G || M >= 2 * gemm::k2G / 256 || ldx >= (int64_t(1) << 40) ||
+      ldq >= (int64_t(1) << 40))
+    return GEMM_ERR_UNSUPPORTED;
+  if (ldx < K || ldq < K) return GEMM_ERR_INVALID_ARG;
+  if (M > 0 && (!S || (K > 0 && (!X || !Q)))) return GEMM_ERR_INVALID_ARG;
+  if (gemm::misaligned(X, x_type == GEMM_TYPE_F32 ? 4 : 2) || gemm::misaligned(Q, 16) ||
+      gemm::misaligned(S, 4) || (ldq & 15) != 0)
+    return GEMM_ERR_MISALIGNED;
+  if (M == 0) return GEMM_OK;
+  const gemm::Int8QuantArgs a{X, (uint8_t*)Q, S, M, K, ldx, ldq};
+  const hipError_t e = gemm::launch_quantize_int8(a, gemm::store_of(x_type), (hipStream_t)stream);
+  return e == hipSuccess ? GEMM_OK : gemm::hip_fail(e);
+}
+
+}  // extern "C"

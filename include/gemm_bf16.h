@@ -288,6 +288,7 @@ int gemm_bf16_ex_noalloc(const char* config,
 #define GEMM_TYPE_F16 1
 #define GEMM_TYPE_F32 2
 #define GEMM_TYPE_E4M3 3
+#define GEMM_TYPE_I8 4
 
 /* The product; c_type is GEMM_TYPE_BF16, _F16 or _F32.  Returns a status. */
 int gemm_fp8(int64_t M, int64_t N, int64_t K,
@@ -425,6 +426,91 @@ const char* gemm_moe_config_name(int type, int64_t R, int64_t N, int64_t K, int6
 int gemm_moe_combine(int64_t T, int64_t k, int64_t N, int64_t R, const void* Y, int64_t ldy,
                      int y_type, const int32_t* pos, const float* weights, void* out,
                      int64_t ldo, int out_type, void* stream);
+
+/* ------------------------------------------------------- 8-bit integers
+ * Products over signed 8-bit integers with one fp32 scale for each row of A
+ * (token) and each row of B (channel):
+ *
+ *   C[m,n] = (fp32(sum_k A[m,k] * B[n,k]) * SA[m]) * SB[n]
+ *
+ * The sum is a 32-bit integer, exact (K at most 131071: GEMM_ERR_UNSUPPORTED
+ * past it); its conversion to fp32 and the two products are rounded to nearest,
+ * C once more to its type.  A(m,k) = A[m*lda + k], B(n,k) = B[n*ldb + k], SA (M)
+ * and SB (N) contiguous; A and B 16-byte aligned with lda and ldb multiples of
+ * 16, C 16-byte aligned with ldc a multiple of 8, scales 4-byte aligned.  Any
+ * M, N, K >= 0; K == 0 sets C to zeros (times the scales).  Elements past K in
+ * a row are not used whatever they hold.  Scales may be any fp32 value.  Limits
+ * of rows and grids, streams and errors as for gemm_fp8; no workspace. */
+int gemm_i8(int64_t M, int64_t N, int64_t K,
+            const void* A, int64_t lda, const float* SA,
+            const void* B, int64_t ldb, const float* SB,
+            void* C, int64_t ldc, int c_type, void* stream);
+
+/* As gemm_i8 with the kernel shape named (one that gemm_fp8_config_at
+ * enumerates; NULL or "" = automatic). */
+int gemm_i8_ex(const char* config, int64_t M, int64_t N, int64_t K,
+               const void* A, int64_t lda, const float* SA,
+               const void* B, int64_t ldb, const float* SB,
+               void* C, int64_t ldc, int c_type, void* stream);
+
+/* Name of the kernel shape gemm_i8 chooses (see gemm_fp8_config_name). */
+const char* gemm_i8_config_name(int64_t M, int64_t N, int64_t K);
+
+/* Quantise X (M rows of K, x_type BF16, F16 or F32; any row stride, aligned to
+ * its type) to 8-bit integers Q (M x K, 16-byte aligned, ldq a multiple of 16;
+ * a row's bytes past K are left as they were) and a scale for each row, S (M):
+ *   amax = max(largest |x| of the row, 2^-100), S = amax / 127,
+ *   Q = x * (127 / amax) rounded to nearest even (all in fp32).
+ * A row that holds a NaN gets a NaN scale (its codes are unspecified), one that
+ * holds an infinity an infinite scale, codes of +-127 for its infinities and 0
+ * for the rest.  The same call serves activations (a scale for each token) and
+ * weights (one for each channel).  M is below 2^24, K below 2^31. */
+int gemm_i8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_type,
+                     void* Q, int64_t ldq, float* S, void* stream);
+
+/* ------------------------------------------------------- gated products
+ * The first half of a gated feed-forward layer in one launch: both
+ * projections, the activation and the product,
+ *
+ *   G = X W_g^T, U = X W_u^T, H = act(G) * U       (M x F each)
+ *
+ * with W's 2 F rows W_g's F, then W_u's F, as gemm_fp8_quantize's and the
+ * experts' halves lie.  GEMM_ACT_SWIGLU: act(g) = g / (1 + exp(-g));
+ * GEMM_ACT_GEGLU: gelu in its tanh form, g (1 + tanh(sqrt(2 / pi) (g +
+ * 0.044715 g^3))) / 2.  G and U are fp32 sums, H is rounded once from them (a
+ * 16-bit H of |act(g)| below 2^-119 may be zero).  g of -infinity gives NaN, as
+ * the formula does. */
+#define GEMM_ACT_GEGLU 2 /* of the gated products only */
+
+/* type GEMM_TYPE_BF16 or _F16, of X (M x K), W (2 F x K) and H (M x F).  GU:
+ * NULL, or where G and U go as well, rounded to `type`, for the backward pass:
+ * G(m,f) = GU[m*ldgu + f], U(m,f) = GU[m*ldgu + Fp + f] with Fp = F rounded up
+ * to a multiple of 8, ldgu >= 2 Fp (what lies between F and Fp is left as it
+ * was).  All 16-byte aligned, strides multiples of 8.  No workspace. */
+int gemm_gated(int type, int64_t M, int64_t F, int64_t K,
+               const void* X, int64_t ldx, const void* W, int64_t ldw, int act,
+               void* H, int64_t ldh, void* GU, int64_t ldgu, void* stream);
+
+/* The same over 8-bit integers, scaled as gemm_i8 (SW: 2 F); h_type BF16, F16
+ * or F32. */
+int gemm_i8_gated(int64_t M, int64_t F, int64_t K,
+                  const void* A, int64_t lda, const float* SA,
+                  const void* W, int64_t ldw, const float* SW, int act,
+                  void* H, int64_t ldh, int h_type, void* stream);
+
+/* With the kernel shape named (of those that gemm_fp8_config_at enumerates, all
+ * but b32x32k4, which does not hold whole pairs of columns). */
+int gemm_gated_ex(const char* config, int type, int64_t M, int64_t F, int64_t K,
+                  const void* X, int64_t ldx, const void* W, int64_t ldw, int act,
+                  void* H, int64_t ldh, void* GU, int64_t ldgu, void* stream);
+int gemm_i8_gated_ex(const char* config, int64_t M, int64_t F, int64_t K,
+                     const void* A, int64_t lda, const float* SA,
+                     const void* W, int64_t ldw, const float* SW, int act,
+                     void* H, int64_t ldh, int h_type, void* stream);
+
+/* Name of the kernel shape the gated product of a type (GEMM_TYPE_I8, _BF16 or
+ * _F16) chooses. */
+const char* gemm_gated_config_name(int type, int64_t M, int64_t F, int64_t K);
 
 /* Human-readable text for a status code.  Static storage; never NULL. */
 const char* gemm_bf16_status_string(int status);
