@@ -93,6 +93,10 @@ _i8_args = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _p, _i64, _c_int, _p]
 _i8_gated_args = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _c_int, _p, _i64, _c_int, _p]
 _gated_args = [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _c_int, _p, _i64, _p, _i64, _p]
 for _name, _args in {
+    "gemm_backward": [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64,
+                      _c_int, _p, ctypes.c_size_t, _p],
+    "gemm_gated_backward": [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _c_int, _p,
+                            _i64, _p, _i64, _p, _i64, _c_int, _p, ctypes.c_size_t, _p],
     "gemm_i8": _i8_args,
     "gemm_i8_ex": [ctypes.c_char_p, *_i8_args],
     "gemm_i8_quantize": [_i64, _i64, _p, _i64, _c_int, _p, _i64, _p, _p],
@@ -116,6 +120,12 @@ _lib.gemm_fp8_config_name.restype = ctypes.c_char_p
 _lib.gemm_fp8_config_name.argtypes = [_i64, _i64, _i64, _c_int]
 _lib.gemm_moe_config_name.restype = ctypes.c_char_p
 _lib.gemm_moe_config_name.argtypes = [_c_int, _i64, _i64, _i64, _i64, _c_int]
+for _name in ("gemm_backward_work_size", "gemm_gated_backward_work_size"):
+    getattr(_lib, _name).restype = ctypes.c_size_t
+    getattr(_lib, _name).argtypes = [_i64, _i64, _i64]
+for _name in ("gemm_backward_config_name", "gemm_gated_backward_config_name"):
+    getattr(_lib, _name).restype = ctypes.c_char_p
+    getattr(_lib, _name).argtypes = [_i64, _i64, _i64, _c_int]
 _lib.gemm_i8_config_name.restype = ctypes.c_char_p
 _lib.gemm_i8_config_name.argtypes = [_i64, _i64, _i64]
 _lib.gemm_gated_config_name.restype = ctypes.c_char_p
@@ -446,6 +456,48 @@ def gemm_gated_ex(config, type, M, F, K, X, ldx, W, ldw, act, H, ldh, GU=None, l
     cfg = None if config is None else config.encode()
     _check(_lib.gemm_gated_ex(cfg, type, M, F, K, _ptr(X), ldx, _ptr(W), ldw, act, _ptr(H), ldh,
                               _ptr(GU), ldgu, _stream(stream)))
+
+
+def gemm_backward(type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, db_type, work=None,
+                  work_bytes=0, stream=None) -> None:
+    """Gradients of C = A . B^T: dA = dC . B and dB = dC^T . A."""
+    _check(_lib.gemm_backward(type, M, N, K, _ptr(dC), lddc, _ptr(A), lda, _ptr(B), ldb, _ptr(dA),
+                              ldda, _ptr(dB), lddb, db_type, _ptr(work), work_bytes,
+                              _stream(stream)))
+
+
+def gemm_gated_backward(type, M, F, K, dH, lddh, X, ldx, W, ldw, act, GU, ldgu, dX, lddx, dW, lddw,
+                        dw_type, work=None, work_bytes=0, stream=None) -> None:
+    """Gradients of gemm_gated's X and W from H's and the GU that it kept."""
+    _check(_lib.gemm_gated_backward(type, M, F, K, _ptr(dH), lddh, _ptr(X), ldx, _ptr(W), ldw, act,
+                                    _ptr(GU), ldgu, _ptr(dX), lddx, _ptr(dW), lddw, dw_type,
+                                    _ptr(work), work_bytes, _stream(stream)))
+
+
+def backward_work_size(M, N, K) -> int:
+    """Bytes of workspace gemm_backward needs."""
+    return int(_lib.gemm_backward_work_size(M, N, K))
+
+
+def gated_backward_work_size(M, F, K) -> int:
+    """Bytes of workspace gemm_gated_backward needs."""
+    return int(_lib.gemm_gated_backward_work_size(M, F, K))
+
+
+def backward_config_name(M, N, K, of_b=False) -> str:
+    """The tile and split of dA's product, or of dB's."""
+    return _lib.gemm_backward_config_name(M, N, K, 1 if of_b else 0).decode()
+
+
+def gated_backward_config_name(M, F, K, of_w=False) -> str:
+    """The tile and split of dX's product, or of dW's."""
+    return _lib.gemm_gated_backward_config_name(M, F, K, 1 if of_w else 0).decode()
+
+
+gemm_backward_config_name = backward_config_name
+gemm_gated_backward_config_name = gated_backward_config_name
+gemm_backward_work_size = backward_work_size
+gemm_gated_backward_work_size = gated_backward_work_size
 
 
 def i8_config_name(M, N, K) -> str:
@@ -815,3 +867,88 @@ def gated_matmul(x, W, act="swiglu", out=None, save=False, config=None):
     if not save:
         return out
     return out, gu.as_strided((M, 2, F), (ldgu, ldgu // 2, 1))
+
+
+def _work(nbytes, device):
+    """Workspace of one call, from torch's allocator: freed to the stream it
+    was used on, and with a graph's memory while one is captured."""
+    return torch.empty(nbytes, device=device, dtype=torch.uint8) if nbytes else None
+
+
+def _grad(out, shape, dtype, device, name):
+    """An output of a backward call: given (checked), None (new), or False
+    (not wanted: None)."""
+    if out is False:
+        return None
+    if out is None:
+        return _out(None, shape, dtype, device)
+    _need(out, name, device, None, shape)
+    return out
+
+
+def _weight_dtype(dw, dw_dtype, dtype):
+    t = dw_dtype or (dtype if dw is None or dw is False else dw.dtype)
+    if t not in (dtype, torch.float32):
+        raise TypeError(f"a weight's gradient is {dtype} or torch.float32")
+    if isinstance(dw, torch.Tensor) and dw.dtype != t:
+        raise TypeError(f"the weight's gradient must be {t}")
+    return t
+
+
+def matmul_backward(dC, A, B, dA=None, dB=None, db_dtype=None):
+    """Gradients of matmul's C = A . B^T from dC (M x N): (dA, dB) with dA = dC .
+    B (M x K) and dB = dC^T . A (N x K).  dC, A and B are all bfloat16 or all
+    float16.  dA, dB: tensors to write, None for new ones, False where a
+    gradient is not wanted (None is returned).  db_dtype: A's type (default) or
+    float32."""
+    _need(dC, "dC")
+    dev, dtype = dC.device, dC.dtype
+    code = _type(dtype, "dC", (GEMM_TYPE_BF16, GEMM_TYPE_F16))
+    if dC.dim() != 2 or A.dim() != 2 or B.dim() != 2 or A.shape[1] != B.shape[1]:
+        raise ValueError("need dC (M x N), A (M x K) and B (N x K)")
+    (M, K), N = A.shape, B.shape[0]
+    _need(dC, "dC", dev, dtype, (M, N))
+    _need(A, "A", dev, dtype)
+    _need(B, "B", dev, dtype)
+    db_dtype = _weight_dtype(dB, db_dtype, dtype)
+    dA = _grad(dA, (M, K), dtype, dev, "dA")
+    if dA is not None and dA.dtype != dtype:
+        raise TypeError(f"dA must be {dtype}")
+    dB = _grad(dB, (N, K), db_dtype, dev, "dB")
+    nbytes = _lib.gemm_backward_work_size(M, N, K)
+    work = _work(nbytes, dev)
+    _call(_lib.gemm_backward, dev, code, M, N, K, dC.data_ptr(), _ld(dC, 8), A.data_ptr(),
+          _ld(A, 8), B.data_ptr(), _ld(B, 8), _ptr(dA), 0 if dA is None else _ld(dA, 8), _ptr(dB),
+          0 if dB is None else _ld(dB, 8), _TYPES[db_dtype], _ptr(work), nbytes)
+    return dA, dB
+
+
+def gated_matmul_backward(dh, x, W, gu, act="swiglu", dx=None, dw=None, dw_dtype=None):
+    """Gradients of gated_matmul's x and W from dh (M x F) and the gu that it
+    returned with save=True: (dx, dW).  act as in the forward call; dx, dw and
+    dw_dtype as matmul_backward's dA, dB and db_dtype."""
+    _need(x, "x")
+    dev, dtype = x.device, x.dtype
+    code = _type(dtype, "x", (GEMM_TYPE_BF16, GEMM_TYPE_F16))
+    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1] or W.shape[0] % 2:
+        raise ValueError("need x (M x K) and W (2F x K)")
+    (M, K), F = x.shape, W.shape[0] // 2
+    _need(W, "W", dev, dtype)
+    _need(dh, "dh", dev, dtype, (M, F))
+    _need(gu, "gu", dev, dtype, (M, 2, F))
+    Fp = -(-F // 8) * 8
+    if M > 0 and F > 0 and gu.stride(1) != Fp:
+        raise ValueError("gu must be as gated_matmul returned it")
+    dw_dtype = _weight_dtype(dw, dw_dtype, dtype)
+    dx = _grad(dx, (M, K), dtype, dev, "dx")
+    if dx is not None and dx.dtype != dtype:
+        raise TypeError(f"dx must be {dtype}")
+    dw = _grad(dw, (2 * F, K), dw_dtype, dev, "dw")
+    nbytes = _lib.gemm_gated_backward_work_size(M, F, K)
+    work = _work(nbytes, dev)
+    _call(_lib.gemm_gated_backward, dev, code, M, F, K, dh.data_ptr(), _ld(dh, 8), x.data_ptr(),
+          _ld(x, 8), W.data_ptr(), _ld(W, 8), _act(act), gu.data_ptr(),
+          gu.stride(0) if M > 1 and F > 0 else max(16, 2 * Fp), _ptr(dx),
+          0 if dx is None else _ld(dx, 8), _ptr(dw), 0 if dw is None else _ld(dw, 8),
+          _TYPES[dw_dtype], _ptr(work), nbytes)
+    return dx, dw

@@ -8,6 +8,8 @@
 //   integer   C[m,n] = SA[m] SB[n] sum_k A[m,k] B[n,k] over 8-bit integers
 //   gated     H[m,f] = act(G[m,f]) U[m,f] with [G | U] a product over bf16,
 //             fp16 or 8-bit integers, B's rows f for G and F + f for U
+//   gradients C = A . B with B's rows along K, and C = A^T . B with the rows of
+//             both along K, over bf16 and fp16: those of a product's operands
 //
 // Two kernels.  block_tile_kernel stages BM x BN tiles through LDS for many
 // rows; block_row_kernel streams B straight into registers for few rows.
@@ -45,6 +47,10 @@ enum : int { kOpE4m3 = 0, kOpBf16 = 1, kOpF16 = 2, kOpI8 = 3 };
 // What becomes of the sums: C, or (kGated) act(g) * u of paired columns.
 enum : int { kPlain = 0, kGated = 1 };
 
+// How the operands lie: rows of K elements (kNT); B's rows along K (kNN: B(k,n)
+// = B[k*ldb + n]); those of both (kTN: A(k,m) = A[k*lda + m] too).
+enum : int { kNT = 0, kNN = 1, kTN = 2 };
+
 struct BlockArgs {
   const uint8_t* A;
   const uint8_t* B;
@@ -75,6 +81,18 @@ struct BlockArgs {
   int64_t ldgu;       // elements from row to row of GU
   int64_t up_gu;      // elements from g to u in a row of GU
   int32_t geglu;      // act: 1: gelu (tanh form), 0: silu
+  // kNN and kTN: K in k_steps / seg_steps parts of equal length (kbytes counts
+  // one part's), of which the next starts seg_a and seg_b bytes further on;
+  int32_t seg_steps;
+  int64_t seg_a, seg_b;
+  // rows of C in two halves of M rows (or one: half_tiles = row_tiles), the
+  // second from half_a bytes on in A and from row M on in C;
+  int32_t half_tiles;
+  int64_t half_a;
+  // and the K-steps split over workgroups, whose sums go to parts of C that
+  // lie part_stride elements apart
+  int32_t splits, split_steps;
+  int64_t part_stride;
 };
 
 // ------------------------------------------------------------- row tiles
@@ -451,8 +469,19 @@ __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
 // wave holds g and u of one element of H in the same lane and register and
 // the activation costs no exchange.  NT: B's loads non-temporal, for one row
 // of tiles, where no other workgroup reads the same B.
+//
+// LAYOUT kNN, kTN: an operand whose rows lie along K is staged in pieces of 64
+// (K) x 64, each 64 LDS rows of 128 bytes as the other form's, so that a load
+// of 512 threads still fills the same rows or columns of the tile.  Fragments
+// are transposed on their way out of LDS: ds_read_b64_tr_b16 takes 4 (K) x 16
+// per 16 lanes and gives each lane its column's four values, so four reads
+// make the two chunks of a fragment, in the same K order as the other form's.
+// The 32-byte column group that a row holds in place u is u ^ (k / 2 % 2 + 2
+// (k / 8 % 2)): the eight rows that half a wave reads then lie in eight
+// different 32-byte groups of the 64 banks.  Rows past K are out of the
+// range of a step's buffer resource and read as zeros.
 template <int BM, int BN, int WM, int WN, int WK, int S, int OP, int OUT, int MODE = kPlain,
-          bool NT = false>
+          bool NT = false, int LAYOUT = kNT>
 __global__ __attribute__((amdgpu_flat_work_group_size(WM * WN * WK * 64, WM * WN * WK * 64),
                           amdgpu_waves_per_eu(2))) void
 block_tile_kernel(BlockArgs a) {
@@ -490,16 +519,31 @@ block_tile_kernel(BlockArgs a) {
   const int wm = wave / WN, wn = wave % WN;
 
   // ---- which tile --------------------------------------------------------
+  constexpr bool kGrad = LAYOUT != kNT, kTransA = LAYOUT == kTN, kTransB = kGrad;
+  static_assert(!kGrad || (WK == 1 && OP != kOpE4m3 && OP != kOpI8 && MODE == kPlain && !NT),
+                "gradients are of 16-bit types");
+  static_assert(!kGrad || (Cfg::kWaveM % 64 == 0 && Cfg::kWaveN % 64 == 0 && 64 % RPI == 0),
+                "whole pieces of 64 columns");
   const int row_tiles = a.offsets ? count_row_tiles(a, BM, lane) : a.row_tiles;
   const int units = row_tiles * a.tiles_n;
-  if ((int)blockIdx.x >= units) return;  // the grid is an upper bound
-  const int logical = xcd_remap(blockIdx.x, units);
+  if (!kGrad && (int)blockIdx.x >= units) return;  // the grid is an upper bound
+  int logical = xcd_remap(blockIdx.x, kGrad ? units * a.splits : units);
+  int split = 0;
+  if constexpr (kGrad) {
+    split = logical / units;
+    logical -= split * units;
+  }
   const int span = a.group_m * a.tiles_n;
   const int gid = logical / span;
   const int first = gid * a.group_m;
   const int gsz = min(row_tiles - first, a.group_m);
   const int in = logical - gid * span;
-  const int rt = first + in % gsz;
+  int rt = first + in % gsz;
+  int half = 0;
+  if constexpr (kGrad) {
+    half = rt / a.half_tiles;
+    rt -= half * a.half_tiles;
+  }
   constexpr bool kPairs = MODE == kGated;
   constexpr int kCols = kPairs ? BN / 2 : BN;  // columns of C
   static_assert(!kPairs || (RPI % 32 == 0 && FN % 2 == 0), "16 and 16 rows of B in turn");
@@ -516,6 +560,8 @@ block_tile_kernel(BlockArgs a) {
 
   // ---- loads -------------------------------------------------------------
   const bool gather = a.rows != nullptr;
+  const uint8_t* const grad_a = a.A + half * a.half_a + (kTransA ? (int64_t)m0 * 2 : 0);
+  const uint8_t* const grad_b = a.B + (int64_t)n0 * 2;
   const u32x4 rsrc_a = gather ? make_rsrc(a.A, (uint32_t)((int64_t)a.a_rows * a.lda))
                               : make_rsrc(a.A + (int64_t)m0 * a.lda, (uint32_t)(rows_a * a.lda));
   // (gated: a wave loads 8 rows at a time, all of the gate or all of the up
@@ -529,7 +575,12 @@ block_tile_kernel(BlockArgs a) {
 #pragma unroll
   for (int i = 0; i < L; ++i) {
     const int row = (i < LA ? i : i - LA) * RPI + r0;
-    if (i < LA) {
+    if (i < LA ? kTransA : kTransB) {
+      // K row `row % 64` of a piece of 64 columns
+      const int col = row / 64 * 64 + ((tid & 7) ^ (((r0 >> 1) & 1) << 1 | ((r0 >> 3) & 1) << 2)) * 8;
+      const int ld = (int)(i < LA ? a.lda : a.ldb);
+      voff[i] = col < (i < LA ? rows_a : rows_b) ? (uint32_t)(row % 64 * ld + col * 2) : kOOB;
+    } else if (i < LA) {
       const int src = row < rows_a ? (gather ? source_row(a, m0 + row) : row) : -1;
       voff[i] = src >= 0 ? (uint32_t)(src * (int)a.lda + chunk * 16) : kOOB;
     } else {
@@ -559,11 +610,15 @@ block_tile_kernel(BlockArgs a) {
            0u);
     }
   }
-  const bool past_k = (a.k_steps - 1) * kStepBytes + chunk * 16 >= a.kbytes;  // in the last step
+  const int last_step = (kGrad ? a.seg_steps : a.k_steps) - 1;  // (of a part of K)
+  const bool past_k = last_step * kStepBytes + chunk * 16 >= a.kbytes;  // in the last step
+  const int k_begin = kGrad ? split * a.split_steps : 0;
+  const int k_here = kGrad ? min(a.k_steps - k_begin, a.split_steps) : a.k_steps;
   // This group's X-th step of K: X * WK + kg, from the tile's starting point
   // on (k_steps or more: past the last one).
   const int rot = a.k_steps > 0 ? __builtin_amdgcn_readfirstlane(tn * a.k_rot % a.k_steps) : 0;
   auto step_of = [&](int X) __attribute__((always_inline)) {
+    if constexpr (kGrad) return X < k_here ? k_begin + X : a.k_steps;
     const int k = X * WK + kg;
     const int r = k + rot >= a.k_steps ? k + rot - a.k_steps : k + rot;
     return k < a.k_steps ? r : k;
@@ -574,6 +629,21 @@ block_tile_kernel(BlockArgs a) {
                          (((i < LA ? i : i - LA) * T + wave * 64) * 16);
     // past K, and in the steps past the last one, a load reads zeros: no
     // branch splits the loop body
+    if constexpr (kGrad) {
+      const bool second = k >= a.seg_steps;  // (two parts at most)
+      const int kk = second ? k - a.seg_steps : k;
+      if (i < LA ? kTransA : kTransB) {
+        const int64_t ld = i < LA ? a.lda : a.ldb;
+        const int left = k < a.k_steps ? min(64, (a.kbytes >> 1) - kk * 64) : 0;
+        const uint8_t* base = (i < LA ? grad_a : grad_b) + (int64_t)(kk * 64) * ld +
+                              (second ? (i < LA ? a.seg_a : a.seg_b) : 0);
+        dma16(make_rsrc(base, (uint32_t)(left * (int)ld)), dst, voff[i], 0u);
+      } else {
+        const uint32_t v = k >= a.k_steps || (past_k && kk == last_step) ? kOOB : voff[i];
+        dma16(rsrc_a, dst, v, (uint32_t)(kk * kStepBytes) + (second ? (uint32_t)a.seg_a : 0u));
+      }
+      return;
+    }
     const uint32_t v = k >= a.k_steps - (past_k ? 1 : 0) ? kOOB : voff[i];
     if (NT && i >= LA)
       dma16<true>(rsrc_b, dst, v, (uint32_t)(k * kStepBytes));
@@ -586,9 +656,16 @@ block_tile_kernel(BlockArgs a) {
       dma4(rs, (uint32_t)(uintptr_t)sa_s + (slot * SA + srow) * 4, voff_s, 0u);
     }
   };
+  // Whether step k holds bytes past K that its loads cannot leave out.
+  auto trims = [&](int k) __attribute__((always_inline)) {
+    if constexpr (kTransA) return false;
+    return (k == a.k_steps - 1 || (kGrad && k == last_step)) && (a.kbytes & 15) != 0;
+  };
   // Zero the bytes past K of the 16-byte chunk that straddles it, each
   // thread in the chunks it loaded (their loads have landed).
   auto trim_one = [&](int k, int slot, int i) __attribute__((always_inline)) {
+    if (i < LA ? kTransA : kTransB) return;  // (whole rows of zeros there)
+    if (kGrad && k >= a.seg_steps) k -= a.seg_steps;
     const int keep = a.kbytes - (k * kStepBytes + chunk * 16);
     if (keep > 0 && keep < 16) {
       lds_u32x4* p = (lds_u32x4*)(smem + slot * Cfg::kStageBytes + (i < LA ? 0 : Cfg::kABytes) +
@@ -625,13 +702,40 @@ block_tile_kernel(BlockArgs a) {
   const lds_u8* const pa = smem + wm * Cfg::kWaveM * kStepBytes;
   const lds_u8* const pb = smem + Cfg::kABytes + wn * Cfg::kWaveN * kStepBytes;
   using Frag = typename St::Frag;
+  // (rows along K: this lane's place in the first 4 x 16 of a piece, and the
+  // XOR of its column group)
+  const int at_k = ((lane >> 4) * 8 + (lrow >> 2)) * kStepBytes + (lrow & 3) * 8;
+  const int group_k = ((lrow >> 3) & 1) << 5 | ((lane >> 4) & 1) << 6;
+  auto read_cols = [&](const lds_u8* base, int f) __attribute__((always_inline)) {
+    typedef short i16x4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+    const lds_u8* p = base + f / 4 * (64 * kStepBytes) + at_k + (group_k ^ (f % 4 * 32));
+    Frag r;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const u32x2 x = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + h * 32 * kStepBytes)));
+      const u32x2 y = __builtin_bit_cast(
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + (h * 32 + 4) * kStepBytes)));
+      r.v[h] = (u32x4){x[0], x[1], y[0], y[1]};
+    }
+    return r;
+  };
   auto read_frag = [&](const lds_u8* base, int f) __attribute__((always_inline)) {
     const u32x4 lo = *(const lds_u32x4*)(base + f * 16 * kStepBytes + at);
     const u32x4 hi = *(const lds_u32x4*)(base + f * 16 * kStepBytes + (at ^ 64));
     return St::make(lo, hi);
   };
+  auto read_a = [&](const lds_u8* base, int f) __attribute__((always_inline)) {
+    if constexpr (kTransA) return read_cols(base, f);
+    else return read_frag(base, f);
+  };
+  auto read_b = [&](const lds_u8* base, int f) __attribute__((always_inline)) {
+    if constexpr (kTransB) return read_cols(base, f);
+    else return read_frag(base, f);
+  };
 
-  const int rounds = (a.k_steps + WK - 1) / WK;
+  const int rounds = kGrad ? k_here : (a.k_steps + WK - 1) / WK;
   // A wave whose rows all lie past the tile's last one (an expert's last
   // tile, C's last rows) only loads: the other waves of its SIMD then have
   // the matrix core to themselves.
@@ -688,7 +792,7 @@ block_tile_kernel(BlockArgs a) {
     };
     // wait for the oldest part in flight, and the barrier
     auto publish = [&](int k, int slot, bool two) __attribute__((always_inline)) {
-      if (k == a.k_steps - 1 && (a.kbytes & 15) != 0) {
+      if (trims(k)) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
         for (int l = 0; l < L; ++l)
@@ -722,13 +826,13 @@ block_tile_kernel(BlockArgs a) {
     };
     auto read_row = [&](int slot, int sslot, auto ic) __attribute__((always_inline)) {
       constexpr int i = decltype(ic)::value;
-      fa[buf_of(i)] = read_frag(pa + slot * Cfg::kStageBytes, i);
+      fa[buf_of(i)] = read_a(pa + slot * Cfg::kStageBytes, i);
       if constexpr (kScaled) sc[i % 4] = sa_s[sslot * SA + wm * Cfg::kWaveM + i * 16 + lrow] * sb;
     };
     scale_b(step_of(0));
     read_row(0, 0, Zero{});
 #pragma unroll
-    for (int j = 0; j < FN; ++j) fb[j] = read_frag(pb, j);
+    for (int j = 0; j < FN; ++j) fb[j] = read_b(pb, j);
     read_row(0, 0, std::integral_constant<int, 1>{});
     int ss = 0;  // X % 3: the slot of step X's row scales, read to the step's end
     for (int X = idle ? rounds : 0; X < rounds; ++X) {
@@ -768,7 +872,7 @@ block_tile_kernel(BlockArgs a) {
         if constexpr (q >= Q0) {
           // the next step's first rows and B fragments
           if constexpr (q == Q0) read_row(next, ss1, Zero{});
-          if constexpr ((q - Q0) % 2 == 1) fb[j] = read_frag(pb + next * Cfg::kStageBytes, j);
+          if constexpr ((q - Q0) % 2 == 1) fb[j] = read_b(pb + next * Cfg::kStageBytes, j);
           if constexpr (q == NQ - 1) read_row(next, ss1, std::integral_constant<int, 1>{});
         }
         if constexpr (kScaled) {
@@ -799,7 +903,7 @@ block_tile_kernel(BlockArgs a) {
     int at_slot = 0, to_slot = S - 1;  // ring slots of steps X and X + S - 1
     for (int X = 0; X < rounds; ++X) {
       const int k = step_of(X), k_ahead = step_of(X + S - 1);
-      if (k == a.k_steps - 1 && (a.kbytes & 15) != 0) {
+      if (trims(k)) {
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
 #pragma unroll
         for (int i = 0; i < L; ++i) trim_one(k, at_slot, i);
@@ -816,8 +920,8 @@ block_tile_kernel(BlockArgs a) {
       const uint32_t slot = at_slot * Cfg::kStageBytes;
       Frag fb[FN], fa[2];
 #pragma unroll
-      for (int j = 0; j < FN; ++j) fb[j] = read_frag(pb + slot, j);
-      fa[0] = read_frag(pa + slot, 0);
+      for (int j = 0; j < FN; ++j) fb[j] = read_b(pb + slot, j);
+      fa[0] = read_a(pa + slot, 0);
       float sb = 0.0f;
       if constexpr (kScaled)
         sb = k < a.k_steps ? sb_s[(wn * Cfg::kWaveN / kScaleBlock) * kMaxKSteps + k] : 0.0f;
@@ -828,7 +932,7 @@ block_tile_kernel(BlockArgs a) {
         if (i < FM) {
           if constexpr (kScaled)
             sc[i & 1] = sa_s[at_slot * SA + wm * Cfg::kWaveM + i * 16 + lrow] * sb;
-          if (i + 1 < FM) fa[(i + 1) & 1] = read_frag(pa + slot, i + 1);
+          if (i + 1 < FM) fa[(i + 1) & 1] = read_a(pa + slot, i + 1);
 #pragma unroll
           for (int j = 0; j < FN; ++j) {
             if constexpr (kScaled)
@@ -862,6 +966,9 @@ block_tile_kernel(BlockArgs a) {
 
   KernelArgs c{};
   c.C = a.C;
+  if constexpr (kGrad)
+    c.C = (uint8_t*)a.C + (half * (int64_t)a.M * a.ldc + split * a.part_stride) *
+                              (OUT == kStoreF32 ? 4 : 2);
   c.ldc = a.ldc;
   c.M = tile.end;
   c.N = a.N;

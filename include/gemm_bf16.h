@@ -512,6 +512,54 @@ int gemm_i8_gated_ex(const char* config, int64_t M, int64_t F, int64_t K,
  * _F16) chooses. */
 const char* gemm_gated_config_name(int type, int64_t M, int64_t F, int64_t K);
 
+/* ------------------------------------------------------------ gradients
+ * Of the dense product C = A B^T (gemm_bf16's and gemm_f16's), from the
+ * gradient of C:
+ *
+ *   dA (M x K) = dC (M x N) . B (N x K)      dB (N x K) = dC^T . A (M x K)
+ *
+ * type GEMM_TYPE_BF16 or _F16, of dC, A, B and dA; db_type that or F32 (for
+ * gradients that are summed over several calls).  fp32 sums in an order fixed
+ * by the sizes, rounded once.  dA or dB may be NULL (not computed; B, or A, is
+ * then not used either).  16-byte aligned, strides multiples of 8.  M == 0
+ * sets dB to zeros, N == 0 dA.  Outputs must not overlap anything.
+ *
+ * `work` is the caller's device memory, 16-byte aligned, of at least
+ * gemm_backward_work_size bytes (0: may be NULL), used by this call alone
+ * until it has run: calls that may overlap, and graphs whose replays may, need
+ * one each.  Too small: GEMM_ERR_SCRATCH.  Nothing is allocated, so the calls
+ * may be captured.  M and K are below 2^30, N below 2^29, 256 rows of an
+ * operand span less than 2^31 - 4096 bytes (GEMM_ERR_UNSUPPORTED). */
+int gemm_backward(int type, int64_t M, int64_t N, int64_t K,
+                  const void* dC, int64_t lddc, const void* A, int64_t lda,
+                  const void* B, int64_t ldb, void* dA, int64_t ldda,
+                  void* dB, int64_t lddb, int db_type,
+                  void* work, size_t work_bytes, void* stream);
+size_t gemm_backward_work_size(int64_t M, int64_t N, int64_t K);
+/* The tile and the ways K is split ("b256x256_k1") of dA's product, or with
+ * of_b != 0 of dB's.  Per-thread static storage. */
+const char* gemm_backward_config_name(int64_t M, int64_t N, int64_t K, int of_b);
+
+/* Of the gated product H = act(G) * U (gemm_gated), from the gradient of H and
+ * the GU that it kept:
+ *
+ *   dU = dH * act(G)                 dG = dH * U * act'(G)
+ *   dX (M x K) = dG W_g + dU W_u     dW (2 F x K) = [dG^T X; dU^T X]
+ *
+ * dG and dU are rounded to `type` before the two products, as G and U were
+ * when they were kept; sums are fp32, in an order fixed by the sizes.  dX or
+ * dW may be NULL.  Rows of dH are read up to F rounded up to a multiple of 8
+ * (within lddh).  The rest, and `work`, as for gemm_backward; F is below 2^29,
+ * and M * ceil(F / 8) below 2^32. */
+int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K,
+                        const void* dH, int64_t lddh, const void* X, int64_t ldx,
+                        const void* W, int64_t ldw, int act,
+                        const void* GU, int64_t ldgu, void* dX, int64_t lddx,
+                        void* dW, int64_t lddw, int dw_type,
+                        void* work, size_t work_bytes, void* stream);
+size_t gemm_gated_backward_work_size(int64_t M, int64_t F, int64_t K);
+const char* gemm_gated_backward_config_name(int64_t M, int64_t F, int64_t K, int of_w);
+
 /* Human-readable text for a status code.  Static storage; never NULL. */
 const char* gemm_bf16_status_string(int status);
 

@@ -1,0 +1,396 @@
+"""Gated products over bf16 and fp16 and the gradients of dense and gated
+products, on the GPU, against 64-bit forms: bit-exact where every sum is
+exact, else within bounds counted from the roundings."""
+import numpy as np
+import pytest
+
+import gated_ref as ref
+from block_ref import HALF_STEP, TINY, U, check_rounded, dtype, padded
+
+pytestmark = pytest.mark.gpu
+
+GATED = ["b256x256", "b256x128", "b128x128", "b128x128k2", "b64x128k2", "b64x64", "b64x64k2",
+         "b32x128", "b32x64k4", "r16x16"]
+
+
+def normal(rng, shape, t, sigma=1.0):
+    import torch
+
+    return torch.from_numpy(rng.normal(0, sigma, shape).astype(np.float32)).to(dtype(t))
+
+
+def ints(rng, shape, t, most=3):
+    import torch
+
+    return torch.from_numpy(rng.integers(-most, most + 1, shape).astype(np.float32)).to(dtype(t))
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def dev(t, extra=1):
+    """On the GPU, rows inside a wider buffer of NaN."""
+    return padded(t, 8, extra)
+
+
+def forward(x, w, act="swiglu", config=None, out=None, save=True):
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    r = g.gated_matmul(dev(x), dev(w, 2), act=act, config=config, out=out, save=save)
+    torch.cuda.synchronize()
+    return r
+
+
+def check_forward(h, gu, x, w, act, t):
+    """h within fp32's error and one rounding of the true one; g and u too."""
+    F = w.shape[0] // 2
+    GU, err = ref.product(f64(x), f64(w))
+    g, u = GU[:, :F], GU[:, F:]
+    bound = ref.gate_error(g, u, act, err[:, :F], err[:, F:])
+    check_rounded(f64(h), ref.gate(g, u, act), bound, t)
+    if gu is not None:
+        check_rounded(f64(gu[:, 0]), g, err[:, :F], t)
+        check_rounded(f64(gu[:, 1]), u, err[:, F:], t)
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+@pytest.mark.parametrize("config", GATED)
+def test_gated_every_shape(config, act, t):
+    """Ragged in M, F and K, padding full of NaN."""
+    rng = np.random.default_rng(3)
+    x, w = normal(rng, (300, 356), t), normal(rng, (2 * 197, 356), t, 356 ** -0.5)
+    h, gu = forward(x, w, act, config)
+    check_forward(h, gu, x, w, act, t)
+
+
+@pytest.mark.parametrize("K", [0, 1, 7, 8, 9, 63, 64, 65, 127, 129, 200])
+@pytest.mark.parametrize("config", GATED)
+def test_gated_every_end_of_k(config, K):
+    """Integers: g and u are exact."""
+    rng = np.random.default_rng(K)
+    x, w = ints(rng, (37, K), "bf16"), ints(rng, (2 * 35, K), "bf16", 2)
+    h, gu = forward(x, w, "swiglu", config)
+    GU = f64(x) @ f64(w).T
+    assert np.abs(GU).max(initial=0) < 2 ** 12
+    import torch
+
+    want = torch.from_numpy(GU).to(torch.bfloat16).double().numpy()
+    assert np.array_equal(np.concatenate([f64(gu[:, 0]), f64(gu[:, 1])], 1), want)
+    check_forward(h, None, x, w, "swiglu", "bf16")
+
+
+@pytest.mark.parametrize("M, F, K", [
+    (1, 1, 64), (1, 5000, 300), (2, 8, 8), (16, 130, 1024), (33, 1000, 640), (64, 512, 2048),
+    (129, 385, 1152), (300, 640, 512), (777, 5001, 200), (1100, 4609, 136), (0, 10, 64), (5, 0, 64)])
+def test_gated_automatic_shapes(M, F, K):
+    rng = np.random.default_rng(M * 7 + F)
+    x, w = normal(rng, (M, K), "f16"), normal(rng, (2 * F, K), "f16", K ** -0.5)
+    h, gu = forward(x, w, "geglu")
+    assert h.shape == (M, F) and gu.shape == (M, 2, F)
+    if M and F:
+        check_forward(h, gu, x, w, "geglu", "f16")
+        alone = forward(x, w, "geglu", save=False)
+        assert np.array_equal(f64(alone), f64(h))  # keeping g and u changes nothing
+
+
+def test_gated_large_and_special_values():
+    """Gates far out on both sides, past where the power overflows; infinities
+    and NaN reach their own elements only."""
+    import torch
+
+    gates = np.array([0, -0.0, 1e-3, -1e-3, 20, -20, 87, -87, 89, -89, 200, -200, 3e4, -3e4, 1e30, -1e30],
+                     np.float32)
+    n = len(gates)
+    x = torch.eye(n, dtype=torch.bfloat16)
+    w = torch.zeros(2 * n, n, dtype=torch.bfloat16)
+    w[:n] = torch.diag(torch.from_numpy(gates)).to(torch.bfloat16)
+    w[n:] = 1.5
+    for act in ("swiglu", "geglu"):
+        h, gu = forward(x, w, act)
+        g = f64(x) @ f64(w[:n]).T
+        check_rounded(f64(h), ref.gate(g, np.full_like(g, 1.5), act),
+                      ref.gate_error(g, np.full_like(g, 1.5), act) + 1.5 * TINY["bf16"], "bf16")
+    x[3, 3], x[5, 0] = float("inf"), float("nan")
+    w = torch.ones(2 * n, n, dtype=torch.bfloat16)
+    h, _ = forward(x, w)
+    h = f64(h)
+    assert (h[3] == np.inf).all() and np.isnan(h[5]).all()
+    assert np.isfinite(np.delete(h, [3, 5], 0)).all()
+    h, _ = forward(x, -w)
+    assert np.isnan(f64(h)[3]).all()  # -inf * 0, as g / (1 + exp(-g)) gives
+
+
+@pytest.mark.parametrize("config", GATED)
+def test_gated_outputs_outside_their_range_are_left_alone(config):
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = np.random.default_rng(3)
+    M, F, K = 70, 45, 100
+    x, w = normal(rng, (M, K), "f16"), normal(rng, (2 * F, K), "f16", 0.1)
+    H = torch.full((74, 64), 7.0, device="cuda", dtype=torch.float16)
+    GU = torch.full((74, 120), 7.0, device="cuda", dtype=torch.float16)
+    dx, dw = dev(x), dev(w)
+    g.gemm_gated_ex(config, g.GEMM_TYPE_F16, M, F, K, dx, dx.stride(0), dw, dw.stride(0),
+                    g.GEMM_ACT_SWIGLU, H[2:, 8:], 64, GU[1:, 8:], 120)
+    torch.cuda.synchronize()
+    gu = torch.stack([GU[1:71, 8:53], GU[1:71, 56:101]], 1)
+    check_forward(H[2:72, 8:53], gu, x, w, "swiglu", "f16")
+    H[2:72, 8:53] = 7
+    GU[1:71, 8:53] = 7
+    GU[1:71, 56:101] = 7
+    assert (H == 7).all() and (GU == 7).all()
+
+
+def test_rows_past_32_bits():
+    """An up projection that starts past 2^32 bytes into W, H past it as well."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    F, K, M = 300000, 8192, 3
+    w = torch.zeros(2 * F, K, device="cuda", dtype=torch.bfloat16)
+    at = [0, 1, 131071, 262144, F - 1]
+    rng = np.random.default_rng(1)
+    rows = normal(rng, (2 * len(at), K), "bf16", K ** -0.5).cuda()
+    w[at] = rows[:len(at)]
+    w[[F + i for i in at]] = rows[len(at):]
+    x = normal(rng, (M, K), "bf16").cuda()
+    h, gu = g.gated_matmul(x, w, save=True)
+    torch.cuda.synchronize()
+    check_forward(h[:, at].cpu(), gu[:, :, at].cpu(), x.cpu(), rows.cpu(), "swiglu", "bf16")
+    assert int((h != 0).sum()) <= M * len(at)
+    del w, h, gu
+
+
+# ------------------------------------------------------------------ gradients
+
+SIZES = [(1, 300, 70), (300, 200, 130), (3000, 136, 72), (72, 3000, 136), (4090, 130, 4100),
+         (130, 4090, 4100), (2100, 2056, 700)]
+
+
+def backward(dc, a, b, db_dtype=None):
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    r = g.matmul_backward(dev(dc), dev(a, 2), dev(b), db_dtype=db_dtype)
+    torch.cuda.synchronize()
+    return r
+
+
+@pytest.mark.parametrize("out", [None, "f32"])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("M, N, K", [
+    *SIZES, (1, 1, 1), (63, 64, 65), (257, 511, 129), (700, 1030, 520), (0, 5, 9), (5, 0, 9),
+    (5, 9, 0)])
+def test_product_gradients_are_exact_on_integers(M, N, K, t, out):
+    """Sums of integers below 2^24 are exact in any order; padding is NaN."""
+    import torch
+
+    rng = np.random.default_rng(M + N)
+    dc, a, b = (ints(rng, s, t) for s in ((M, N), (M, K), (N, K)))
+    da, db = backward(dc, a, b, None if out is None else torch.float32)
+    DC = f64(dc)
+    wa, wb = DC @ f64(b), DC.T @ f64(a)
+    assert da.shape == (M, K) and db.shape == (N, K) and da.dtype == dtype(t)
+    assert np.array_equal(f64(da), torch.from_numpy(wa).float().to(dtype(t)).double().numpy())
+    want = torch.from_numpy(wb).float().to(db.dtype).double().numpy()
+    assert np.array_equal(f64(db), want)
+
+
+def test_plans_that_the_gradients_run_as():
+    """Both tiles, split and not, of both products, are reached by the sizes of
+    these tests."""
+    import dense_gemm_bf16_amd as g
+
+    seen = set()
+    for M, N, K in SIZES:
+        for of_b in (False, True):
+            tile, splits = g.backward_config_name(M, N, K, of_b).split("_k")
+            seen.add((tile, int(splits) > 1, of_b))
+    assert {("b128x128", s, b) for s in (False, True) for b in (False, True)} <= seen, seen
+    assert ("b256x256", False, False) in seen and ("b256x256", False, True) in seen, seen
+
+
+@pytest.mark.parametrize("M, N, K", [(40, 5000, 100), (333, 777, 555), (1500, 100, 60), (2100, 2056, 700)])
+def test_product_gradients_on_normal_values(M, N, K):
+    import torch
+
+    rng = np.random.default_rng(N)
+    dc, a, b = (normal(rng, s, "bf16") for s in ((M, N), (M, K), (N, K)))
+    da, db = backward(dc, a, b, torch.float32)
+    want, err = ref.product(f64(dc), f64(b).T)
+    check_rounded(f64(da), want, err, "bf16")
+    want, err = ref.product(f64(dc).T, f64(a).T)
+    check_rounded(f64(db), want, err, "f32")
+
+
+def gated_backward(dh, x, w, gu, act, **kw):
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    r = g.gated_matmul_backward(dev(dh), dev(x), dev(w, 2), gu, act=act, **kw)
+    torch.cuda.synchronize()
+    return r
+
+
+def check_gated_backward(dx, dw, dh, x, w, gu, act, t, w_out):
+    """From the kept g and u: dg and du are off by fp32's error and a rounding
+    to the type, which reach dx and dw through the products."""
+    g, u = f64(gu[:, 0]), f64(gu[:, 1])
+    dg, du = ref.gate_gradients(f64(dh), g, u, act)
+    eg, eu = ref.gate_gradient_error(f64(dh), g, u, act)
+    d, e = np.concatenate([dg, du], 1), np.concatenate([eg, eu], 1)
+    e = e + HALF_STEP[t] * (np.abs(d) + e) + TINY[t]
+    W, X = f64(w), f64(x)
+    k = 2 * U * (d.shape[1] + 16)
+    check_rounded(f64(dx), d @ W, e @ np.abs(W) + k * ((np.abs(d) + e) @ np.abs(W)), t)
+    k = 2 * U * (d.shape[0] + 16)
+    check_rounded(f64(dw), d.T @ X, e.T @ np.abs(X) + k * ((np.abs(d) + e).T @ np.abs(X)), w_out)
+
+
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("M, F, K", [
+    (1, 1, 1), (1, 200, 64), (2, 7, 9), (65, 63, 64), (300, 197, 130), (257, 320, 72),
+    (3000, 70, 40), (64, 3000, 136), (2100, 1030, 264), (4090, 77, 4100),
+    (136, 2090, 4100)])
+def test_gated_gradients(M, F, K, t, act):
+    import torch
+
+    rng = np.random.default_rng(M + F)
+    x, w = normal(rng, (M, K), t), normal(rng, (2 * F, K), t, 2 * K ** -0.5)
+    dh = normal(rng, (M, F), t)
+    _, gu = forward(x, w, act)
+    f32 = (M + F) % 2 == 0
+    dx, dw = gated_backward(dh, x, w, gu, act, dw_dtype=torch.float32 if f32 else None)
+    check_gated_backward(dx, dw, dh, x, w, gu, act, t, "f32" if f32 else t)
+
+
+def test_gated_gradients_one_at_a_time_and_in_place_of_others():
+    """Either output alone, and given tensors whose surroundings stay."""
+    import torch
+
+    rng = np.random.default_rng(8)
+    M, F, K = 130, 77, 90
+    x, w, dh = normal(rng, (M, K), "bf16"), normal(rng, (2 * F, K), "bf16", 0.1), normal(rng, (M, F), "bf16")
+    _, gu = forward(x, w)
+    dx, dw = gated_backward(dh, x, w, gu, "swiglu")
+    only, none = gated_backward(dh, x, w, gu, "swiglu", dw=False)
+    assert none is None and torch.equal(only, dx)
+    none, only = gated_backward(dh, x, w, gu, "swiglu", dx=False)
+    assert none is None and torch.equal(only, dw)
+    assert gated_backward(dh, x, w, gu, "swiglu", dx=False, dw=False) == (None, None)
+    bx = torch.full((M + 4, 112), 7.0, device="cuda", dtype=torch.bfloat16)
+    bw = torch.full((2 * F + 4, 112), 7.0, device="cuda", dtype=torch.float32)
+    gated_backward(dh, x, w, gu, "swiglu", dx=bx[2:-2, 8:98], dw=bw[2:-2, 8:98])
+    assert torch.equal(bx[2:-2, 8:98], dx) and torch.equal(bw[2:-2, 8:98].to(torch.bfloat16), dw)
+    bx[2:-2, 8:98] = 7
+    bw[2:-2, 8:98] = 7
+    assert (bx == 7).all() and (bw == 7).all()
+
+
+def test_gated_gradients_of_special_values():
+    """Gates far out: nothing overflows; an infinite or NaN gradient reaches its
+    own row of dx only."""
+    import torch
+
+    n = 16
+    gates = torch.tensor([0, 1e-3, -1e-3, 5, -5, 50, -50, 88, -88, 150, -150, 3e4, -3e4, 1e25, -1e25, -0.0])
+    gu = torch.stack([gates.repeat(n, 1), torch.full((n, n), 1.5)], 1).to(torch.bfloat16).cuda()
+    x, w, dh = torch.eye(n).bfloat16(), torch.cat([torch.eye(n)] * 2).bfloat16(), torch.ones(n, n).bfloat16()
+    for act in ("swiglu", "geglu"):
+        dx, dw = gated_backward(dh, x, w, gu, act, dw_dtype=torch.float32)
+        g, u = f64(gu[:, 0]), f64(gu[:, 1])
+        dg, du = ref.gate_gradients(f64(dh), g, u, act)
+        eg, eu = ref.gate_gradient_error(f64(dh), g, u, act)
+        tiny = 2.0 ** -126  # what the products may flush
+        check_rounded(f64(dw)[:n], dg.T, (eg + HALF_STEP["bf16"] * np.abs(dg) + tiny).T, "f32")
+        check_rounded(f64(dw)[n:], du.T, (eu + HALF_STEP["bf16"] * np.abs(du) + tiny).T, "f32")
+    dh[3, 2], dh[7, 1] = float("inf"), float("nan")
+    dx, _ = gated_backward(dh, x, w, gu, "swiglu")
+    assert np.isfinite(np.delete(f64(dx), [3, 7], 0)).all()
+    assert not np.isfinite(f64(dx)[3]).all() and not np.isfinite(f64(dx)[7]).all()
+
+
+def test_gradients_against_differences():
+    """The loss sum(r * h(x, W)) moves along a direction as the gradients say.
+    (In 64 bits between the two ends; what the kernels' roundings leave is
+    bounded by their outputs' norms: 2^-8 of g, u, dg, du and of the outputs.)"""
+    rng = np.random.default_rng(4)
+    M, F, K = 40, 56, 48
+    for act in ("swiglu", "geglu"):
+        x, w = normal(rng, (M, K), "bf16"), normal(rng, (2 * F, K), "bf16", K ** -0.5)
+        r = normal(rng, (M, F), "bf16")
+        _, gu = forward(x, w, act)
+        dx, dw = gated_backward(r, x, w, gu, act)
+        X, W, R = f64(x), f64(w), f64(r)
+
+        def loss(X, W):
+            GU = X @ W.T
+            return (R * ref.gate(GU[:, :F], GU[:, F:], act)).sum()
+
+        for _ in range(4):
+            ex, ew = rng.normal(0, 1, X.shape), rng.normal(0, K ** -0.5, W.shape)
+            s = 1e-4
+            slope = (loss(X + s * ex, W + s * ew) - loss(X - s * ex, W - s * ew)) / (2 * s)
+            told = (f64(dx) * ex).sum() + (f64(dw) * ew).sum()
+            size = np.linalg.norm(f64(dx)) * np.linalg.norm(ex) + np.linalg.norm(f64(dw)) * np.linalg.norm(ew)
+            assert abs(slope - told) <= 4 * HALF_STEP["bf16"] * size
+
+
+def test_a_captured_training_step():
+    """Forward and backward in one graph, replayed with new contents between
+    eager work; a second graph of other sizes beside it keeps its own
+    workspace."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    def step_of(M, F, K):
+        x = torch.empty(M, K, device="cuda", dtype=torch.bfloat16)
+        w = torch.empty(2 * F, K, device="cuda", dtype=torch.bfloat16)
+        dh = torch.empty(M, F, device="cuda", dtype=torch.bfloat16)
+
+        def fill():
+            x.normal_()
+            w.normal_(0, K ** -0.5)
+            dh.normal_()
+
+        def step():
+            h, gu = g.gated_matmul(x, w, save=True)
+            return (h, *g.gated_matmul_backward(dh, x, w, gu))
+
+        fill()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            outs = step()
+        return fill, step, graph, outs
+
+    assert g.gated_backward_config_name(2048, 64, 64, True).split("_k")[1] != "1"
+    a, b = step_of(2048, 64, 64), step_of(600, 88, 200)
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(4):
+        a[0]()
+        b[0]()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(one):
+            a[2].replay()
+        with torch.cuda.stream(two):
+            b[2].replay()
+        torch.cuda.synchronize()
+        for fill, step, graph, outs in (a, b):
+            for p, q in zip(outs, step()):
+                assert torch.equal(p, q)
