@@ -471,14 +471,15 @@ __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
 // of tiles, where no other workgroup reads the same B.
 //
 // LAYOUT kNN, kTN: an operand whose rows lie along K is staged in pieces of 64
-// (K) x 64, each 64 LDS rows of 128 bytes as the other form's, so that a load
-// of 512 threads still fills the same rows or columns of the tile.  Fragments
-// are transposed on their way out of LDS: ds_read_b64_tr_b16 takes 4 (K) x 16
-// per 16 lanes and gives each lane its column's four values, so four reads
-// make the two chunks of a fragment, in the same K order as the other form's.
-// The 32-byte column group that a row holds in place u is u ^ (k / 2 % 2 + 2
-// (k / 8 % 2)): the eight rows that half a wave reads then lie in eight
-// different 32-byte groups of the 64 banks.  Rows past K are out of the
+// (K) x 64 (a workgroup of 512) or x 32 (of 256), one load of all threads
+// each, so that a load still fills the rows or columns of the tile that it
+// does in the other form.  Fragments are transposed on their way out of LDS:
+// ds_read_b64_tr_b16 takes 4 (K) x 16 per 16 lanes and gives each lane its
+// column's four values, so four reads make the two chunks of a fragment, in
+// the same K order as the other form's.  The 32-byte column group that row k
+// of a piece holds in place u is u ^ (k / 2 % 2 + 2 (k / 8 % 2)), or u ^ (k /
+// 8 % 2) in pieces of 32: the eight rows that half a wave reads then lie in
+// eight different 32-byte groups of the 64 banks.  Rows past K are out of the
 // range of a step's buffer resource and read as zeros.
 template <int BM, int BN, int WM, int WN, int WK, int S, int OP, int OUT, int MODE = kPlain,
           bool NT = false, int LAYOUT = kNT>
@@ -522,8 +523,10 @@ block_tile_kernel(BlockArgs a) {
   constexpr bool kGrad = LAYOUT != kNT, kTransA = LAYOUT == kTN, kTransB = kGrad;
   static_assert(!kGrad || (WK == 1 && OP != kOpE4m3 && OP != kOpI8 && MODE == kPlain && !NT),
                 "gradients are of 16-bit types");
-  static_assert(!kGrad || (Cfg::kWaveM % 64 == 0 && Cfg::kWaveN % 64 == 0 && 64 % RPI == 0),
-                "whole pieces of 64 columns");
+  constexpr int kPiece = RPI;  // columns of a piece
+  static_assert(!kGrad || ((kPiece == 32 || kPiece == 64) && Cfg::kWaveM % kPiece == 0 &&
+                           Cfg::kWaveN % kPiece == 0),
+                "whole pieces");
   const int row_tiles = a.offsets ? count_row_tiles(a, BM, lane) : a.row_tiles;
   const int units = row_tiles * a.tiles_n;
   if (!kGrad && (int)blockIdx.x >= units) return;  // the grid is an upper bound
@@ -576,10 +579,12 @@ block_tile_kernel(BlockArgs a) {
   for (int i = 0; i < L; ++i) {
     const int row = (i < LA ? i : i - LA) * RPI + r0;
     if (i < LA ? kTransA : kTransB) {
-      // K row `row % 64` of a piece of 64 columns
-      const int col = row / 64 * 64 + ((tid & 7) ^ (((r0 >> 1) & 1) << 1 | ((r0 >> 3) & 1) << 2)) * 8;
+      // piece i (or i - LA), its row k and the 16 bytes there
+      const int k = tid / (kPiece / 8), place = tid % (kPiece / 8);
+      const int swap = kPiece == 64 ? ((k >> 1) & 1) << 1 | ((k >> 3) & 1) << 2 : ((k >> 3) & 1) << 1;
+      const int col = (i < LA ? i : i - LA) * kPiece + (place ^ swap) * 8;
       const int ld = (int)(i < LA ? a.lda : a.ldb);
-      voff[i] = col < (i < LA ? rows_a : rows_b) ? (uint32_t)(row % 64 * ld + col * 2) : kOOB;
+      voff[i] = col < (i < LA ? rows_a : rows_b) ? (uint32_t)(k * ld + col * 2) : kOOB;
     } else if (i < LA) {
       const int src = row < rows_a ? (gather ? source_row(a, m0 + row) : row) : -1;
       voff[i] = src >= 0 ? (uint32_t)(src * (int)a.lda + chunk * 16) : kOOB;
@@ -704,19 +709,22 @@ block_tile_kernel(BlockArgs a) {
   using Frag = typename St::Frag;
   // (rows along K: this lane's place in the first 4 x 16 of a piece, and the
   // XOR of its column group)
-  const int at_k = ((lane >> 4) * 8 + (lrow >> 2)) * kStepBytes + (lrow & 3) * 8;
-  const int group_k = ((lrow >> 3) & 1) << 5 | ((lane >> 4) & 1) << 6;
+  constexpr int kPieceRow = kPiece * 2;  // bytes
+  const int at_k = ((lane >> 4) * 8 + (lrow >> 2)) * kPieceRow + (lrow & 3) * 8;
+  const int group_k = kPiece == 64 ? ((lrow >> 3) & 1) << 5 | ((lane >> 4) & 1) << 6
+                                   : ((lane >> 4) & 1) << 5;
   auto read_cols = [&](const lds_u8* base, int f) __attribute__((always_inline)) {
     typedef short i16x4 __attribute__((ext_vector_type(4)));
     typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
-    const lds_u8* p = base + f / 4 * (64 * kStepBytes) + at_k + (group_k ^ (f % 4 * 32));
+    constexpr int kGroups = kPiece / 16;
+    const lds_u8* p = base + f / kGroups * (64 * kPieceRow) + at_k + (group_k ^ (f % kGroups * 32));
     Frag r;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const u32x2 x = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + h * 32 * kStepBytes)));
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + h * 32 * kPieceRow)));
       const u32x2 y = __builtin_bit_cast(
-          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + (h * 32 + 4) * kStepBytes)));
+          u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(p + (h * 32 + 4) * kPieceRow)));
       r.v[h] = (u32x4){x[0], x[1], y[0], y[1]};
     }
     return r;

@@ -33,7 +33,7 @@ struct GradTile {
 };
 const GradTile kTiles[] = {
     {"b256x256", 256, 256, 512, 1.60, 6.0, &launch_grad_tile<256, 256, 2, 4, 2>},
-    {"b128x128", 128, 128, 256, 0.60, 3.5, &launch_grad_tile<128, 128, 2, 2, 4>},
+    {"b128x128", 128, 128, 256, 0.60, 3.5, &launch_grad_tile<128, 128, 2, 2, 2>},
 };
 
 struct GradPlan {

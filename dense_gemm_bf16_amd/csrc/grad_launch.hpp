@@ -34,7 +34,7 @@ hipError_t launch_grad_tile(const BlockArgs& a, int grid, hipStream_t s, int op,
 // Built shapes: X(name, launcher template arguments).
 #define GRAD_TILES(X)             \
   X(b256x256, 256, 256, 2, 4, 2)  \
-  X(b128x128, 128, 128, 2, 2, 4)
+  X(b128x128, 128, 128, 2, 2, 2)
 
 #define GRAD_DECLARE(NAME, A, B, C, D, S)                                                 \
   extern template hipError_t launch_grad_tile<A, B, C, D, S>(const BlockArgs&, int, \
