@@ -128,6 +128,8 @@ for _name in ("gemm_backward_config_name", "gemm_gated_backward_config_name"):
     getattr(_lib, _name).argtypes = [_i64, _i64, _i64, _c_int]
 _lib.gemm_i8_config_name.restype = ctypes.c_char_p
 _lib.gemm_i8_config_name.argtypes = [_i64, _i64, _i64]
+_lib.gemm_i8_config_at.restype = ctypes.c_char_p
+_lib.gemm_i8_config_at.argtypes = [ctypes.c_int]
 _lib.gemm_gated_config_name.restype = ctypes.c_char_p
 _lib.gemm_gated_config_name.argtypes = [_c_int, _i64, _i64, _i64]
 _lib.gemm_fp8_config_at.restype = ctypes.c_char_p
@@ -508,6 +510,21 @@ def i8_config_name(M, N, K) -> str:
 def gated_config_name(type, M, F, K) -> str:
     """The kernel shape the gated product of a type chooses."""
     return _lib.gemm_gated_config_name(type, M, F, K).decode()
+
+
+def gemm_i8_config_at(i: int):
+    """The i-th kernel shape of gemm_i8 and the gated products, or None past
+    the end."""
+    n = _lib.gemm_i8_config_at(i)
+    return None if n is None else n.decode()
+
+
+def i8_config_names() -> list[str]:
+    """The kernel shapes built for gemm_i8 and the gated products."""
+    out = []
+    while (n := gemm_i8_config_at(len(out))) is not None:
+        out.append(n)
+    return out
 
 
 gemm_i8_config_name = i8_config_name

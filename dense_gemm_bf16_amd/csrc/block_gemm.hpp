@@ -1044,15 +1044,19 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const void* base, ui
 // layout (a lane holds two 16-byte chunks of its row), U steps ahead; the
 // waves' sums meet in LDS and are added in the order of the waves.
 //
-// MODE kGated: fragments of B in turn from the gate's and the up projection's
-// rows (FN = 2: 16 columns of H).
-template <int FM, int FN, int W, int U, int OP, int OUT, int MODE = kPlain>
+// MODE kGated: a fragment of B is BR / 2 rows of the gate and the same ones of
+// the up projection, so that few columns still make as many workgroups.  BR 8:
+// half a fragment's rows, the rest of it left out of the loads, so that twice
+// as many CUs read (one takes in about 23 bytes a ns, whatever it has in
+// flight: 8 steps ahead, or 16 waves, were no faster).
+template <int FM, int FN, int W, int U, int OP, int OUT, int MODE = kPlain, int BR = 16>
 __global__ __attribute__((amdgpu_flat_work_group_size(W * 64, W * 64))) void
 block_row_kernel(BlockArgs a) {
   constexpr bool kScaled = OP == kOpE4m3;
   constexpr bool kPairs = MODE == kGated;
-  static_assert(!kPairs || FN == 2, "one fragment of the gate, one of the up projection");
-  constexpr int BM = 16 * FM, BN = kPairs ? 16 : 16 * FN;
+  static_assert((!kPairs && BR == 16) || FN == 1, "one fragment of both");
+  static_assert(BR == 16 || BR == 8, "whole or half fragments");
+  constexpr int BM = 16 * FM, BN = kPairs ? BR / 2 : BR * FN;  // rows and columns of C
   static_assert(kScaleBlock % BN == 0, "the tile's columns share one scale");
   __shared__ f32x4 sums[W][FM * FN][64];
 
@@ -1077,8 +1081,11 @@ block_row_kernel(BlockArgs a) {
              : buffer_of(a.A + (int64_t)m0 * a.lda, (uint32_t)(rows_a * a.lda));
   const __amdgpu_buffer_rsrc_t rsrc_b = buffer_of(a.B + tile.expert * a.stride_b + (int64_t)n0 * a.ldb,
                                  (uint32_t)(rows_b * a.ldb));
-  const __amdgpu_buffer_rsrc_t rsrc_u =
-      kPairs ? buffer_of(a.B + a.up_b + (int64_t)n0 * a.ldb, (uint32_t)(rows_b * a.ldb)) : rsrc_b;
+  // gated: the lanes of a fragment read two places of W, more than a buffer
+  // resource may span apart; rows past the last column read its row again
+  const uint8_t* const pair_row =
+      a.B + (lrow < BR / 2 ? 0 : a.up_b) +
+      (int64_t)(n0 + min(lrow % (BR / 2), rows_b - 1)) * a.ldb + lchunk;
   uint32_t va[FM], vb[FN], vs[FM];
 #pragma unroll
   for (int i = 0; i < FM; ++i) {
@@ -1089,7 +1096,7 @@ block_row_kernel(BlockArgs a) {
   }
 #pragma unroll
   for (int j = 0; j < FN; ++j) {
-    const int row = kPairs ? lrow : j * 16 + lrow;
+    const int row = j * 16 + lrow;
     vb[j] = row < rows_b ? (uint32_t)(row * (int)a.ldb + lchunk) : kOOB;
   }
   const float* sb_row = !kScaled ? nullptr : a.SB + tile.expert * a.stride_sb + (int64_t)(n0 / kScaleBlock) * a.ldsb;
@@ -1115,10 +1122,18 @@ block_row_kernel(BlockArgs a) {
     };
     const std::true_type nt{};    // B is read by this workgroup alone
     const std::false_type keep{};
+    if constexpr (kPairs) {
+      // (a chunk past K: any, `multiply` clears it)
+      if (lrow < BR) {
+        s.fb[0][0] = __builtin_nontemporal_load((const u32x4*)(pair_row + (in0 ? k0 : -lchunk)));
+        s.fb[0][1] = __builtin_nontemporal_load((const u32x4*)(pair_row + (in1 ? k0 + 64 : -lchunk)));
+      }
+    } else {
 #pragma unroll
-    for (int j = 0; j < FN; ++j) {
-      s.fb[j][0] = get(kPairs && j ? rsrc_u : rsrc_b, vb[j], in0, 0, nt);
-      s.fb[j][1] = get(kPairs && j ? rsrc_u : rsrc_b, vb[j], in1, 64, nt);
+      for (int j = 0; j < FN; ++j) {
+        s.fb[j][0] = get(rsrc_b, vb[j], in0, 0, nt);
+        s.fb[j][1] = get(rsrc_b, vb[j], in1, 64, nt);
+      }
     }
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
@@ -1147,7 +1162,7 @@ block_row_kernel(BlockArgs a) {
     }
   };
   auto multiply = [&](Stage& s, int X) __attribute__((always_inline)) {
-    if (X == a.k_steps - 1 && (a.kbytes & 15) != 0) {
+    if (X == a.k_steps - 1 && (a.kbytes & (kPairs ? kStepBytes - 1 : 15)) != 0) {
       const int keep = a.kbytes - X * kStepBytes - lchunk;
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
@@ -1219,12 +1234,12 @@ block_row_kernel(BlockArgs a) {
     }
   };
   if constexpr (kPairs) {
-    for (int q = tid; q < FM * 64; q += W * 64) {
-      const int i = q >> 6, l = q & 63;
+    for (int q = tid; q < FM * 2 * BR; q += W * 64) {
+      const int i = q / (2 * BR), l = q % (2 * BR);
       const int row = i * 16 + (l & 15), n = n0 + 4 * (l >> 4);
       if (row >= rows_a) continue;
-      const f32x4 g = scaled(total(2 * i, l), a.SB, row, n);
-      const f32x4 u = scaled(total(2 * i + 1, l), a.SB + a.up_sb, row, n);
+      const f32x4 g = scaled(total(i, l), a.SB, row, n);
+      const f32x4 u = scaled(total(i, l + 2 * BR), a.SB + a.up_sb, row, n);
       f32x4 h;
 #pragma unroll
       for (int r = 0; r < 4; ++r) h[r] = gate<OUT>(g[r], u[r], a.geglu != 0);
@@ -1240,7 +1255,7 @@ block_row_kernel(BlockArgs a) {
     for (int q = tid; q < FM * FN * 64; q += W * 64) {
       const int f = q >> 6, l = q & 63;
       const int row = (f / FN) * 16 + (l & 15), n = n0 + (f % FN) * 16 + 4 * (l >> 4);
-      if (row < rows_a) store_quad<OUT>(a.C, a.ldc, scaled(total(f, l), a.SB, row, n), m0 + row, n, a.N);
+      if (row < rows_a && l < 4 * BR) store_quad<OUT>(a.C, a.ldc, scaled(total(f, l), a.SB, row, n), m0 + row, n, a.N);
     }
   }
 }

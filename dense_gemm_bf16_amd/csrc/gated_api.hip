@@ -29,54 +29,69 @@ struct Cost {
 struct Shape {
   GatedConfig built;
   int k_groups, resident;
-  int gated_rows;  // rows of B of a workgroup with paired columns
-  Cost cost;
+  Cost ints, halves;  // of 8-bit integers, of 16-bit types
 };
 const Shape kShapes[] = {
 #define ROW(NAME, A, B, C, D, E, S, RESIDENT, ...)                                        \
   {{#NAME, A, B, (C) * (D) * (E) * 64, (B) / (D) / 16 % 2 == 0,                           \
-    &launch_gated_tile<A, B, C, D, E, S>}, E, RESIDENT, B, __VA_ARGS__},
-    ROW(b256x256, 256, 256, 2, 4, 1, 2, 1, {1.586f, 6.15f, 0.69f, 2.19f})
-    ROW(b256x128, 256, 128, 4, 2, 1, 3, 1, {0.932f, 4.29f, 0.76f, 1.51f})
-    ROW(b128x128, 128, 128, 2, 2, 1, 2, 2, {1.032f, 3.95f, 0.55f, 2.44f})
-    ROW(b128x128k2, 128, 128, 2, 2, 2, 2, 1, {1.172f, 5.23f, 0.83f, 1.37f})
-    ROW(b64x128k2, 64, 128, 2, 2, 2, 3, 1, {0.873f, 3.68f, 0.75f, 1.39f})
-    ROW(b64x64, 64, 64, 2, 2, 1, 4, 2, {0.492f, 3.41f, 0.67f, 1.06f})
-    ROW(b64x64k2, 64, 64, 2, 2, 2, 4, 1, {0.528f, 3.97f, 0.84f, 0.44f})
-    ROW(b32x128, 32, 128, 1, 4, 1, 3, 2, {0.645f, 3.14f, 0.62f, 0.83f})
-    ROW(b32x64k4, 32, 64, 2, 2, 4, 3, 1, {0.678f, 4.52f, 0.88f, 0.00f})
-    ROW(b32x32k4, 32, 32, 2, 2, 4, 4, 1, {0.508f, 3.15f, 0.96f, 1.30f})
+    &launch_gated_tile<A, B, C, D, E, S>}, E, RESIDENT, __VA_ARGS__},
+    ROW(b256x256, 256, 256, 2, 4, 1, 2, 1,
+        {1.478f, 13.89f, 0.64f, 0.00f}, {1.415f, 14.41f, 0.76f, 0.00f})
+    ROW(b256x128, 256, 128, 4, 2, 1, 3, 1,
+        {0.836f, 9.01f, 0.70f, 0.00f}, {0.930f, 7.85f, 0.71f, 0.00f})
+    ROW(b128x128, 128, 128, 2, 2, 1, 2, 2,
+        {0.841f, 9.28f, 0.50f, 0.18f}, {0.929f, 7.23f, 0.51f, 0.00f})
+    ROW(b128x128k2, 128, 128, 2, 2, 2, 2, 1,
+        {1.051f, 6.47f, 0.79f, 1.07f}, {1.098f, 5.72f, 0.81f, 0.81f})
+    ROW(b64x128k2, 64, 128, 2, 2, 2, 3, 1,
+        {0.714f, 4.19f, 0.86f, 0.92f}, {0.755f, 3.96f, 0.88f, 0.54f})
+    ROW(b64x64, 64, 64, 2, 2, 1, 4, 2,
+        {0.403f, 3.02f, 0.57f, 1.75f}, {0.426f, 2.64f, 0.59f, 1.64f})
+    ROW(b64x64k2, 64, 64, 2, 2, 2, 4, 1,
+        {0.434f, 3.24f, 0.86f, 1.52f}, {0.475f, 2.78f, 0.85f, 1.94f})
+    ROW(b32x128, 32, 128, 1, 4, 1, 3, 2,
+        {0.537f, 3.06f, 0.60f, 0.95f}, {0.586f, 1.59f, 0.61f, 1.14f})
+    ROW(b32x64k4, 32, 64, 2, 2, 4, 3, 1,
+        {0.644f, 3.33f, 0.91f, 1.48f}, {0.678f, 3.10f, 0.89f, 1.79f})
+    ROW(b32x32k4, 32, 32, 2, 2, 4, 4, 1,
+        {0.413f, 3.12f, 0.97f, 1.03f}, {0, 0, 0, 0})
 #undef ROW
-    {{"r16x16", 16, 16, 512, true, &launch_gated_row<1, 1, 8, 4>}, 8, 4, 32,
-     {2.435f, 1.11f, 0.24f, 3.08f}},
+#define ROW(NAME, A, B, C, D, E, RESIDENT, ...)                                             \
+  {{#NAME, 16 * (A), (E) * (B), (C) * 64, true, &launch_gated_row<A, B, C, D, E>}, C, RESIDENT, \
+   __VA_ARGS__},
+    ROW(r16x16, 1, 1, 8, 4, 16, 4,
+        {3.197f, 2.25f, 0.16f, 2.37f}, {2.928f, 3.80f, 0.17f, 2.29f})
+    ROW(r16x8, 1, 1, 8, 4, 8, 4,
+        {2.212f, 2.33f, 0.15f, 2.30f}, {2.210f, 3.06f, 0.12f, 2.50f})
+    ROW(r32x16, 2, 1, 8, 4, 16, 4,
+        {3.386f, 3.55f, 0.24f, 1.89f}, {3.613f, 3.77f, 0.20f, 2.44f})
+#undef ROW
 };
-constexpr double kStreamMBPerUs = 5.2, kStreamBaseUs = 2.5;
+constexpr double kStreamMBPerUs = 6.3, kStreamBaseUs = 2.2;
+constexpr double kSecondLaunchUs = 2.5, kSplitGain = 0.93;
 
 // A product as the choice sees it: rows of A and of B, bytes of a row and from
 // row to row, and whether B's rows are paired.
 struct Product {
   int64_t M, rows_b, k_bytes, lda, ldb;
-  bool gated;
+  bool gated, ints;
 };
 
-int rows_of_b(const Shape& s, bool gated) { return gated ? s.gated_rows : s.built.bn; }
-
-int64_t tiles_n(const Shape& s, const Product& p, int64_t rows_b) {
-  const int bn = rows_of_b(s, p.gated);
-  return (rows_b + bn - 1) / bn;
+int64_t tiles_n(const Shape& s, int64_t rows_b) {
+  return (rows_b + s.built.bn - 1) / s.built.bn;
 }
 
 // Whether a shape can run rows_b rows of B (see the block products).
 bool fits(const Shape& s, const Product& p, int64_t rows_b) {
   if (p.gated && !s.built.gated) return false;
-  if (rows_of_b(s, p.gated) * p.ldb >= kRangeLimit || s.built.bm * p.lda >= kRangeLimit) return false;
-  return (p.M + s.built.bm - 1) / s.built.bm * tiles_n(s, p, rows_b) < 2 * k2G / s.built.threads;
+  if (s.built.bn * p.ldb >= kRangeLimit || s.built.bm * p.lda >= kRangeLimit) return false;
+  return (p.M + s.built.bm - 1) / s.built.bm * tiles_n(s, rows_b) < 2 * k2G / s.built.threads;
 }
 
 double model_time(const Shape& s, const Product& p, int64_t rows_b) {
-  const Cost& c = s.cost;
+  const Cost& c = p.ints ? s.ints : s.halves;
   const double units =
-      (double)((p.M + s.built.bm - 1) / s.built.bm) * (double)tiles_n(s, p, rows_b);
+      (double)((p.M + s.built.bm - 1) / s.built.bm) * (double)tiles_n(s, rows_b);
   const double pass = 256.0 * s.resident;
   double passes = (double)(int64_t)(units / pass);
   const double rest = units / pass - passes;
@@ -113,19 +128,19 @@ DensePlan choose(const Product& p) {
   double best = 0;
   DensePlan plan{cheapest(p, p.rows_b, &best), nullptr, p.rows_b};
   if (p.M < 1 || !plan.shape) return plan;
-  best *= 0.97;
+  best *= kSplitGain;
   for (const Shape& s : kShapes) {
-    const int64_t rows = (p.M + s.built.bm - 1) / s.built.bm, cols = tiles_n(s, p, p.rows_b);
+    const int64_t rows = (p.M + s.built.bm - 1) / s.built.bm, cols = tiles_n(s, p.rows_b);
     const int64_t pass = 256 * s.resident;
     if (rows > pass) continue;
-    const int64_t head = rows * cols / pass * pass / rows * rows_of_b(s, p.gated) / 128 * 128;
+    const int64_t head = rows * cols / pass * pass / rows * s.built.bn / 128 * 128;
     if (head <= 0 || head >= p.rows_b || !fits(s, p, head)) continue;
     const double t1 = model_time(s, p, head);
     if (t1 >= best) continue;
     double t2 = 0;
     const Shape* tail = cheapest(p, p.rows_b - head, &t2);
-    if (!tail || t1 + t2 >= best) continue;
-    best = t1 + t2;
+    if (!tail || t1 + t2 + kSecondLaunchUs >= best) continue;
+    best = t1 + t2 + kSecondLaunchUs;
     plan = DensePlan{&s, tail, head};
   }
   return plan;
@@ -171,7 +186,7 @@ int dense_product(const char* config, int type, bool gated, int64_t M, int64_t N
       (ldc & 7) != 0 || (GU && (ldgu & 7) != 0))
     return GEMM_ERR_MISALIGNED;
 
-  const Product p{M, gated ? 2 * N : N, K * es, lda * es, ldb * es, gated};
+  const Product p{M, gated ? 2 * N : N, K * es, lda * es, ldb * es, gated, ints};
   DensePlan plan{nullptr, nullptr, p.rows_b};
   if (config && config[0]) {
     plan.shape = shape_named(config);
@@ -208,7 +223,7 @@ int dense_product(const char* config, int type, bool gated, int64_t M, int64_t N
   auto launch = [&](const Shape& s, int64_t rows_b) {
     const int64_t row_tiles = (M + s.built.bm - 1) / s.built.bm;
     a.N = (int32_t)(gated ? rows_b / 2 : rows_b);
-    a.tiles_n = (int32_t)tiles_n(s, p, rows_b);
+    a.tiles_n = (int32_t)tiles_n(s, rows_b);
     a.row_tiles = (int32_t)row_tiles;
     // (one row of tiles: see the block products)
     a.k_rot = row_tiles == 1 ? 3 : 0;
@@ -234,7 +249,7 @@ const char* plan_name(int type, bool gated, int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0 || M >= k2G || N >= (gated ? k2G / 2 : k2G) || K >= k2G / 2 ||
       (ints && K > kMaxIntK) || (!ints && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16))
     return "invalid";
-  const DensePlan p = choose(Product{M, gated ? 2 * N : N, ints ? K : 2 * K, 0, 0, gated});
+  const DensePlan p = choose(Product{M, gated ? 2 * N : N, ints ? K : 2 * K, 0, 0, gated, ints});
   if (!p.shape) return "invalid";
   if (!p.tail) return p.shape->built.name;
   snprintf(g_plan_name, sizeof g_plan_name, "%s+%s", p.shape->built.name, p.tail->built.name);
@@ -288,6 +303,11 @@ int gemm_gated(int type, int64_t M, int64_t F, int64_t K, const void* X, int64_t
 
 const char* gemm_i8_config_name(int64_t M, int64_t N, int64_t K) {
   return gemm::plan_name(GEMM_TYPE_I8, false, M, N, K);
+}
+
+const char* gemm_i8_config_at(int i) {
+  const int n = (int)(sizeof gemm::kShapes / sizeof *gemm::kShapes);
+  return i >= 0 && i < n ? gemm::kShapes[i].built.name : nullptr;
 }
 
 const char* gemm_gated_config_name(int type, int64_t M, int64_t F, int64_t K) {

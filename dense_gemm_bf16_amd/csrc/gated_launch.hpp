@@ -67,14 +67,13 @@ hipError_t launch_gated_tile(const BlockArgs& a, int grid, hipStream_t s, int op
   });
 }
 
-// (rows: FN fragments of B plain, the gate's and the up projection's gated)
-template <int FM, int FN, int W, int U>
+template <int FM, int FN, int W, int U, int BR>
 hipError_t launch_gated_row(const BlockArgs& a, int grid, hipStream_t s, int op, int out,
                             bool gated, bool) {
   return by_gated_types(op, out, gated, [&](auto o, auto t, auto m) {
     constexpr int kMode = decltype(m)::value;
-    hipLaunchKernelGGL((block_row_kernel<FM, kMode == kGated ? 2 : FN, W, U, decltype(o)::value,
-                                         decltype(t)::value, kMode>),
+    hipLaunchKernelGGL((block_row_kernel<FM, FN, W, U, decltype(o)::value, decltype(t)::value, kMode,
+                                         BR>),
                        dim3(grid), dim3(W * 64), 0, s, a);
     return hipGetLastError();
   });
@@ -86,10 +85,16 @@ hipError_t launch_gated_row(const BlockArgs& a, int grid, hipStream_t s, int op,
                                                                  bool);
 BLOCK_TILES(GATED_DECLARE)
 #undef GATED_DECLARE
-#define GATED_DECLARE(NAME, A, B, C, D)                                                      \
-  extern template hipError_t launch_gated_row<A, B, C, D>(const BlockArgs&, int, hipStream_t, \
-                                                          int, int, bool, bool);
-BLOCK_ROWS(GATED_DECLARE)
+// The row kernel's shapes here: X(name, fragments of A and of B, waves, steps
+// ahead, rows of B in a fragment).
+#define GATED_ROWS(X)          \
+  X(r16x16, 1, 1, 8, 4, 16)    \
+  X(r16x8, 1, 1, 8, 4, 8)      \
+  X(r32x16, 2, 1, 8, 4, 16)
+#define GATED_DECLARE(NAME, A, B, C, D, E)                                                     \
+  extern template hipError_t launch_gated_row<A, B, C, D, E>(const BlockArgs&, int, hipStream_t, \
+                                                             int, int, bool, bool);
+GATED_ROWS(GATED_DECLARE)
 #undef GATED_DECLARE
 
 }  // namespace gemm

@@ -446,7 +446,7 @@ int gemm_i8(int64_t M, int64_t N, int64_t K,
             const void* B, int64_t ldb, const float* SB,
             void* C, int64_t ldc, int c_type, void* stream);
 
-/* As gemm_i8 with the kernel shape named (one that gemm_fp8_config_at
+/* As gemm_i8 with the kernel shape named (one that gemm_i8_config_at
  * enumerates; NULL or "" = automatic). */
 int gemm_i8_ex(const char* config, int64_t M, int64_t N, int64_t K,
                const void* A, int64_t lda, const float* SA,
@@ -455,6 +455,10 @@ int gemm_i8_ex(const char* config, int64_t M, int64_t N, int64_t K,
 
 /* Name of the kernel shape gemm_i8 chooses (see gemm_fp8_config_name). */
 const char* gemm_i8_config_name(int64_t M, int64_t N, int64_t K);
+
+/* The i-th kernel shape of gemm_i8 and the gated products, or NULL past the
+ * end. */
+const char* gemm_i8_config_at(int i);
 
 /* Quantise X (M rows of K, x_type BF16, F16 or F32; any row stride, aligned to
  * its type) to 8-bit integers Q (M x K, 16-byte aligned, ldq a multiple of 16;
@@ -498,7 +502,7 @@ int gemm_i8_gated(int64_t M, int64_t F, int64_t K,
                   const void* W, int64_t ldw, const float* SW, int act,
                   void* H, int64_t ldh, int h_type, void* stream);
 
-/* With the kernel shape named (of those that gemm_fp8_config_at enumerates, all
+/* With the kernel shape named (of those that gemm_i8_config_at enumerates, all
  * but b32x32k4, which does not hold whole pairs of columns). */
 int gemm_gated_ex(const char* config, int type, int64_t M, int64_t F, int64_t K,
                   const void* X, int64_t ldx, const void* W, int64_t ldw, int act,
