@@ -125,7 +125,7 @@ for _name in ("gemm_backward_work_size", "gemm_gated_backward_work_size"):
     getattr(_lib, _name).argtypes = [_i64, _i64, _i64]
 for _name in ("gemm_backward_config_name", "gemm_gated_backward_config_name"):
     getattr(_lib, _name).restype = ctypes.c_char_p
-    getattr(_lib, _name).argtypes = [_i64, _i64, _i64, _c_int]
+    getattr(_lib, _name).argtypes = [_i64, _i64, _i64]
 _lib.gemm_i8_config_name.restype = ctypes.c_char_p
 _lib.gemm_i8_config_name.argtypes = [_i64, _i64, _i64]
 _lib.gemm_i8_config_at.restype = ctypes.c_char_p
@@ -486,14 +486,14 @@ def gated_backward_work_size(M, F, K) -> int:
     return int(_lib.gemm_gated_backward_work_size(M, F, K))
 
 
-def backward_config_name(M, N, K, of_b=False) -> str:
-    """The tile and split of dA's product, or of dB's."""
-    return _lib.gemm_backward_config_name(M, N, K, 1 if of_b else 0).decode()
+def backward_config_name(M, N, K) -> str:
+    """The tile and the splits of K of both gradients' products."""
+    return _lib.gemm_backward_config_name(M, N, K).decode()
 
 
-def gated_backward_config_name(M, F, K, of_w=False) -> str:
-    """The tile and split of dX's product, or of dW's."""
-    return _lib.gemm_gated_backward_config_name(M, F, K, 1 if of_w else 0).decode()
+def gated_backward_config_name(M, F, K) -> str:
+    """The same of a gated product's gradients."""
+    return _lib.gemm_gated_backward_config_name(M, F, K).decode()
 
 
 gemm_backward_config_name = backward_config_name

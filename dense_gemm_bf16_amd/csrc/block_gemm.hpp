@@ -481,42 +481,54 @@ __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
 // 8 % 2) in pieces of 32: the eight rows that half a wave reads then lie in
 // eight different 32-byte groups of the 64 banks.  Rows past K are out of the
 // range of a step's buffer resource and read as zeros.
-template <int BM, int BN, int WM, int WN, int WK, int S, int OP, int OUT, int MODE = kPlain,
-          bool NT = false, int LAYOUT = kNT>
-__global__ __attribute__((amdgpu_flat_work_group_size(WM * WN * WK * 64, WM * WN * WK * 64),
-                          amdgpu_waves_per_eu(2))) void
-block_tile_kernel(BlockArgs a) {
+typedef const __attribute__((address_space(3))) float lds_f32;
+
+// Sizes of a tile's kernel.
+template <int BM, int BN, int WM, int WN, int WK, int S, int OP, int OUT>
+struct BlockTile {
   using Cfg = TileCfg<BM, BN, 64, WM, WN, S, 3, 16>;
+  static constexpr int kRowsPerLoad = Cfg::kThreads / 8;  // of one load of all threads
+  // A widened fragment takes twice the registers, too many for this form,
+  // and a load of all threads has to be half a wave row of A
+  static constexpr bool kPipe = S == 2 && (Cfg::kFragM == 4 || Cfg::kFragM == 8) &&
+                                kRowsPerLoad * 2 == Cfg::kWaveM && !Step<OP, OUT>::kWide;
+  static constexpr int kScaleCols = (BN + kScaleBlock - 1) / kScaleBlock;  // across a tile
+  static constexpr int kRowScales = BM < 64 ? 64 : BM;                     // of a slot
+  static constexpr int kScaleSlots = kPipe ? 3 : S;
+  static constexpr int kRingBytes = WK * Cfg::kLdsBytes;
+  static constexpr int kRowScaleFloats = OP == kOpE4m3 ? WK * kScaleSlots * kRowScales : 1;
+  static constexpr int kColScaleFloats = OP == kOpE4m3 ? kScaleCols * kMaxKSteps : 1;
+};
+
+// Workgroup `block`'s tile; ring, sa_lds and sb_lds: BlockTile's LDS.
+template <int BM, int BN, int WM, int WN, int WK, int S, int OP, int OUT, int MODE, bool NT,
+          int LAYOUT>
+__device__ __forceinline__ void block_tile(const BlockArgs& a, int block, lds_u8* ring,
+                                           lds_f32* sa_lds, lds_f32* sb_lds) {
+  using Tile = BlockTile<BM, BN, WM, WN, WK, S, OP, OUT>;
+  using Cfg = typename Tile::Cfg;
   constexpr int T = Cfg::kThreads, W = WM * WN;  // threads and waves of one K group
   constexpr int FM = Cfg::kFragM, FN = Cfg::kFragN;
   constexpr int LA = Cfg::kLoadsA, LB = Cfg::kLoadsB, L = LA + LB;
-  constexpr int RPI = T / 8;  // rows of one load of all threads
+  constexpr int RPI = Tile::kRowsPerLoad;
   constexpr bool kScaled = OP == kOpE4m3;
   using St = Step<OP, OUT>;
-  // A widened fragment takes twice the registers, too many for this form,
-  // and a load of all threads has to be half a wave row of A
-  constexpr bool kPipe = S == 2 && (FM == 4 || FM == 8) && RPI * 2 == Cfg::kWaveM && !St::kWide;
-  constexpr int NB = (BN + kScaleBlock - 1) / kScaleBlock;  // scale blocks across a tile
-  constexpr int SA = BM < 64 ? 64 : BM;                     // row scales of a slot
-  constexpr int SS = kPipe ? 3 : S;                         // slots of row scales
+  constexpr bool kPipe = Tile::kPipe;
+  constexpr int NB = Tile::kScaleCols, SA = Tile::kRowScales, SS = Tile::kScaleSlots;
   constexpr int kInFlight = (S - 2) * (L + (kScaled ? 1 : 0));
   static_assert(RPI % 16 == 0, "the swizzle repeats every 16 rows");
   static_assert(kScaleBlock % Cfg::kWaveN == 0, "a wave's columns share one scale");
   static_assert(SA / 64 <= W, "one wave loads 64 row scales");
   static_assert(kInFlight < 64, "vmcnt range");
 
-  __shared__ __attribute__((aligned(1024))) uint8_t smem_raw[WK * Cfg::kLdsBytes];
-  __shared__ float sa_lds[kScaled ? WK * SS * SA : 1];
-  __shared__ float sb_lds[kScaled ? NB * kMaxKSteps : 1];
   const int tid = threadIdx.x % T;
   const int lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int kg = WK > 1 ? __builtin_amdgcn_readfirstlane((int)threadIdx.x / T) : 0;
-  lds_u8* const smem = (lds_u8*)smem_raw + kg * Cfg::kLdsBytes;
+  lds_u8* const smem = ring + kg * Cfg::kLdsBytes;
   const uint32_t smem_addr = (uint32_t)(uintptr_t)smem;
-  typedef const __attribute__((address_space(3))) float lds_f32;
-  lds_f32* const sa_s = (lds_f32*)sa_lds + kg * SS * SA;
-  lds_f32* const sb_s = (lds_f32*)sb_lds;
+  lds_f32* const sa_s = sa_lds + kg * SS * SA;
+  lds_f32* const sb_s = sb_lds;
   const int wm = wave / WN, wn = wave % WN;
 
   // ---- which tile --------------------------------------------------------
@@ -529,8 +541,8 @@ block_tile_kernel(BlockArgs a) {
                 "whole pieces");
   const int row_tiles = a.offsets ? count_row_tiles(a, BM, lane) : a.row_tiles;
   const int units = row_tiles * a.tiles_n;
-  if (!kGrad && (int)blockIdx.x >= units) return;  // the grid is an upper bound
-  int logical = xcd_remap(blockIdx.x, kGrad ? units * a.splits : units);
+  if (!kGrad && block >= units) return;  // the grid is an upper bound
+  int logical = xcd_remap(block, kGrad ? units * a.splits : units);
   int split = 0;
   if constexpr (kGrad) {
     split = logical / units;
@@ -1001,7 +1013,7 @@ block_tile_kernel(BlockArgs a) {
             acc[i / FN][i % FN] =
                 add_sums<OP>(acc[i / FN][i % FN], mine[g * (Cfg::kLdsBytes / 16) + i * 64]);
       }
-      finish_gated<Cfg, OP, OUT, T * WK>(a, (lds_u8*)smem_raw, acc, m0, tile.end, n0, wm, wn, lane,
+      finish_gated<Cfg, OP, OUT, T * WK>(a, ring, acc, m0, tile.end, n0, wm, wn, lane,
                                          kg == 0);
       return;
     }
@@ -1024,6 +1036,43 @@ block_tile_kernel(BlockArgs a) {
     scale_sums<OP, FM, FN>(a, acc, tile.end, m0 + wm * Cfg::kWaveM, n0 + wn * Cfg::kWaveN, lane);
     finish_tile<Cfg, OUT, false>(c, smem, wave, m0, n0, acc, m0 + wm * Cfg::kWaveM,
                                  n0 + wn * Cfg::kWaveN, lane, 0);
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int WK, int S, int OP, int OUT, int MODE = kPlain,
+          bool NT = false>
+__global__ __attribute__((amdgpu_flat_work_group_size(WM * WN * WK * 64, WM * WN * WK * 64),
+                          amdgpu_waves_per_eu(2))) void
+block_tile_kernel(BlockArgs a) {
+  using Tile = BlockTile<BM, BN, WM, WN, WK, S, OP, OUT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[Tile::kRingBytes];
+  __shared__ float sa_lds[Tile::kRowScaleFloats];
+  __shared__ float sb_lds[Tile::kColScaleFloats];
+  block_tile<BM, BN, WM, WN, WK, S, OP, OUT, MODE, NT, kNT>(a, (int)blockIdx.x, (lds_u8*)ring,
+                                                            (lds_f32*)sa_lds, (lds_f32*)sb_lds);
+}
+
+// Both gradients of a product in one launch, kNN's tiles of `x` (to OUT_X) and
+// kTN's of `w` (to OUT_W): each alone would leave CUs idle in its last pass,
+// or in its only one.  Workgroups below `first` (a multiple of 8, so that
+// each tile stays with its XCD) are x's, or w's where w_first, the others the
+// other's; either may have none.
+template <int BM, int BN, int WM, int WN, int S, int OP, int OUT_X, int OUT_W>
+__global__ __attribute__((amdgpu_flat_work_group_size(WM * WN * 64, WM * WN * 64),
+                          amdgpu_waves_per_eu(2))) void
+grad_pair_kernel(BlockArgs x, BlockArgs w, int first, int w_first) {
+  __shared__ __attribute__((aligned(1024)))
+  uint8_t ring[BlockTile<BM, BN, WM, WN, 1, S, OP, OUT_X>::kRingBytes];
+  __shared__ float none[1];
+  const int block = (int)blockIdx.x < first ? (int)blockIdx.x : (int)blockIdx.x - first;
+  if (((int)blockIdx.x < first) == (w_first != 0)) {
+    if (block < w.row_tiles * w.tiles_n * w.splits)
+      block_tile<BM, BN, WM, WN, 1, S, OP, OUT_W, kPlain, false, kTN>(
+          w, block, (lds_u8*)ring, (lds_f32*)none, (lds_f32*)none);
+  } else {
+    if (block < x.row_tiles * x.tiles_n * x.splits)
+      block_tile<BM, BN, WM, WN, 1, S, OP, OUT_X, kPlain, false, kNN>(
+          x, block, (lds_u8*)ring, (lds_f32*)none, (lds_f32*)none);
   }
 }
 

@@ -74,4 +74,16 @@ struct GateGradArgs {
 };
 hipError_t launch_gate_grad(const GateGradArgs& a, bool half, hipStream_t s);
 
+// C (rows x N) = the sum of `splits` parts (rows x ld fp32, `stride` apart),
+// in their order, rounded once to `out`.
+struct SumParts {
+  const float* parts;
+  int64_t rows, ld, stride;
+  int splits;  // 1 or less: nothing to do
+  void* C;
+  int64_t ldc, N;
+  int out;
+};
+hipError_t launch_sum_parts(const SumParts& x, const SumParts& w, hipStream_t s);
+
 }  // namespace gemm

@@ -317,8 +317,8 @@ const char* gemm_gated_config_name(int type, int64_t M, int64_t F, int64_t K) {
 int gemm_i8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_type, void* Q,
                      int64_t ldq, float* S, void* stream) {
   if (M < 0 || K < 0 || !gemm::is_float_type(x_type)) return GEMM_ERR_INVALID_ARG;
-  // (a workgroup of 256 a row: a grid holds fewer than 2^32 threads)
-  if (K >= gemm::k2G || M >= 2 * gemm::k2G / 256 || ldx >= (int64_t(1) << 40) ||
+  // (a workgroup of up to 1024 a row: a grid holds fewer than 2^32 threads)
+  if (K >= gemm::k2G || M >= 2 * gemm::k2G / 1024 || ldx >= (int64_t(1) << 40) ||
       ldq >= (int64_t(1) << 40))
     return GEMM_ERR_UNSUPPORTED;
   if (ldx < K || ldq < K) return GEMM_ERR_INVALID_ARG;

@@ -1,25 +1,30 @@
-// Gradient of h = act(g) u with act(g) = g s(z), s the sigmoid, z = g for silu
-// and z = 2 sqrt(2 / pi) (g + 0.044715 g^3) for gelu in its tanh form:
+// The elementwise parts of the gradients.
+//
+// Of h = act(g) u with act(g) = g s(z), s the sigmoid, z = g for silu and z =
+// 2 sqrt(2 / pi) (g + 0.044715 g^3) for gelu in its tanh form:
 //
 //   du = dh g s(z)        dg = dh u (s(z) + g s(z) s(-z) z'(g))
 //
 // from dh and the saved g and u, each rounded once to the operands' type: they
 // are operands of the two products that follow.  s(z) and s(-z) = 1 - s(z)
 // both come from e = exp(-|z|), so neither cancels and nothing overflows.
+// Three values read, two written: bound by memory.
 //
-// Elementwise, bound by memory: three values read, two written.
+// And the sum of a split product's parts, in their order.
 #include "block_internal.h"
 
 namespace gemm {
 namespace {
 
+constexpr int kRowGroups = 32768;  // rows of the grid's second dimension
+
 template <typename T>
 __global__ __launch_bounds__(256) void gate_grad_kernel(GateGradArgs a) {
   typedef T t8 __attribute__((ext_vector_type(8)));
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int64_t chunks = a.Fp >> 3;
-  if (i >= a.M * chunks) return;
-  const int64_t m = i / chunks, f = (i - m * chunks) * 8;
+  const int64_t f = ((int64_t)blockIdx.x * 64 + (threadIdx.x & 63)) * 8;
+  const int64_t m =
+      ((int64_t)blockIdx.z * kRowGroups + blockIdx.y) * 4 + (threadIdx.x >> 6);
+  if (f >= a.Fp || m >= a.M) return;
   const t8 dh = *(const t8*)((const T*)a.dH + m * a.lddh + f);
   const T* gu = (const T*)a.GU + m * a.ldgu + f;
   const t8 g8 = *(const t8*)gu, u8 = *(const t8*)(gu + a.Fp);
@@ -43,14 +48,51 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateGradArgs a) {
   *(t8*)(out + a.Fp) = du;
 }
 
+// Four columns a thread; the parts' loads do not wait for one another.
+__global__ __launch_bounds__(256) void sum_parts_kernel(SumParts x, SumParts w, int first) {
+  const bool is_x = (int)blockIdx.x < first;
+  const SumParts& p = is_x ? x : w;
+  const int64_t i = (int64_t)((int)blockIdx.x - (is_x ? 0 : first)) * 256 + threadIdx.x;
+  const uint32_t quads = (uint32_t)(p.ld >> 2);
+  if (i >= p.rows * quads) return;
+  const float* at = p.parts + i * 4;
+  f32x4 v = *(const f32x4*)at;
+  int s = 1;
+  for (; s + 4 <= p.splits; s += 4) {
+    f32x4 q[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = *(const f32x4*)(at + (s + j) * p.stride);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v += q[j];
+  }
+  for (; s < p.splits; ++s) v += *(const f32x4*)(at + s * p.stride);
+  const int64_t m = i / quads;
+  const int n = (int)(i - m * quads) * 4;
+  if (p.out == kStoreF32) store_quad<kStoreF32>(p.C, p.ldc, v, (int)m, n, (int)p.N);
+  else if (p.out == kStoreF16) store_quad<kStoreF16>(p.C, p.ldc, v, (int)m, n, (int)p.N);
+  else store_quad<kStoreBf16>(p.C, p.ldc, v, (int)m, n, (int)p.N);
+}
+
+int sum_blocks(const SumParts& p) { return (int)((p.rows * (p.ld >> 2) + 255) / 256); }
+
 }  // namespace
 
 hipError_t launch_gate_grad(const GateGradArgs& a, bool half, hipStream_t s) {
-  const int64_t blocks = (a.M * (a.Fp >> 3) + 255) / 256;
+  const int64_t groups = (a.M + 3) / 4;
+  const dim3 grid((unsigned)((a.Fp + 511) / 512), (unsigned)(groups < kRowGroups ? groups : kRowGroups),
+                  (unsigned)((groups + kRowGroups - 1) / kRowGroups));
   if (half)
-    hipLaunchKernelGGL(gate_grad_kernel<_Float16>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(gate_grad_kernel<_Float16>, grid, dim3(256), 0, s, a);
   else
-    hipLaunchKernelGGL(gate_grad_kernel<__bf16>, dim3((unsigned)blocks), dim3(256), 0, s, a);
+    hipLaunchKernelGGL(gate_grad_kernel<__bf16>, grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_sum_parts(const SumParts& x, const SumParts& w, hipStream_t s) {
+  const int first = x.splits > 1 ? sum_blocks(x) : 0;
+  const int rest = w.splits > 1 ? sum_blocks(w) : 0;
+  if (first + rest == 0) return hipSuccess;
+  hipLaunchKernelGGL(sum_parts_kernel, dim3((unsigned)(first + rest)), dim3(256), 0, s, x, w, first);
   return hipGetLastError();
 }
 

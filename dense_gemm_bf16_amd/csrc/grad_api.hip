@@ -24,56 +24,80 @@ struct GradShape {
   int64_t M, N, k;
   int parts, halves;
 };
+constexpr GradShape kNoProduct{0, 0, 0, 1, 1};
 
+// `resident` workgroups a CU; a workgroup's time is steps * step + tile with
+// all of them there, `part` of that where it has the GPU to itself (us).
 struct GradTile {
   const char* name;
-  int bm, bn, threads;
-  double step, tile;  // us: of a K-step of 64, of first loads and epilogue
-  hipError_t (*launch)(const BlockArgs&, int grid, hipStream_t, int op, int out, int layout);
+  int bm, bn, threads, resident;
+  double step, tile, part;
+  hipError_t (*launch)(const GradPair&, hipStream_t, int op, int out_x, int out_w);
 };
 const GradTile kTiles[] = {
-    {"b256x256", 256, 256, 512, 1.60, 6.0, &launch_grad_tile<256, 256, 2, 4, 2>},
-    {"b128x128", 128, 128, 256, 0.60, 3.5, &launch_grad_tile<128, 128, 2, 2, 2>},
+    {"b256x256", 256, 256, 512, 1, 1.42, 9.0, 0.75, &launch_grad_pair<256, 256, 2, 4, 2>},
+    {"b128x128", 128, 128, 256, 2, 0.93, 6.0, 0.51, &launch_grad_pair<128, 128, 2, 2, 2>},
 };
+constexpr double kSumUs = 3.5, kSumUsPerMB = 0.32;
 
 struct GradPlan {
   const GradTile* tile;
-  int splits;  // ways that K is split over workgroups
+  int split_x, split_w;  // ways that K is split over workgroups
 };
 
+int64_t up4(int64_t n) { return (n + 3) / 4 * 4; }
 int64_t tiles_of(const GradTile& t, const GradShape& p) {
   return (p.M + t.bm - 1) / t.bm * p.halves * ((p.N + t.bn - 1) / t.bn);
 }
 int64_t steps_of(const GradShape& p) { return (p.k + 63) / 64 * p.parts; }
+int64_t part_floats(const GradShape& p) { return p.M * p.halves * up4(p.N); }
+int64_t split_bytes(const GradShape& p, int splits) {
+  return splits > 1 ? 4 * splits * part_floats(p) : 0;
+}
 
-// The cheapest tile and split under the model of the dense products: passes of
-// 256 workgroups, a last one that is part full at two thirds to all of a
-// pass's time, and for a split the round trip of its fp32 sums.
-GradPlan choose(const GradShape& p) {
-  GradPlan best{nullptr, 1};
+// The tile and splits whose launch a model finds cheapest: as long as its
+// longest workgroup, shorter where the GPU is part empty, or as all of them
+// over the places there are; and for splits the round trip of their fp32 sums.
+GradPlan choose(const GradShape& x, const GradShape& w) {
+  GradPlan best{nullptr, 1, 1};
   double best_t = 0;
-  const int64_t steps = steps_of(p);
+  const int64_t steps[2] = {steps_of(x), steps_of(w)};
   for (const GradTile& t : kTiles) {
-    const int64_t tiles = tiles_of(t, p);
-    for (int s : {1, 2, 3, 4, 6, 8, 12, 16}) {
-      if (s > 1 && (steps / s < 4 || tiles * s > 1024)) break;
-      const int64_t per = (steps + s - 1) / s, units = tiles * s;
-      if (s > 1 && (steps + per - 1) / per != s) continue;
-      double passes = (double)(units / 256);
-      if (units % 256) passes += 0.67 + 0.33 * (double)(units % 256) / 256;
-      double us = passes * ((double)per * t.step + t.tile);
-      if (s > 1) us += 2.5 + 0.32e-6 * 4 * s * (double)p.M * p.halves * (double)up8(p.N);
-      if (best.tile && us >= best_t) continue;
-      best = GradPlan{&t, s};
-      best_t = us;
+    const int64_t tiles[2] = {tiles_of(t, x), tiles_of(t, w)};
+    const double places = 256.0 * t.resident;
+    for (int sx = 1; sx <= 16; sx *= 2) {
+      if (sx > 1 && (steps[0] / sx < 4 || tiles[0] * sx > 1024)) break;
+      for (int sw = 1; sw <= 16; sw *= 2) {
+        if (sw > 1 && (steps[1] / sw < 4 || tiles[1] * sw > 1024)) break;
+        const double ux = (double)((steps[0] + sx - 1) / sx) * t.step + t.tile;
+        const double uw = (double)((steps[1] + sw - 1) / sw) * t.step + t.tile;
+        const double nx = (double)(tiles[0] * sx), nw = (double)(tiles[1] * sw);
+        const double longest = nx > 0 && (ux > uw || nw == 0) ? ux : uw;
+        const double fill = (nx + nw) / places;
+        double us = longest * (t.part + (1 - t.part) * (fill < 1 ? fill : 1));
+        const double all = (nx * ux + nw * uw) / places;
+        if (fill > 1) us = all > us ? all + 0.3 * longest : us + 0.3 * longest;
+        if (sx > 1 || sw > 1)
+          us += kSumUs + kSumUsPerMB * 1e-6 * (double)(split_bytes(x, sx) + split_bytes(w, sw));
+        if (best.tile && us >= best_t) continue;
+        best = GradPlan{&t, sx, sw};
+        best_t = us;
+      }
     }
   }
+  // (splits that leave no workgroup empty)
+  auto even = [](int64_t n, int s) {
+    const int64_t per = s > 1 ? (n + s - 1) / s : 1;
+    return s > 1 ? (int)((n + per - 1) / per) : 1;
+  };
+  best.split_x = even(steps[0], best.split_x);
+  best.split_w = even(steps[1], best.split_w);
   return best;
 }
 
-int64_t split_bytes(const GradShape& p) {
-  const int s = choose(p).splits;
-  return s > 1 ? 4 * s * p.halves * p.M * up8(p.N) : 0;
+int64_t plan_bytes(const GradShape& x, const GradShape& w) {
+  const GradPlan p = choose(x, w);
+  return split_bytes(x, p.split_x) + split_bytes(w, p.split_w);
 }
 
 // Whether both tiles can run it: what a workgroup loads from one base lies
@@ -81,7 +105,7 @@ int64_t split_bytes(const GradShape& p) {
 bool runs(const GradShape& p, bool a_rows_m, int64_t lda, int64_t ldb) {
   for (const GradTile& t : kTiles)
     if ((a_rows_m ? t.bm : 64) * lda * 2 >= kRangeLimit || 64 * ldb * 2 >= kRangeLimit ||
-        tiles_of(t, p) >= 2 * k2G / t.threads)
+        tiles_of(t, p) >= k2G / t.threads)
       return false;
   return true;
 }
@@ -89,29 +113,26 @@ bool runs(const GradShape& p, bool a_rows_m, int64_t lda, int64_t ldb) {
 struct Operands {
   const void *A, *B;
   int64_t lda, ldb, seg_a, seg_b, half_a;  // elements
+  void* C;
+  int64_t ldc;
 };
 
-hipError_t grad_product(int layout, int type, const GradShape& p, const Operands& o, void* C,
-                        int64_t ldc, int c_type, void* work, hipStream_t stream) {
-  if (p.M == 0 || p.N == 0) return hipSuccess;
-  const GradPlan plan = choose(p);
-  const GradTile& t = *plan.tile;
-  const int64_t row_tiles = (p.M + t.bm - 1) / t.bm * p.halves, cols = (p.N + t.bn - 1) / t.bn;
-  const int64_t steps = steps_of(p);
-  const int store = c_type == GEMM_TYPE_F32 ? kStoreF32 : c_type == GEMM_TYPE_F16 ? kStoreF16 : kStoreBf16;
+BlockArgs product_args(const GradTile& t, const GradShape& p, const Operands& o, int splits,
+                       float* parts) {
+  const int64_t row_tiles = (p.M + t.bm - 1) / t.bm * p.halves, steps = steps_of(p);
   BlockArgs a{};
   a.A = (const uint8_t*)o.A;
   a.B = (const uint8_t*)o.B;
-  a.C = C;
+  a.C = splits > 1 ? parts : o.C;
   a.lda = o.lda * 2;
   a.ldb = o.ldb * 2;
-  a.ldc = ldc;
+  a.ldc = splits > 1 ? up4(p.N) : o.ldc;
   a.M = (int32_t)p.M;
   a.N = (int32_t)p.N;
   a.kbytes = (int32_t)(p.k * 2);
   a.a_rows = (int32_t)p.M;
   a.E = 1;
-  a.tiles_n = (int32_t)cols;
+  a.tiles_n = (int32_t)((p.N + t.bn - 1) / t.bn);
   a.k_steps = (int32_t)steps;
   a.row_tiles = (int32_t)row_tiles;
   a.group_m = 4;
@@ -120,21 +141,42 @@ hipError_t grad_product(int layout, int type, const GradShape& p, const Operands
   a.seg_b = o.seg_b * 2;
   a.half_tiles = (int32_t)(row_tiles / p.halves);
   a.half_a = o.half_a * 2;
-  a.splits = plan.splits;
-  a.split_steps = (int32_t)((steps + plan.splits - 1) / plan.splits);
-  const int64_t ldp = up8(p.N), rows = p.M * p.halves;
-  if (plan.splits > 1) {
-    a.C = work;
-    a.ldc = ldp;
-    a.part_stride = rows * ldp;
-  }
-  hipError_t e = t.launch(a, (int)(row_tiles * cols * plan.splits), stream,
-                          type == GEMM_TYPE_F16 ? kOpF16 : kOpBf16,
-                          plan.splits > 1 ? kStoreF32 : store, layout);
-  if (e == hipSuccess && plan.splits > 1)
-    e = launch_splitk_reduce((const float*)work, ldp, rows * ldp, plan.splits, C, ldc, (int)rows,
-                             (int)p.N, store, stream);
-  return e;
+  a.splits = splits;
+  a.split_steps = (int32_t)((steps + splits - 1) / splits);
+  a.part_stride = part_floats(p);
+  return a;
+}
+
+int store_of(int type) {
+  return type == GEMM_TYPE_F32 ? kStoreF32 : type == GEMM_TYPE_F16 ? kStoreF16 : kStoreBf16;
+}
+
+// Both products (a shape without rows or columns: none) and their sums.
+hipError_t grad_products(int type, const GradShape& x, const Operands& ox, const GradShape& w,
+                         const Operands& ow, int w_type, void* work, hipStream_t stream) {
+  const GradPlan plan = choose(x, w);
+  const GradTile& t = *plan.tile;
+  float* const px = (float*)work;
+  float* const pw = px + split_bytes(x, plan.split_x) / 4;
+  GradPair pair{};
+  pair.x = product_args(t, x, ox, plan.split_x, px);
+  pair.w = product_args(t, w, ow, plan.split_w, pw);
+  const int64_t nx = tiles_of(t, x) * plan.split_x, nw = tiles_of(t, w) * plan.split_w;
+  if (nx + nw == 0) return hipSuccess;
+  // the longer workgroups first
+  pair.w_first = nx == 0 || (nw > 0 && pair.w.split_steps > pair.x.split_steps);
+  const int64_t n1 = pair.w_first ? nw : nx, n2 = pair.w_first ? nx : nw;
+  pair.first = (int)((n1 + 7) / 8 * 8);
+  pair.grid = (int)(n2 > 0 ? pair.first + n2 : n1);
+  const int sx = store_of(type), sw = store_of(w_type);
+  hipError_t e = t.launch(pair, stream, type == GEMM_TYPE_F16 ? kOpF16 : kOpBf16,
+                          plan.split_x > 1 ? kStoreF32 : sx, plan.split_w > 1 ? kStoreF32 : sw);
+  if (e != hipSuccess) return e;
+  auto sum = [](const GradShape& p, const Operands& o, const float* parts, int splits, int out) {
+    return SumParts{parts, p.M * p.halves, up4(p.N), part_floats(p), splits, o.C, o.ldc, p.N, out};
+  };
+  return launch_sum_parts(sum(x, ox, px, nx > 0 ? plan.split_x : 1, sx),
+                          sum(w, ow, pw, nw > 0 ? plan.split_w : 1, sw), stream);
 }
 
 // dA (M x K) = dC (M x N) . B (N x K), and dB (N x K) = dC^T . A (M x K).
@@ -148,15 +190,21 @@ bool size_refused(int64_t M, int64_t N, int64_t K) {
   return M >= k2G / 2 || N >= k2G / 4 || K >= k2G / 2;
 }
 
-thread_local char g_plan_name[32];
+int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
 
-const char* plan_name(const GradShape& p) {
-  const GradPlan plan = choose(p);
-  snprintf(g_plan_name, sizeof g_plan_name, "%s_k%d", plan.tile->name, plan.splits);
+thread_local char g_plan_name[48];
+
+const char* plan_name(const GradShape& x, const GradShape& w) {
+  const GradPlan plan = choose(x, w);
+  snprintf(g_plan_name, sizeof g_plan_name, "%s_k%d_k%d", plan.tile->name, plan.split_x,
+           plan.split_w);
   return g_plan_name;
 }
 
-int64_t larger(int64_t a, int64_t b) { return a > b ? a : b; }
+// Parts of both gradients, or of either one alone.
+int64_t most_bytes(const GradShape& x, const GradShape& w) {
+  return larger(plan_bytes(x, w), larger(plan_bytes(x, kNoProduct), plan_bytes(kNoProduct, w)));
+}
 
 int64_t gate_bytes(int64_t M, int64_t F) { return up256(M * 2 * up8(F) * 2); }
 
@@ -167,19 +215,17 @@ extern "C" {
 
 size_t gemm_backward_work_size(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0 || gemm::size_refused(M, N, K)) return 0;
-  return (size_t)gemm::larger(gemm::split_bytes(gemm::input_shape(M, N, K)),
-                              gemm::split_bytes(gemm::weight_shape(M, N, K)));
+  return (size_t)gemm::most_bytes(gemm::input_shape(M, N, K), gemm::weight_shape(M, N, K));
 }
 
-const char* gemm_backward_config_name(int64_t M, int64_t N, int64_t K, int of_b) {
+const char* gemm_backward_config_name(int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0 || gemm::size_refused(M, N, K)) return "invalid";
-  return gemm::plan_name(of_b ? gemm::weight_shape(M, N, K) : gemm::input_shape(M, N, K));
+  return gemm::plan_name(gemm::input_shape(M, N, K), gemm::weight_shape(M, N, K));
 }
 
-const char* gemm_gated_backward_config_name(int64_t M, int64_t F, int64_t K, int of_w) {
+const char* gemm_gated_backward_config_name(int64_t M, int64_t F, int64_t K) {
   if (M < 0 || F < 0 || K < 0 || gemm::size_refused(M, F, K)) return "invalid";
-  return gemm::plan_name(of_w ? gemm::gated_weight_shape(M, F, K)
-                              : gemm::gated_input_shape(M, F, K));
+  return gemm::plan_name(gemm::gated_input_shape(M, F, K), gemm::gated_weight_shape(M, F, K));
 }
 
 int gemm_backward(int type, int64_t M, int64_t N, int64_t K, const void* dC, int64_t lddc,
@@ -203,27 +249,24 @@ int gemm_backward(int type, int64_t M, int64_t N, int64_t K, const void* dC, int
       misaligned(dB, 16) || misaligned(work, 16) || (lddc & 7) || (dA && ((ldb | ldda) & 7)) ||
       (dB && ((lda | lddb) & 7)))
     return GEMM_ERR_MISALIGNED;
-  const GradShape pa = input_shape(M, N, K), pb = weight_shape(M, N, K);
+  const GradShape pa = has_a ? input_shape(M, N, K) : kNoProduct;
+  const GradShape pb = has_b ? weight_shape(M, N, K) : kNoProduct;
   if ((has_a && !runs(pa, true, lddc, ldb)) || (has_b && !runs(pb, false, lddc, lda)))
     return GEMM_ERR_UNSUPPORTED;
-  const int64_t need = larger(has_a ? split_bytes(pa) : 0, has_b ? split_bytes(pb) : 0);
+  const int64_t need = plan_bytes(pa, pb);
   if (need > 0 && (!work || (int64_t)work_bytes < need)) return GEMM_ERR_SCRATCH;
-  hipError_t e = hipSuccess;
-  if (has_a)
-    e = grad_product(kNN, type, pa, Operands{dC, B, lddc, ldb, 0, 0, 0}, dA, ldda, type, work,
-                     (hipStream_t)stream);
-  if (e == hipSuccess && has_b)
-    e = grad_product(kTN, type, pb, Operands{dC, A, lddc, lda, 0, 0, 0}, dB, lddb, db_type, work,
-                     (hipStream_t)stream);
+  const hipError_t e =
+      grad_products(type, pa, Operands{dC, B, lddc, ldb, 0, 0, 0, dA, ldda}, pb,
+                    Operands{dC, A, lddc, lda, 0, 0, 0, dB, lddb}, dB ? db_type : type, work,
+                    (hipStream_t)stream);
   return e == hipSuccess ? GEMM_OK : hip_fail(e);
 }
 
 size_t gemm_gated_backward_work_size(int64_t M, int64_t F, int64_t K) {
   if (M < 0 || F < 0 || K < 0 || gemm::size_refused(M, F, K)) return 0;
   if (M > 0 && gemm::up8(F) > gemm::kStrideLimit / M) return 0;
-  return (size_t)(gemm::gate_bytes(M, F) +
-                  gemm::larger(gemm::split_bytes(gemm::gated_input_shape(M, F, K)),
-                               gemm::split_bytes(gemm::gated_weight_shape(M, F, K))));
+  return (size_t)(gemm::gate_bytes(M, F) + gemm::most_bytes(gemm::gated_input_shape(M, F, K),
+                                                           gemm::gated_weight_shape(M, F, K)));
 }
 
 int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* dH, int64_t lddh,
@@ -250,26 +293,22 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* d
       misaligned(dX, 16) || misaligned(dW, 16) || misaligned(work, 16) || ((lddh | ldgu) & 7) ||
       (dX && ((ldw | lddx) & 7)) || (dW && ((ldx | lddw) & 7)))
     return GEMM_ERR_MISALIGNED;
-  const GradShape px = gated_input_shape(M, F, K), pw = gated_weight_shape(M, F, K);
+  const GradShape px = has_x ? gated_input_shape(M, F, K) : kNoProduct;
+  const GradShape pw = has_w ? gated_weight_shape(M, F, K) : kNoProduct;
   if ((has_x && !runs(px, true, 2 * Fp, ldw)) || (has_w && !runs(pw, false, 2 * Fp, ldx)))
     return GEMM_ERR_UNSUPPORTED;
   if (!has_x && !has_w) return GEMM_OK;
-  const int64_t gate = gate_bytes(M, F);
-  const int64_t need =
-      gate + larger(has_x ? split_bytes(px) : 0, has_w ? split_bytes(pw) : 0);
+  const int64_t gate = gate_bytes(M, F), need = gate + plan_bytes(px, pw);
   if (need > 0 && (!work || (int64_t)work_bytes < need)) return GEMM_ERR_SCRATCH;
   hipError_t e = hipSuccess;
   if (M > 0 && F > 0) {
     const GateGradArgs g{dH, GU, work, M, Fp, lddh, ldgu, 2 * Fp, act == GEMM_ACT_GEGLU};
     e = launch_gate_grad(g, type == GEMM_TYPE_F16, (hipStream_t)stream);
   }
-  void* const parts = (uint8_t*)work + gate;
-  if (e == hipSuccess && has_x)
-    e = grad_product(kNN, type, px, Operands{work, W, 2 * Fp, ldw, Fp, F * ldw, 0}, dX, lddx, type,
-                     parts, (hipStream_t)stream);
-  if (e == hipSuccess && has_w)
-    e = grad_product(kTN, type, pw, Operands{work, X, 2 * Fp, ldx, 0, 0, Fp}, dW, lddw, dw_type,
-                     parts, (hipStream_t)stream);
+  if (e == hipSuccess)
+    e = grad_products(type, px, Operands{work, W, 2 * Fp, ldw, Fp, F * ldw, 0, dX, lddx}, pw,
+                      Operands{work, X, 2 * Fp, ldx, 0, 0, Fp, dW, lddw}, dW ? dw_type : type,
+                      (uint8_t*)work + gate, (hipStream_t)stream);
   return e == hipSuccess ? GEMM_OK : hip_fail(e);
 }
 

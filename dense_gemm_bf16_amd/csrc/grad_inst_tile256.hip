@@ -2,5 +2,5 @@
 #include "grad_launch.hpp"
 
 namespace gemm {
-template hipError_t launch_grad_tile<256, 256, 2, 4, 2>(const BlockArgs&, int, hipStream_t, int, int, int);
+template hipError_t launch_grad_pair<256, 256, 2, 4, 2>(const GradPair&, hipStream_t, int, int, int);
 }  // namespace gemm

@@ -6,29 +6,32 @@
 
 namespace gemm {
 
-// op kOpBf16 or kOpF16; out kStoreF32 or that type; layout kNN or kTN.
+// Both products in one launch.  op kOpBf16 or kOpF16; out_x and out_w
+// kStoreF32 or that type.
+struct GradPair {
+  BlockArgs x, w;
+  int first;     // workgroups of the first product, rounded up to a multiple of 8
+  bool w_first;  // which is w's
+  int grid;
+};
+
 template <int BM, int BN, int WM, int WN, int S>
-hipError_t launch_grad_tile(const BlockArgs& a, int grid, hipStream_t s, int op, int out,
-                            int layout) {
-  auto launch = [&](auto o, auto t, auto l) {
-    hipLaunchKernelGGL((block_tile_kernel<BM, BN, WM, WN, 1, S, decltype(o)::value,
-                                          decltype(t)::value, kPlain, false, decltype(l)::value>),
-                       dim3(grid), dim3(WM * WN * 64), 0, s, a);
+hipError_t launch_grad_pair(const GradPair& p, hipStream_t s, int op, int out_x, int out_w) {
+  auto launch = [&](auto o, auto tx, auto tw) {
+    hipLaunchKernelGGL((grad_pair_kernel<BM, BN, WM, WN, S, decltype(o)::value,
+                                         decltype(tx)::value, decltype(tw)::value>),
+                       dim3(p.grid), dim3(WM * WN * 64), 0, s, p.x, p.w, p.first,
+                       p.w_first ? 1 : 0);
     return hipGetLastError();
   };
-  auto by_layout = [&](auto o, auto t) {
-    return layout == kNN ? launch(o, t, std::integral_constant<int, kNN>{})
-                         : launch(o, t, std::integral_constant<int, kTN>{});
-  };
   const std::integral_constant<int, kStoreF32> f32{};
-  if (op == kOpBf16) {
-    const std::integral_constant<int, kOpBf16> o{};
-    return out == kStoreF32 ? by_layout(o, f32)
-                            : by_layout(o, std::integral_constant<int, kStoreBf16>{});
-  }
-  const std::integral_constant<int, kOpF16> o{};
-  return out == kStoreF32 ? by_layout(o, f32)
-                          : by_layout(o, std::integral_constant<int, kStoreF16>{});
+  auto by_out = [&](auto o, auto own) {
+    if (out_x == kStoreF32) return out_w == kStoreF32 ? launch(o, f32, f32) : launch(o, f32, own);
+    return out_w == kStoreF32 ? launch(o, own, f32) : launch(o, own, own);
+  };
+  if (op == kOpBf16)
+    return by_out(std::integral_constant<int, kOpBf16>{}, std::integral_constant<int, kStoreBf16>{});
+  return by_out(std::integral_constant<int, kOpF16>{}, std::integral_constant<int, kStoreF16>{});
 }
 
 // Built shapes: X(name, launcher template arguments).
@@ -36,9 +39,9 @@ hipError_t launch_grad_tile(const BlockArgs& a, int grid, hipStream_t s, int op,
   X(b256x256, 256, 256, 2, 4, 2)  \
   X(b128x128, 128, 128, 2, 2, 2)
 
-#define GRAD_DECLARE(NAME, A, B, C, D, S)                                                 \
-  extern template hipError_t launch_grad_tile<A, B, C, D, S>(const BlockArgs&, int, \
-                                                             hipStream_t, int, int, int);
+#define GRAD_DECLARE(NAME, A, B, C, D, S)                                                  \
+  extern template hipError_t launch_grad_pair<A, B, C, D, S>(const GradPair&, hipStream_t, int, \
+                                                             int, int);
 GRAD_TILES(GRAD_DECLARE)
 #undef GRAD_DECLARE
 

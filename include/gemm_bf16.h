@@ -468,7 +468,7 @@ const char* gemm_i8_config_at(int i);
  * A row that holds a NaN gets a NaN scale (its codes are unspecified), one that
  * holds an infinity an infinite scale, codes of +-127 for its infinities and 0
  * for the rest.  The same call serves activations (a scale for each token) and
- * weights (one for each channel).  M is below 2^24, K below 2^31. */
+ * weights (one for each channel).  M is below 2^22, K below 2^31. */
 int gemm_i8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_type,
                      void* Q, int64_t ldq, float* S, void* stream);
 
@@ -540,9 +540,10 @@ int gemm_backward(int type, int64_t M, int64_t N, int64_t K,
                   void* dB, int64_t lddb, int db_type,
                   void* work, size_t work_bytes, void* stream);
 size_t gemm_backward_work_size(int64_t M, int64_t N, int64_t K);
-/* The tile and the ways K is split ("b256x256_k1") of dA's product, or with
- * of_b != 0 of dB's.  Per-thread static storage. */
-const char* gemm_backward_config_name(int64_t M, int64_t N, int64_t K, int of_b);
+/* The tile of both gradients' products, which share a launch, and the ways that
+ * K of dA's and of dB's is split ("b128x128_k4_k1").  Per-thread static
+ * storage. */
+const char* gemm_backward_config_name(int64_t M, int64_t N, int64_t K);
 
 /* Of the gated product H = act(G) * U (gemm_gated), from the gradient of H and
  * the GU that it kept:
@@ -562,7 +563,7 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K,
                         void* dW, int64_t lddw, int dw_type,
                         void* work, size_t work_bytes, void* stream);
 size_t gemm_gated_backward_work_size(int64_t M, int64_t F, int64_t K);
-const char* gemm_gated_backward_config_name(int64_t M, int64_t F, int64_t K, int of_w);
+const char* gemm_gated_backward_config_name(int64_t M, int64_t F, int64_t K);
 
 /* Human-readable text for a status code.  Static storage; never NULL. */
 const char* gemm_bf16_status_string(int status);

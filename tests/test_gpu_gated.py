@@ -171,7 +171,7 @@ def test_rows_past_32_bits():
 # ------------------------------------------------------------------ gradients
 
 SIZES = [(1, 300, 70), (300, 200, 130), (3000, 136, 72), (72, 3000, 136), (4090, 130, 4100),
-         (130, 4090, 4100), (2100, 2056, 700)]
+         (130, 4090, 4100), (2100, 2056, 700), (1500, 1500, 200)]
 
 
 def backward(dc, a, b, db_dtype=None):
@@ -205,17 +205,16 @@ def test_product_gradients_are_exact_on_integers(M, N, K, t, out):
 
 
 def test_plans_that_the_gradients_run_as():
-    """Both tiles, split and not, of both products, are reached by the sizes of
-    these tests."""
+    """Both tiles, and splits of either product, of both and of none, are
+    reached by the sizes of these tests."""
     import dense_gemm_bf16_amd as g
 
     seen = set()
     for M, N, K in SIZES:
-        for of_b in (False, True):
-            tile, splits = g.backward_config_name(M, N, K, of_b).split("_k")
-            seen.add((tile, int(splits) > 1, of_b))
-    assert {("b128x128", s, b) for s in (False, True) for b in (False, True)} <= seen, seen
-    assert ("b256x256", False, False) in seen and ("b256x256", False, True) in seen, seen
+        tile, x, w = g.backward_config_name(M, N, K).split("_k")
+        seen.add((tile, int(x) > 1, int(w) > 1))
+    assert {s[0] for s in seen} == {"b128x128", "b256x256"}, seen
+    assert {s[1:] for s in seen} == {(a, b) for a in (False, True) for b in (False, True)}, seen
 
 
 @pytest.mark.parametrize("M, N, K", [(40, 5000, 100), (333, 777, 555), (1500, 100, 60), (2100, 2056, 700)])
@@ -379,7 +378,7 @@ def test_a_captured_training_step():
             outs = step()
         return fill, step, graph, outs
 
-    assert g.gated_backward_config_name(2048, 64, 64, True).split("_k")[1] != "1"
+    assert g.gated_backward_config_name(2048, 64, 64) != "b128x128_k1_k1"
     a, b = step_of(2048, 64, 64), step_of(600, 88, 200)
     one, two = torch.cuda.Stream(), torch.cuda.Stream()
     for _ in range(4):
