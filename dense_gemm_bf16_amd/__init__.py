@@ -6,7 +6,10 @@
 and of its operators for 8-bit and mixture-of-experts layers: products over
 e4m3 operands with scales per block of 128 (gemm_fp8), quantising to them
 (gemm_fp8_quantize), routing (gemm_moe_route, gemm_moe_plan), the experts'
-products (gemm_moe) and the weighted sum back to tokens (gemm_moe_combine).
+products (gemm_moe) and the weighted sum back to tokens (gemm_moe_combine);
+and of dense gated layers: products over 8-bit integers (gemm_i8,
+gemm_i8_quantize), gated products (gemm_gated, gemm_i8_gated) and the gradients
+of dense and gated products (gemm_backward, gemm_gated_backward).
 
 The functions here only marshal arguments (sizes, device pointers, a HIP
 stream) to the C entry points of the same names declared in
@@ -123,6 +126,8 @@ _lib.gemm_moe_config_name.argtypes = [_c_int, _i64, _i64, _i64, _i64, _c_int]
 for _name in ("gemm_backward_work_size", "gemm_gated_backward_work_size"):
     getattr(_lib, _name).restype = ctypes.c_size_t
     getattr(_lib, _name).argtypes = [_i64, _i64, _i64]
+_lib.gemm_gated_kept_row.restype = ctypes.c_size_t
+_lib.gemm_gated_kept_row.argtypes = [_i64]
 for _name in ("gemm_backward_config_name", "gemm_gated_backward_config_name"):
     getattr(_lib, _name).restype = ctypes.c_char_p
     getattr(_lib, _name).argtypes = [_i64, _i64, _i64]
@@ -447,17 +452,19 @@ def gemm_i8_gated_ex(config, M, F, K, A, lda, SA, W, ldw, SW, act, H, ldh, h_typ
                                  _ptr(H), ldh, h_type, _stream(stream)))
 
 
-def gemm_gated(type, M, F, K, X, ldx, W, ldw, act, H, ldh, GU=None, ldgu=0, stream=None) -> None:
-    """H = act(X . Wg^T) * (X . Wu^T), bf16 or fp16; G and U to GU as well."""
-    gemm_gated_ex(None, type, M, F, K, X, ldx, W, ldw, act, H, ldh, GU, ldgu, stream)
+def gemm_gated(type, M, F, K, X, ldx, W, ldw, act, H, ldh, kept=None, ld_kept=0,
+               stream=None) -> None:
+    """H = act(X . Wg^T) * (X . Wu^T), bf16 or fp16; what the backward pass
+    needs to `kept`."""
+    gemm_gated_ex(None, type, M, F, K, X, ldx, W, ldw, act, H, ldh, kept, ld_kept, stream)
 
 
-def gemm_gated_ex(config, type, M, F, K, X, ldx, W, ldw, act, H, ldh, GU=None, ldgu=0,
+def gemm_gated_ex(config, type, M, F, K, X, ldx, W, ldw, act, H, ldh, kept=None, ld_kept=0,
                   stream=None) -> None:
     """As gemm_gated with the kernel shape named (None = automatic)."""
     cfg = None if config is None else config.encode()
     _check(_lib.gemm_gated_ex(cfg, type, M, F, K, _ptr(X), ldx, _ptr(W), ldw, act, _ptr(H), ldh,
-                              _ptr(GU), ldgu, _stream(stream)))
+                              _ptr(kept), ld_kept, _stream(stream)))
 
 
 def gemm_backward(type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, db_type, work=None,
@@ -468,11 +475,11 @@ def gemm_backward(type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, d
                               _stream(stream)))
 
 
-def gemm_gated_backward(type, M, F, K, dH, lddh, X, ldx, W, ldw, act, GU, ldgu, dX, lddx, dW, lddw,
-                        dw_type, work=None, work_bytes=0, stream=None) -> None:
-    """Gradients of gemm_gated's X and W from H's and the GU that it kept."""
+def gemm_gated_backward(type, M, F, K, dH, lddh, X, ldx, W, ldw, act, kept, ld_kept, dX, lddx, dW,
+                        lddw, dw_type, work=None, work_bytes=0, stream=None) -> None:
+    """Gradients of gemm_gated's X and W from H's and what it kept."""
     _check(_lib.gemm_gated_backward(type, M, F, K, _ptr(dH), lddh, _ptr(X), ldx, _ptr(W), ldw, act,
-                                    _ptr(GU), ldgu, _ptr(dX), lddx, _ptr(dW), lddw, dw_type,
+                                    _ptr(kept), ld_kept, _ptr(dX), lddx, _ptr(dW), lddw, dw_type,
                                     _ptr(work), work_bytes, _stream(stream)))
 
 
@@ -500,6 +507,14 @@ gemm_backward_config_name = backward_config_name
 gemm_gated_backward_config_name = gated_backward_config_name
 gemm_backward_work_size = backward_work_size
 gemm_gated_backward_work_size = gated_backward_work_size
+
+
+def gated_kept_row(F) -> int:
+    """Bytes that gemm_gated keeps of a row of F columns."""
+    return int(_lib.gemm_gated_kept_row(F))
+
+
+gemm_gated_kept_row = gated_kept_row
 
 
 def i8_config_name(M, N, K) -> str:
@@ -864,8 +879,8 @@ def gated_matmul_int8(A, SA, W, SW, act="swiglu", out=None, out_dtype=None, conf
 def gated_matmul(x, W, act="swiglu", out=None, save=False, config=None):
     """h (M x F) = act(g) * u with g = x . Wg^T and u = x . Wu^T: x (M x K) and W
     (2F x K: Wg's rows, then Wu's) both bfloat16 or both float16.  act: "swiglu"
-    (silu) or "geglu" (gelu, tanh form).  save: also return gu (M x 2 x F), g and
-    u rounded to x's type, for gated_matmul_backward."""
+    (silu) or "geglu" (gelu, tanh form).  save: return (h, kept), kept (uint8) what
+    gated_matmul_backward needs: g and u to 24 bits, 6 bytes for each column."""
     _need(x, "x")
     dev, code = x.device, _type(x.dtype, "x", (GEMM_TYPE_BF16, GEMM_TYPE_F16))
     _need(W, "W", dev, x.dtype)
@@ -873,17 +888,18 @@ def gated_matmul(x, W, act="swiglu", out=None, save=False, config=None):
         raise ValueError("need x (M x K) and W (2F x K)")
     (M, K), F = x.shape, W.shape[0] // 2
     out = _out(out, (M, F), x.dtype, dev)
-    gu, ldgu = None, 0
+    kept, row = None, 0
     if save:
-        Fp = -(-F // 8) * 8
-        ldgu = max(16, 2 * Fp)
-        gu = torch.empty(M, ldgu, device=dev, dtype=x.dtype)
+        row = _kept_row(F)
+        kept = torch.empty(M, row, device=dev, dtype=torch.uint8)
     _call(_lib.gemm_gated_ex, dev, None if config is None else config.encode(), code, M, F, K,
           x.data_ptr(), _ld(x, 8), W.data_ptr(), _ld(W, 8), _act(act), out.data_ptr(), _ld(out, 8),
-          None if gu is None else gu.data_ptr(), ldgu)
-    if not save:
-        return out
-    return out, gu.as_strided((M, 2, F), (ldgu, ldgu // 2, 1))
+          None if kept is None else kept.data_ptr(), row)
+    return (out, kept) if save else out
+
+
+def _kept_row(F):
+    return 6 * (-(-F // 16) * 16)
 
 
 def _work(nbytes, device):
@@ -940,9 +956,9 @@ def matmul_backward(dC, A, B, dA=None, dB=None, db_dtype=None):
     return dA, dB
 
 
-def gated_matmul_backward(dh, x, W, gu, act="swiglu", dx=None, dw=None, dw_dtype=None):
-    """Gradients of gated_matmul's x and W from dh (M x F) and the gu that it
-    returned with save=True: (dx, dW).  act as in the forward call; dx, dw and
+def gated_matmul_backward(dh, x, W, kept, act="swiglu", dx=None, dw=None, dw_dtype=None):
+    """Gradients of gated_matmul's x and W from dh (M x F) and what it kept
+    (save=True): (dx, dW).  act as in the forward call; dx, dw and
     dw_dtype as matmul_backward's dA, dB and db_dtype."""
     _need(x, "x")
     dev, dtype = x.device, x.dtype
@@ -952,10 +968,7 @@ def gated_matmul_backward(dh, x, W, gu, act="swiglu", dx=None, dw=None, dw_dtype
     (M, K), F = x.shape, W.shape[0] // 2
     _need(W, "W", dev, dtype)
     _need(dh, "dh", dev, dtype, (M, F))
-    _need(gu, "gu", dev, dtype, (M, 2, F))
-    Fp = -(-F // 8) * 8
-    if M > 0 and F > 0 and gu.stride(1) != Fp:
-        raise ValueError("gu must be as gated_matmul returned it")
+    _need(kept, "kept", dev, torch.uint8, (M, _kept_row(F)))
     dw_dtype = _weight_dtype(dw, dw_dtype, dtype)
     dx = _grad(dx, (M, K), dtype, dev, "dx")
     if dx is not None and dx.dtype != dtype:
@@ -964,8 +977,46 @@ def gated_matmul_backward(dh, x, W, gu, act="swiglu", dx=None, dw=None, dw_dtype
     nbytes = _lib.gemm_gated_backward_work_size(M, F, K)
     work = _work(nbytes, dev)
     _call(_lib.gemm_gated_backward, dev, code, M, F, K, dh.data_ptr(), _ld(dh, 8), x.data_ptr(),
-          _ld(x, 8), W.data_ptr(), _ld(W, 8), _act(act), gu.data_ptr(),
-          gu.stride(0) if M > 1 and F > 0 else max(16, 2 * Fp), _ptr(dx),
-          0 if dx is None else _ld(dx, 8), _ptr(dw), 0 if dw is None else _ld(dw, 8),
-          _TYPES[dw_dtype], _ptr(work), nbytes)
+          _ld(x, 8), W.data_ptr(), _ld(W, 8), _act(act), kept.data_ptr(),
+          _ld(kept, 16), _ptr(dx), 0 if dx is None else _ld(dx, 8), _ptr(dw),
+          0 if dw is None else _ld(dw, 8), _TYPES[dw_dtype], _ptr(work), nbytes)
     return dx, dw
+
+
+def gated_mlp(x, W1, W2, act="swiglu", save=False):
+    """A gated feed-forward layer: y (M x N) = (act(g) * u) . W2^T, (g, u) the
+    two halves of x . W1^T.  x (M x K), W1 (2F x K) and W2 (N x F) are all
+    bfloat16 or all float16.  save: return (y, h, kept), h (M x F) and what
+    gated_matmul kept, for gated_mlp_backward.  The second product is matmul's, with its workspace: a
+    captured call whose plan splits K needs it reserved on the capturing
+    stream."""
+    if W2.dim() != 2 or W1.dim() != 2 or 2 * W2.shape[1] != W1.shape[0]:
+        raise ValueError("need W1 (2F x K) and W2 (N x F)")
+    _need(x, "x")
+    _need(W2, "W2", x.device, x.dtype)
+    r = gated_matmul(x, W1, act=act, save=save)
+    h = r[0] if save else r
+    y = _out(None, (x.shape[0], W2.shape[0]), x.dtype, x.device)
+    with torch.cuda.device(x.device):
+        matmul(h, W2, out=y)
+    return (y, *r) if save else y
+
+
+def gated_mlp_backward(dy, x, W1, W2, h, kept, act="swiglu", dw_dtype=None):
+    """Gradients of gated_mlp from dy (M x N) and the h and kept that it returned
+    with save=True: (dx, dW1, dW2), those of the weights of dw_dtype (x's type,
+    the default, or float32)."""
+    dh, dW2 = matmul_backward(dy, h, W2, db_dtype=dw_dtype)
+    dx, dW1 = gated_matmul_backward(dh, x, W1, kept, act=act, dw_dtype=dw_dtype)
+    return dx, dW1, dW2
+
+
+def gated_mlp_int8(x, W1, S1, W2, S2, act="swiglu"):
+    """gated_mlp over 8-bit integers: x (M x K, bfloat16 or float16), W1 (2F x K)
+    and W2 (N x F) int8 with scales S1 (2F) and S2 (N), as quantize_int8 makes
+    them of weights.  Activations are quantised per row before each product; h
+    is rounded to x's type.  Returns M x N of x's type."""
+    q, s = quantize_int8(x)
+    h = gated_matmul_int8(q, s, W1, S1, act=act, out_dtype=x.dtype)
+    q, s = quantize_int8(h)
+    return matmul_int8(q, s, W2, S2, out_dtype=x.dtype)

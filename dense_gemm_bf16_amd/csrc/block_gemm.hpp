@@ -77,9 +77,10 @@ struct BlockArgs {
   // gated: N counts the columns of H (in C), and
   int64_t up_b;       // bytes from B's row f (gate) to its row F + f (up)
   int64_t up_sb;      // floats from SB's entry f to its entry F + f
-  void* GU;           // where g and u go as well, or null
-  int64_t ldgu;       // elements from row to row of GU
-  int64_t up_gu;      // elements from g to u in a row of GU
+  uint8_t* kept;      // where g and u go as well (see store_kept), or null
+  int64_t ld_kept;    // bytes from row to row of it
+  int64_t kept_f;     // columns of one of its planes
+  int32_t kept_first; // the column there of this launch's first one
   int32_t geglu;      // act: 1: gelu (tanh form), 0: silu
   // kNN and kTN: K in k_steps / seg_steps parts of equal length (kbytes counts
   // one part's), of which the next starts seg_a and seg_b bytes further on;
@@ -391,9 +392,82 @@ __device__ __forceinline__ void store_staged(lds_u8* region, const f32x4 (&v)[FM
   }
 }
 
-// H = act(g) * u (rounded once, from the unrounded sums) and, where GU is
-// asked for, g and u rounded to H's type.  Waves with `mine` hold the sums,
-// g in the even fragments of their columns and u in the odd ones.
+// g and u for the backward pass, 24 bits each: fp32 without its last eight
+// (rounded).  Kept in H's type they would double the error of the gradients
+// beside that of dg's and du's own rounding (bf16: 0.0030 of dW in norm, of
+// which 0.0017 is its own rounding, against 0.0024); kept in fp32 they would
+// take a third more memory and time.  A row of `kept` holds four planes of
+// kept_f columns, F rounded up to 16: the upper halves of g, those of u (2
+// bytes each), the third bytes of g and of u.
+__device__ __forceinline__ uint32_t kept_bits(float x) {
+  return __builtin_bit_cast(uint32_t, x) + 0x80u;  // (an infinity or quiet NaN stays one)
+}
+__device__ __forceinline__ u32x2 kept_high(const f32x4& v) {
+  return (u32x2){(kept_bits(v[0]) >> 16) | (kept_bits(v[1]) & 0xFFFF0000u),
+                 (kept_bits(v[2]) >> 16) | (kept_bits(v[3]) & 0xFFFF0000u)};
+}
+__device__ __forceinline__ uint32_t kept_third(const f32x4& v) {
+  return (kept_bits(v[0]) >> 8 & 0xFFu) | (kept_bits(v[1]) & 0xFF00u) |
+         (kept_bits(v[2]) << 8 & 0xFF0000u) | (kept_bits(v[3]) << 16 & 0xFF000000u);
+}
+__device__ __forceinline__ float kept_value(uint32_t high, uint32_t third) {
+  return __builtin_bit_cast(float, high << 16 | third << 8);
+}
+
+// A workgroup's g (up 0) or u (up 1) into `kept`, staged as store_staged
+// stages H.  The planes' rows are padded, so pieces are stored whole.
+template <int BM, int COLS, int THREADS, int FM, int FN>
+__device__ __forceinline__ void store_kept(lds_u8* region, const BlockArgs& a,
+                                           const f32x4 (&acc)[FM][2 * FN], int up, bool mine,
+                                           int wm, int wn, int lane, int m0, int m_end, int f0) {
+  // 16-byte piece c of row r, rows of 2^LOG pieces
+  auto at = [](int r, int c, auto log) {
+    constexpr int kLog = decltype(log)::value;
+    const int sw = (r >> (kLog >= 4 ? 0 : 4 - kLog)) & ((1 << (kLog > 4 ? 4 : kLog)) - 1);
+    return (uint32_t)((r << (kLog + 4)) + ((c ^ sw) << 4));
+  };
+  constexpr int kLogHigh = COLS == 128 ? 4 : COLS == 64 ? 3 : 2;
+  static_assert(COLS == 8 << kLogHigh, "32, 64 or 128 columns");
+  const std::integral_constant<int, kLogHigh> high{};
+  const std::integral_constant<int, kLogHigh - 1> third{};
+  lds_u8* const region3 = region + BM * COLS * 2;
+  if (mine) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i) {
+      const int r = (wm * FM + i) * 16 + (lane & 15);
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        const int q = (wn * FN + j) * 4 + (lane >> 4);  // column / 4
+        const f32x4& v = acc[i][2 * j + up];
+        *(__attribute__((address_space(3))) u32x2*)(region + at(r, q >> 1, high) + ((q & 1) << 3)) =
+            kept_high(v);
+        *(__attribute__((address_space(3))) uint32_t*)(region3 + at(r, q >> 2, third) +
+                                                       ((q & 3) << 2)) = kept_third(v);
+      }
+    }
+  }
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+  auto rows = [&](auto log, const lds_u8* from, int per, int64_t plane, int bytes) {
+    constexpr int kPieces = 1 << decltype(log)::value, kRows = THREADS / kPieces;
+    const int c = (int)threadIdx.x % kPieces, col = f0 + c * per;
+#pragma unroll
+    for (int r0 = 0; r0 < BM; r0 += kRows) {
+      const int r = r0 + (int)threadIdx.x / kPieces;
+      if (BM % kRows != 0 && r >= BM) break;
+      const u32x4 x = *(const lds_u32x4*)(from + at(r, c, log));
+      if (m0 + r < m_end && col < a.N)
+        __builtin_nontemporal_store(
+            x, (u32x4*)(a.kept + (int64_t)(m0 + r) * a.ld_kept + plane +
+                        (int64_t)(a.kept_first + col) * bytes));
+    }
+  };
+  rows(high, region, 8, up * 2 * a.kept_f, 2);
+  rows(third, region3, 16, (4 + up) * a.kept_f, 1);
+}
+
+// H = act(g) * u (rounded once, from the unrounded sums) and, where asked
+// for, g and u to `kept`.  Waves with `mine` hold the sums, g in the even
+// fragments of their columns and u in the odd ones.
 template <typename Cfg, int OP, int OUT, int THREADS>
 __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
                                              f32x4 (&acc)[Cfg::kFragM][Cfg::kFragN], int m0,
@@ -439,17 +513,11 @@ __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
   store_staged<BM, COLS, THREADS, OUT>(region, h, mine, wm, wn, lane, a.C, a.ldc, m0, m_end, f0,
                                        a.N);
   if constexpr (OP != kOpI8) {
-    if (a.GU != nullptr) {
+    if (a.kept != nullptr) {
 #pragma unroll
-      for (int p = 0; p < 2; ++p) {
-#pragma unroll
-        for (int i = 0; i < FM; ++i)
-#pragma unroll
-          for (int j = 0; j < FN; ++j) h[i][j] = acc[i][2 * j + p];
+      for (int up = 0; up < 2; ++up) {
         asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        store_staged<BM, COLS, THREADS, OUT>(region, h, mine, wm, wn, lane,
-                                             (uint16_t*)a.GU + p * a.up_gu, a.ldgu, m0, m_end, f0,
-                                             a.N);
+        store_kept<BM, COLS, THREADS, FM, FN>(region, a, acc, up, mine, wm, wn, lane, m0, m_end, f0);
       }
     }
   }
@@ -1294,9 +1362,13 @@ block_row_kernel(BlockArgs a) {
       for (int r = 0; r < 4; ++r) h[r] = gate<OUT>(g[r], u[r], a.geglu != 0);
       store_quad<OUT>(a.C, a.ldc, h, m0 + row, n, a.N);
       if constexpr (OP != kOpI8) {
-        if (a.GU != nullptr) {
-          store_quad<OUT>(a.GU, a.ldgu, g, m0 + row, n, a.N);
-          store_quad<OUT>((uint16_t*)a.GU + a.up_gu, a.ldgu, u, m0 + row, n, a.N);
+        if (a.kept != nullptr && n < a.N) {
+          uint8_t* const at = a.kept + (int64_t)(m0 + row) * a.ld_kept;
+          const int64_t f = a.kept_first + n;
+          *(u32x2*)(at + f * 2) = kept_high(g);
+          *(u32x2*)(at + (a.kept_f + f) * 2) = kept_high(u);
+          *(uint32_t*)(at + 4 * a.kept_f + f) = kept_third(g);
+          *(uint32_t*)(at + 5 * a.kept_f + f) = kept_third(u);
         }
       }
     }

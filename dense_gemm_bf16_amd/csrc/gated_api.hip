@@ -162,28 +162,28 @@ int store_of(int type) {
 int op_of(int type) {
   return type == GEMM_TYPE_I8 ? kOpI8 : type == GEMM_TYPE_F16 ? kOpF16 : kOpBf16;
 }
-int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 
 // C (M x N) of A and B's N rows, or with `gated` H (M x N) of B's 2 N rows.
 int dense_product(const char* config, int type, bool gated, int64_t M, int64_t N, int64_t K,
                   const void* A, int64_t lda, const float* SA, const void* B, int64_t ldb,
-                  const float* SB, int act, void* C, int64_t ldc, int c_type, void* GU,
-                  int64_t ldgu, void* stream) {
+                  const float* SB, int act, void* C, int64_t ldc, int c_type, void* kept,
+                  int64_t ld_kept, void* stream) {
   const bool ints = type == GEMM_TYPE_I8;
   if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
   if (!ints && type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return GEMM_ERR_INVALID_ARG;
   if (!is_float_type(c_type) || (!ints && c_type != type)) return GEMM_ERR_INVALID_ARG;
   if (gated && act != GEMM_ACT_SWIGLU && act != GEMM_ACT_GEGLU) return GEMM_ERR_INVALID_ARG;
   if (M >= k2G || N >= (gated ? k2G / 2 : k2G) || K >= k2G / 2 || lda >= k2G || ldb >= k2G ||
-      ldc >= (int64_t(1) << 40) || ldgu >= (int64_t(1) << 40) || (ints && K > kMaxIntK))
+      ldc >= (int64_t(1) << 40) || ld_kept >= (int64_t(1) << 40) || (ints && K > kMaxIntK))
     return GEMM_ERR_UNSUPPORTED;
-  if (lda < K || ldb < K || ldc < N || (GU && ldgu < 2 * up8(N))) return GEMM_ERR_INVALID_ARG;
+  if (lda < K || ldb < K || ldc < N || (kept && ld_kept < 6 * up16(N))) return GEMM_ERR_INVALID_ARG;
   const bool work = M > 0 && N > 0;
   if (work && (!C || (K > 0 && (!A || !B)) || (ints && (!SA || !SB)))) return GEMM_ERR_INVALID_ARG;
   const int es = ints ? 1 : 2;
-  if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 16) || misaligned(GU, 16) ||
+  if (misaligned(A, 16) || misaligned(B, 16) || misaligned(C, 16) || misaligned(kept, 16) ||
       misaligned(SA, 4) || misaligned(SB, 4) || ((lda | ldb) & (16 / es - 1)) != 0 ||
-      (ldc & 7) != 0 || (GU && (ldgu & 7) != 0))
+      (ldc & 7) != 0 || (kept && (ld_kept & 15) != 0))
     return GEMM_ERR_MISALIGNED;
 
   const Product p{M, gated ? 2 * N : N, K * es, lda * es, ldb * es, gated, ints};
@@ -215,9 +215,9 @@ int dense_product(const char* config, int type, bool gated, int64_t M, int64_t N
   if (gated) {
     a.up_b = N * p.ldb;
     a.up_sb = N;
-    a.GU = GU;
-    a.ldgu = ldgu;
-    a.up_gu = up8(N);
+    a.kept = (uint8_t*)kept;
+    a.ld_kept = ld_kept;
+    a.kept_f = up16(N);
     a.geglu = act == GEMM_ACT_GEGLU;
   }
   auto launch = [&](const Shape& s, int64_t rows_b) {
@@ -236,7 +236,7 @@ int dense_product(const char* config, int type, bool gated, int64_t M, int64_t N
     a.B += col * p.ldb;
     if (SB) a.SB += col;
     a.C = (uint8_t*)C + col * (c_type == GEMM_TYPE_F32 ? 4 : 2);
-    if (GU) a.GU = (uint16_t*)GU + col;
+    a.kept_first = (int32_t)col;
     e = launch(*plan.tail, p.rows_b - plan.split_b);
   }
   return e == hipSuccess ? GEMM_OK : hip_fail(e);
@@ -288,17 +288,21 @@ int gemm_i8_gated(int64_t M, int64_t F, int64_t K, const void* A, int64_t lda, c
 }
 
 int gemm_gated_ex(const char* config, int type, int64_t M, int64_t F, int64_t K, const void* X,
-                  int64_t ldx, const void* W, int64_t ldw, int act, void* H, int64_t ldh, void* GU,
-                  int64_t ldgu, void* stream) {
+                  int64_t ldx, const void* W, int64_t ldw, int act, void* H, int64_t ldh, void* kept,
+                  int64_t ld_kept, void* stream) {
   if (type == GEMM_TYPE_I8) return GEMM_ERR_INVALID_ARG;
   return gemm::dense_product(config, type, true, M, F, K, X, ldx, nullptr, W, ldw, nullptr, act, H,
-                             ldh, type, GU, ldgu, stream);
+                             ldh, type, kept, ld_kept, stream);
 }
 
 int gemm_gated(int type, int64_t M, int64_t F, int64_t K, const void* X, int64_t ldx,
-               const void* W, int64_t ldw, int act, void* H, int64_t ldh, void* GU, int64_t ldgu,
+               const void* W, int64_t ldw, int act, void* H, int64_t ldh, void* kept, int64_t ld_kept,
                void* stream) {
-  return gemm_gated_ex(nullptr, type, M, F, K, X, ldx, W, ldw, act, H, ldh, GU, ldgu, stream);
+  return gemm_gated_ex(nullptr, type, M, F, K, X, ldx, W, ldw, act, H, ldh, kept, ld_kept, stream);
+}
+
+size_t gemm_gated_kept_row(int64_t F) {
+  return F < 0 || F >= gemm::k2G / 2 ? 0 : (size_t)(6 * gemm::up16(F));
 }
 
 const char* gemm_i8_config_name(int64_t M, int64_t N, int64_t K) {

@@ -35,10 +35,10 @@ struct GradTile {
   hipError_t (*launch)(const GradPair&, hipStream_t, int op, int out_x, int out_w);
 };
 const GradTile kTiles[] = {
-    {"b256x256", 256, 256, 512, 1, 1.42, 9.0, 0.75, &launch_grad_pair<256, 256, 2, 4, 2>},
-    {"b128x128", 128, 128, 256, 2, 0.93, 6.0, 0.51, &launch_grad_pair<128, 128, 2, 2, 2>},
+    {"b256x256", 256, 256, 512, 1, 0.88, 12.8, 0.91, &launch_grad_pair<256, 256, 2, 4, 2>},
+    {"b128x128", 128, 128, 256, 2, 0.78, 4.8, 0.78, &launch_grad_pair<128, 128, 2, 2, 2>},
 };
-constexpr double kSumUs = 3.5, kSumUsPerMB = 0.32;
+constexpr double kSumUs = 2.1, kSumUsPerMB = 0.87, kTail = 0.03;
 
 struct GradPlan {
   const GradTile* tile;
@@ -76,7 +76,7 @@ GradPlan choose(const GradShape& x, const GradShape& w) {
         const double fill = (nx + nw) / places;
         double us = longest * (t.part + (1 - t.part) * (fill < 1 ? fill : 1));
         const double all = (nx * ux + nw * uw) / places;
-        if (fill > 1) us = all > us ? all + 0.3 * longest : us + 0.3 * longest;
+        if (fill > 1) us = (all > us ? all : us) + kTail * longest;
         if (sx > 1 || sw > 1)
           us += kSumUs + kSumUsPerMB * 1e-6 * (double)(split_bytes(x, sx) + split_bytes(w, sw));
         if (best.tile && us >= best_t) continue;
@@ -271,26 +271,26 @@ size_t gemm_gated_backward_work_size(int64_t M, int64_t F, int64_t K) {
 
 int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* dH, int64_t lddh,
                         const void* X, int64_t ldx, const void* W, int64_t ldw, int act,
-                        const void* GU, int64_t ldgu, void* dX, int64_t lddx, void* dW,
+                        const void* kept, int64_t ld_kept, void* dX, int64_t lddx, void* dW,
                         int64_t lddw, int dw_type, void* work, size_t work_bytes, void* stream) {
   using namespace gemm;
   if (M < 0 || F < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
   if (type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return GEMM_ERR_INVALID_ARG;
   if (act != GEMM_ACT_SWIGLU && act != GEMM_ACT_GEGLU) return GEMM_ERR_INVALID_ARG;
   if (dW && dw_type != type && dw_type != GEMM_TYPE_F32) return GEMM_ERR_INVALID_ARG;
-  const int64_t Fp = up8(F < k2G ? F : k2G);
+  const int64_t Fp = up8(F < k2G ? F : k2G), kept_f = (Fp + 15) / 16 * 16;
   // (a workgroup of 256 for 2048 values of dGU: a grid holds fewer than 2^32 threads)
   if (size_refused(M, F, K) || (M > 0 && Fp / 8 >= 2 * k2G / M) || lddh >= kStrideLimit ||
-      ldx >= kStrideLimit || ldw >= kStrideLimit || ldgu >= kStrideLimit || lddx >= kStrideLimit ||
+      ldx >= kStrideLimit || ldw >= kStrideLimit || ld_kept >= kStrideLimit || lddx >= kStrideLimit ||
       lddw >= kStrideLimit)
     return GEMM_ERR_UNSUPPORTED;
   const bool has_x = dX && M > 0 && K > 0, has_w = dW && F > 0 && K > 0;
-  if (lddh < F || ldgu < 2 * Fp || (dX && (ldw < K || lddx < K)) || (dW && (ldx < K || lddw < K)))
+  if (lddh < F || ld_kept < 6 * kept_f || (dX && (ldw < K || lddx < K)) || (dW && (ldx < K || lddw < K)))
     return GEMM_ERR_INVALID_ARG;
-  if ((has_x || has_w) && M > 0 && F > 0 && (!dH || !GU || (has_x && !W) || (has_w && !X)))
+  if ((has_x || has_w) && M > 0 && F > 0 && (!dH || !kept || (has_x && !W) || (has_w && !X)))
     return GEMM_ERR_INVALID_ARG;
-  if (misaligned(dH, 16) || misaligned(X, 16) || misaligned(W, 16) || misaligned(GU, 16) ||
-      misaligned(dX, 16) || misaligned(dW, 16) || misaligned(work, 16) || ((lddh | ldgu) & 7) ||
+  if (misaligned(dH, 16) || misaligned(X, 16) || misaligned(W, 16) || misaligned(kept, 16) ||
+      misaligned(dX, 16) || misaligned(dW, 16) || misaligned(work, 16) || (lddh & 7) || (ld_kept & 15) ||
       (dX && ((ldw | lddx) & 7)) || (dW && ((ldx | lddw) & 7)))
     return GEMM_ERR_MISALIGNED;
   const GradShape px = has_x ? gated_input_shape(M, F, K) : kNoProduct;
@@ -302,7 +302,8 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* d
   if (need > 0 && (!work || (int64_t)work_bytes < need)) return GEMM_ERR_SCRATCH;
   hipError_t e = hipSuccess;
   if (M > 0 && F > 0) {
-    const GateGradArgs g{dH, GU, work, M, Fp, lddh, ldgu, 2 * Fp, act == GEMM_ACT_GEGLU};
+    const GateGradArgs g{dH,      (const uint8_t*)kept, work,   M, Fp, lddh,
+                         ld_kept, kept_f,               act == GEMM_ACT_GEGLU};
     e = launch_gate_grad(g, type == GEMM_TYPE_F16, (hipStream_t)stream);
   }
   if (e == hipSuccess)

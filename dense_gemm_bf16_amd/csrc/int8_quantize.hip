@@ -2,11 +2,11 @@
 //
 //   amax = max(largest |x| of the row, 2^-100)
 //   S    = amax / 127
-//   q    = x * (127 / amax), rounded to nearest even
+//   q    = x * (127 * (1 / amax)), rounded to nearest even
 //
-// Both divisions and the product are IEEE fp32, so the codes are a function
-// of the inputs alone.  |x| * (127 / amax) is at most 127 (1 + 2^-22), which
-// rounds to 127.  A row that holds a NaN has a NaN scale, so that whatever it
+// Each operation is an IEEE fp32 one, so the codes are a function of the
+// inputs alone.  |x| times the factor is at most 127 (1 + 2^-21), which rounds
+// to 127.  A row that holds a NaN has a NaN scale, so that whatever it
 // enters is NaN; one that holds an infinity (and no NaN) an infinite scale,
 // codes of +-127 for its infinities and 0 for the rest.
 //
@@ -78,7 +78,7 @@ __device__ __forceinline__ float row_factor(uint32_t most, float* scale) {
   float amax = __builtin_bit_cast(float, most);
   if (amax < kAmaxFloor) amax = kAmaxFloor;  // (false for NaN)
   if (scale) *scale = amax / kInt8Max;
-  return kInt8Max / amax;
+  return kInt8Max * (1.0f / amax);
 }
 
 __device__ __forceinline__ void store_codes(uint8_t* q, const float (&v)[8], float inv, int n) {

@@ -464,7 +464,7 @@ const char* gemm_i8_config_at(int i);
  * its type) to 8-bit integers Q (M x K, 16-byte aligned, ldq a multiple of 16;
  * a row's bytes past K are left as they were) and a scale for each row, S (M):
  *   amax = max(largest |x| of the row, 2^-100), S = amax / 127,
- *   Q = x * (127 / amax) rounded to nearest even (all in fp32).
+ *   Q = x * (127 * (1 / amax)) rounded to nearest even, each operation in fp32.
  * A row that holds a NaN gets a NaN scale (its codes are unspecified), one that
  * holds an infinity an infinite scale, codes of +-127 for its infinities and 0
  * for the rest.  The same call serves activations (a scale for each token) and
@@ -486,14 +486,16 @@ int gemm_i8_quantize(int64_t M, int64_t K, const void* X, int64_t ldx, int x_typ
  * the formula does. */
 #define GEMM_ACT_GEGLU 2 /* of the gated products only */
 
-/* type GEMM_TYPE_BF16 or _F16, of X (M x K), W (2 F x K) and H (M x F).  GU:
- * NULL, or where G and U go as well, rounded to `type`, for the backward pass:
- * G(m,f) = GU[m*ldgu + f], U(m,f) = GU[m*ldgu + Fp + f] with Fp = F rounded up
- * to a multiple of 8, ldgu >= 2 Fp (what lies between F and Fp is left as it
- * was).  All 16-byte aligned, strides multiples of 8.  No workspace. */
+/* type GEMM_TYPE_BF16 or _F16, of X (M x K), W (2 F x K) and H (M x F), all
+ * 16-byte aligned, strides multiples of 8.  kept: NULL, or where G and U go as
+ * well for gemm_gated_backward, to 24 bits (fp32 without its last eight): M
+ * rows of gemm_gated_kept_row(F) bytes (six for each column, F rounded up to a
+ * multiple of 16), ld_kept bytes apart, a multiple of 16; 16-byte aligned.  No
+ * workspace. */
 int gemm_gated(int type, int64_t M, int64_t F, int64_t K,
                const void* X, int64_t ldx, const void* W, int64_t ldw, int act,
-               void* H, int64_t ldh, void* GU, int64_t ldgu, void* stream);
+               void* H, int64_t ldh, void* kept, int64_t ld_kept, void* stream);
+size_t gemm_gated_kept_row(int64_t F);
 
 /* The same over 8-bit integers, scaled as gemm_i8 (SW: 2 F); h_type BF16, F16
  * or F32. */
@@ -506,7 +508,7 @@ int gemm_i8_gated(int64_t M, int64_t F, int64_t K,
  * but b32x32k4, which does not hold whole pairs of columns). */
 int gemm_gated_ex(const char* config, int type, int64_t M, int64_t F, int64_t K,
                   const void* X, int64_t ldx, const void* W, int64_t ldw, int act,
-                  void* H, int64_t ldh, void* GU, int64_t ldgu, void* stream);
+                  void* H, int64_t ldh, void* kept, int64_t ld_kept, void* stream);
 int gemm_i8_gated_ex(const char* config, int64_t M, int64_t F, int64_t K,
                      const void* A, int64_t lda, const float* SA,
                      const void* W, int64_t ldw, const float* SW, int act,
@@ -546,20 +548,19 @@ size_t gemm_backward_work_size(int64_t M, int64_t N, int64_t K);
 const char* gemm_backward_config_name(int64_t M, int64_t N, int64_t K);
 
 /* Of the gated product H = act(G) * U (gemm_gated), from the gradient of H and
- * the GU that it kept:
+ * what it kept of G and U:
  *
  *   dU = dH * act(G)                 dG = dH * U * act'(G)
  *   dX (M x K) = dG W_g + dU W_u     dW (2 F x K) = [dG^T X; dU^T X]
  *
- * dG and dU are rounded to `type` before the two products, as G and U were
- * when they were kept; sums are fp32, in an order fixed by the sizes.  dX or
- * dW may be NULL.  Rows of dH are read up to F rounded up to a multiple of 8
+ * dG and dU are rounded to `type` before the two products; sums are fp32, in an
+ * order fixed by the sizes.  dX or dW may be NULL.  Rows of dH are read up to F rounded up to a multiple of 8
  * (within lddh).  The rest, and `work`, as for gemm_backward; F is below 2^29,
  * and M * ceil(F / 8) below 2^32. */
 int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K,
                         const void* dH, int64_t lddh, const void* X, int64_t ldx,
                         const void* W, int64_t ldw, int act,
-                        const void* GU, int64_t ldgu, void* dX, int64_t lddx,
+                        const void* kept, int64_t ld_kept, void* dX, int64_t lddx,
                         void* dW, int64_t lddw, int dw_type,
                         void* work, size_t work_bytes, void* stream);
 size_t gemm_gated_backward_work_size(int64_t M, int64_t F, int64_t K);

@@ -79,5 +79,38 @@ def quantize(x):
     x = x.astype(np.float32)
     amax = np.maximum(np.abs(x).max(1) if x.shape[1] else np.zeros(len(x), np.float32),
                       np.float32(2.0 ** -100))
-    q = np.rint(x * (np.float32(127) / amax)[:, None])
+    q = np.rint(x * (np.float32(127) * (np.float32(1) / amax))[:, None])
     return q.astype(np.int8), amax / np.float32(127)
+
+
+KEPT_HALF_STEP = 2.0 ** -16  # of what a gated product keeps of g and u: fp32 less eight bits
+
+
+def kept_row(F):
+    return 6 * (-(-F // 16) * 16)
+
+
+def unkept(kept, F):
+    """(g, u) of kept rows: planes of upper halves and third bytes."""
+    k = np.ascontiguousarray(kept)
+    M, fp = len(k), kept_row(F) // 6
+    high = k[:, :4 * fp].copy().view(np.uint16).reshape(M, 2, fp)[:, :, :F].astype(np.uint32)
+    third = k[:, 4 * fp:6 * fp].reshape(M, 2, fp)[:, :, :F].astype(np.uint32)
+    v = (high << 16 | third << 8).astype(np.uint32).view(np.float32).astype(np.float64)
+    return v[:, 0], v[:, 1]
+
+
+def keep(g, u):
+    """Kept rows of values that fit (24 bits)."""
+    M, F = g.shape
+    fp = kept_row(F) // 6
+    bits = np.stack([g, u], 1).astype(np.float32).view(np.uint32)
+    assert not (bits & 0xFF).any()
+    out = np.zeros((M, 6 * fp), np.uint8)
+    high = np.zeros((M, 2, fp), np.uint16)
+    high[:, :, :F] = bits >> 16
+    out[:, :4 * fp] = high.reshape(M, -1).view(np.uint8)
+    third = np.zeros((M, 2, fp), np.uint8)
+    third[:, :, :F] = bits >> 8 & 0xFF
+    out[:, 4 * fp:] = third.reshape(M, -1)
+    return out
