@@ -500,13 +500,20 @@ __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
         }
       }
     }
+    // (a loop for each activation: a choice in the loop would compute both)
+    auto gates = [&](bool geglu) __attribute__((always_inline)) {
 #pragma unroll
-    for (int i = 0; i < FM; ++i)
+      for (int i = 0; i < FM; ++i)
 #pragma unroll
-      for (int j = 0; j < FN; ++j)
+        for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-          h[i][j][r] = gate<OUT>(acc[i][2 * j][r], acc[i][2 * j + 1][r], a.geglu != 0);
+          for (int r = 0; r < 4; ++r)
+            h[i][j][r] = gate<OUT>(acc[i][2 * j][r], acc[i][2 * j + 1][r], geglu);
+    };
+    if (a.geglu != 0)
+      gates(true);
+    else
+      gates(false);
   }
   // every wave is done with the ring
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
