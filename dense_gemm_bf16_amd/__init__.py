@@ -96,6 +96,7 @@ _i8_args = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _p, _i64, _c_int, _p]
 _i8_gated_args = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _c_int, _p, _i64, _c_int, _p]
 _gated_args = [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _c_int, _p, _i64, _p, _i64, _p]
 for _name, _args in {
+    "gemm_work": [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, ctypes.c_size_t, _p],
     "gemm_backward": [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64,
                       _c_int, _p, ctypes.c_size_t, _p],
     "gemm_gated_backward": [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _c_int, _p,
@@ -126,6 +127,8 @@ _lib.gemm_moe_config_name.argtypes = [_c_int, _i64, _i64, _i64, _i64, _c_int]
 for _name in ("gemm_backward_work_size", "gemm_gated_backward_work_size"):
     getattr(_lib, _name).restype = ctypes.c_size_t
     getattr(_lib, _name).argtypes = [_i64, _i64, _i64]
+_lib.gemm_work_size.restype = ctypes.c_size_t
+_lib.gemm_work_size.argtypes = [_c_int, _i64, _i64, _i64]
 _lib.gemm_gated_kept_row.restype = ctypes.c_size_t
 _lib.gemm_gated_kept_row.argtypes = [_i64]
 for _name in ("gemm_backward_config_name", "gemm_gated_backward_config_name"):
@@ -465,6 +468,20 @@ def gemm_gated_ex(config, type, M, F, K, X, ldx, W, ldw, act, H, ldh, kept=None,
     cfg = None if config is None else config.encode()
     _check(_lib.gemm_gated_ex(cfg, type, M, F, K, _ptr(X), ldx, _ptr(W), ldw, act, _ptr(H), ldh,
                               _ptr(kept), ld_kept, _stream(stream)))
+
+
+def gemm_work(type, M, N, K, A, lda, B, ldb, C, ldc, work=None, work_bytes=0, stream=None) -> None:
+    """gemm_bf16 or gemm_f16 with its workspace given."""
+    _check(_lib.gemm_work(type, M, N, K, _ptr(A), lda, _ptr(B), ldb, _ptr(C), ldc, _ptr(work),
+                          work_bytes, _stream(stream)))
+
+
+def work_size(type, M, N, K) -> int:
+    """Bytes of workspace gemm_work needs."""
+    return int(_lib.gemm_work_size(type, M, N, K))
+
+
+gemm_work_size = work_size
 
 
 def gemm_backward(type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, db_type, work=None,
@@ -987,18 +1004,20 @@ def gated_mlp(x, W1, W2, act="swiglu", save=False):
     """A gated feed-forward layer: y (M x N) = (act(g) * u) . W2^T, (g, u) the
     two halves of x . W1^T.  x (M x K), W1 (2F x K) and W2 (N x F) are all
     bfloat16 or all float16.  save: return (y, h, kept), h (M x F) and what
-    gated_matmul kept, for gated_mlp_backward.  The second product is matmul's, with its workspace: a
-    captured call whose plan splits K needs it reserved on the capturing
-    stream."""
+    gated_matmul kept, for gated_mlp_backward."""
     if W2.dim() != 2 or W1.dim() != 2 or 2 * W2.shape[1] != W1.shape[0]:
         raise ValueError("need W1 (2F x K) and W2 (N x F)")
     _need(x, "x")
-    _need(W2, "W2", x.device, x.dtype)
+    dev, code = x.device, _type(x.dtype, "x", (GEMM_TYPE_BF16, GEMM_TYPE_F16))
+    _need(W2, "W2", dev, x.dtype)
     r = gated_matmul(x, W1, act=act, save=save)
     h = r[0] if save else r
-    y = _out(None, (x.shape[0], W2.shape[0]), x.dtype, x.device)
-    with torch.cuda.device(x.device):
-        matmul(h, W2, out=y)
+    (M, F), N = h.shape, W2.shape[0]
+    y = _out(None, (M, N), x.dtype, dev)
+    nbytes = _lib.gemm_work_size(code, M, N, F)
+    work = _work(nbytes, dev)
+    _call(_lib.gemm_work, dev, code, M, N, F, h.data_ptr(), _ld(h, 8), W2.data_ptr(), _ld(W2, 8),
+          y.data_ptr(), _ld(y, 8), _ptr(work), nbytes)
     return (y, *r) if save else y
 
 

@@ -751,6 +751,26 @@ int gemm_bf16_ex(const char* config, int64_t M, int64_t N, int64_t K, const void
   return gemm::gemm_entry(config, M, N, K, A, lda, B, ldb, C, ldc, out_f32 != 0, false, stream);
 }
 
+size_t gemm_work_size(int type, int64_t M, int64_t N, int64_t K) {
+  if (M <= 0 || N <= 0 || K <= 0 || (type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16)) return 0;
+  return gemm::workspace_bytes(gemm::choose_plan(M, N, K, type == GEMM_TYPE_F16), M, N);
+}
+
+int gemm_work(int type, int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
+              int64_t ldb, void* C, int64_t ldc, void* work, size_t work_bytes, void* stream) {
+  if (type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return GEMM_ERR_INVALID_ARG;
+  int rc = gemm::check_args(M, N, K, A, lda, B, ldb, C, ldc);
+  if (rc != GEMM_OK) return rc;
+  if (((uintptr_t)work & 15) != 0) return GEMM_ERR_MISALIGNED;
+  gemm::Plan p{};
+  rc = gemm::make_plan(nullptr, M, N, K, type == GEMM_TYPE_F16, &p);
+  if (rc != GEMM_OK) return rc;
+  const size_t need = M > 0 && N > 0 ? gemm::workspace_bytes(p, M, N) : 0;
+  if (need > (work ? work_bytes : 0)) return GEMM_ERR_SCRATCH;
+  return gemm::run(p, M, N, K, A, lda, B, ldb, C, ldc, false, type == GEMM_TYPE_F16,
+                   (hipStream_t)stream, work, work_bytes);
+}
+
 int gemm_f16(int64_t M, int64_t N, int64_t K, const void* A, int64_t lda, const void* B,
              int64_t ldb, void* C, int64_t ldc, void* stream) {
   return gemm::gemm_entry(nullptr, M, N, K, A, lda, B, ldb, C, ldc, false, true, stream);

@@ -427,6 +427,19 @@ int gemm_moe_combine(int64_t T, int64_t k, int64_t N, int64_t R, const void* Y, 
                      int y_type, const int32_t* pos, const float* weights, void* out,
                      int64_t ldo, int out_type, void* stream);
 
+/* ----------------------------------------- products in a caller's workspace
+ * gemm_bf16 or gemm_f16 (type GEMM_TYPE_BF16 or _F16; the same plan, so the
+ * same bits) with the split-K partials in the caller's device memory: `work`,
+ * 16-byte aligned, of at least gemm_work_size bytes (0: may be NULL), used by
+ * this call alone until it has run.  Too small: GEMM_ERR_SCRATCH.  Nothing is
+ * allocated or shared, so calls may be captured, and graphs with a workspace
+ * of their own replayed side by side, which those above, whose workspace goes
+ * by the stream they were captured on, may not. */
+int gemm_work(int type, int64_t M, int64_t N, int64_t K,
+              const void* A, int64_t lda, const void* B, int64_t ldb,
+              void* C, int64_t ldc, void* work, size_t work_bytes, void* stream);
+size_t gemm_work_size(int type, int64_t M, int64_t N, int64_t K);
+
 /* ------------------------------------------------------- 8-bit integers
  * Products over signed 8-bit integers with one fp32 scale for each row of A
  * (token) and each row of B (channel):

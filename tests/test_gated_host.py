@@ -31,12 +31,13 @@ def g():
 def test_declared_functions_are_exported_and_bound(g):
     text = open(os.path.join(ROOT, "include", "gemm_bf16.h")).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    names = sorted(set(re.findall(r"\b(gemm_(?:i8|gated|backward)\w*)\s*\(", text)))
+    names = sorted(set(re.findall(r"\b(gemm_(?:i8|gated|backward|work)\w*)\s*\(", text)))
     assert names == ["gemm_backward", "gemm_backward_config_name", "gemm_backward_work_size",
                      "gemm_gated", "gemm_gated_backward", "gemm_gated_backward_config_name",
                      "gemm_gated_backward_work_size", "gemm_gated_config_name", "gemm_gated_ex",
                      "gemm_gated_kept_row", "gemm_i8", "gemm_i8_config_at", "gemm_i8_config_name", "gemm_i8_ex",
-                     "gemm_i8_gated", "gemm_i8_gated_ex", "gemm_i8_quantize"]
+                     "gemm_i8_gated", "gemm_i8_gated_ex", "gemm_i8_quantize", "gemm_work",
+                     "gemm_work_size"]
     so = ctypes.CDLL(g.LIB_PATH)
     for n in names:
         assert hasattr(so, n) and hasattr(g, n), n
@@ -166,6 +167,26 @@ def gated_backward(g, type=F16, M=8, F=9, K=64, dH=P, lddh=16, X=P, ldx=64, W=P,
     (dict(F=1 << 22, lddh=1 << 22, ld_kept=1 << 25), 3)])
 def test_gated_backward_refusals(g, bad, code):
     assert gated_backward(g, **bad) == code
+
+
+def work(g, type=BF16, M=256, N=8192, K=8192, A=P, lda=8192, B=P, ldb=8192, C=P, ldc=8192, work=P,
+         nbytes=1 << 30):
+    return g._lib.gemm_work(type, M, N, K, A, lda, B, ldb, C, ldc, work, nbytes, None)
+
+
+@pytest.mark.parametrize("bad, code", [
+    (dict(type=F32), 1), (dict(type=I8), 1), (dict(M=-1), 1), (dict(lda=8184), 1), (dict(A=NUL), 1),
+    (dict(C=NUL), 1), (dict(A=ODD), 2), (dict(work=ODD), 2), (dict(ldc=8196), 2), (dict(work=NUL), 6),
+    (dict(nbytes=1 << 20), 6), (dict(M=0, C=NUL, work=NUL), 0), (dict(ldb=1 << 30), 3)])
+def test_work_refusals(g, bad, code):
+    assert work(g, **bad) == code
+
+
+def test_work_sizes_are_the_dense_products(g):
+    for M, N, K in ((1, 8192, 8192), (256, 8192, 8192), (512, 10240, 8192), (4096, 4096, 4096)):
+        for t in (BF16, F16):
+            assert g.work_size(t, M, N, K) == g.workspace_size(M, N, K)
+    assert g.work_size(BF16, 256, 8192, 8192) > 0 == g.work_size(F32, 256, 8192, 8192)
 
 
 def test_workspaces(g):

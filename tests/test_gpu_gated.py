@@ -495,3 +495,82 @@ def test_two_streams_at_once():
     for i in range(2):
         for r in got[i]:
             assert all(torch.equal(a, b) for a, b in zip(r, want[i]))
+
+
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("M, N, K", [(256, 1024, 4096), (1, 520, 1000), (777, 1234, 600)])
+def test_products_in_a_given_workspace_are_the_same(M, N, K, t):
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = np.random.default_rng(M)
+    a, b = dev(normal(rng, (M, K), t)), dev(normal(rng, (N, K), t))
+    code = g.GEMM_TYPE_BF16 if t == "bf16" else g.GEMM_TYPE_F16
+    n = g.work_size(code, M, N, K)
+    ld = -(-N // 8) * 8
+    c, want = (torch.full((M, ld), 7.0, device="cuda", dtype=dtype(t)) for _ in range(2))
+    work = torch.full((n + 64,), 99, device="cuda", dtype=torch.uint8)
+    g.gemm_work(code, M, N, K, a, a.stride(0), b, b.stride(0), c, ld, work, n)
+    g.matmul(a, b, out=want[:, :N])
+    torch.cuda.synchronize()
+    assert torch.equal(c, want) and (work[n:] == 99).all()
+
+
+def test_two_captured_layers_replayed_at_once():
+    """Graphs captured on one stream, with split plans, replayed on two."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    torch.manual_seed(5)
+    M, F, K, N = 256, 4096, 512, 1024
+    assert g.work_size(g.GEMM_TYPE_BF16, M, N, F) > 0
+    w1 = (torch.randn(2 * F, K, device="cuda") * K ** -0.5).to(torch.bfloat16)
+    w2 = (torch.randn(N, F, device="cuda") * F ** -0.5).to(torch.bfloat16)
+    xs = [torch.randn(M, K, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    g.gated_mlp(xs[0], w1, w2)
+    torch.cuda.synchronize()
+    graphs, outs, stream = [], [], torch.cuda.Stream()
+    for x in xs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=stream):
+            outs.append(g.gated_mlp(x, w1, w2))
+        graphs.append(graph)
+    sides = [torch.cuda.Stream() for _ in xs]
+    for _ in range(5):
+        for x in xs:
+            x.normal_()
+        torch.cuda.synchronize()
+        for graph, side in zip(graphs, sides):
+            with torch.cuda.stream(side):
+                graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(xs, outs):
+            assert torch.equal(y, g.gated_mlp(x, w1, w2))
+
+
+def test_gradients_past_32_bits():
+    """A weight whose second half starts past 2^32 bytes, and its gradient."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    F, K, M = 300000, 8192, 3
+    at = [0, 1, 131071, 262144, F - 1]
+    rng = np.random.default_rng(2)
+    w = torch.zeros(2 * F, K, device="cuda", dtype=torch.bfloat16)
+    rows = normal(rng, (2 * len(at), K), "bf16", K ** -0.5)
+    w[at], w[[F + i for i in at]] = rows[:len(at)].cuda(), rows[len(at):].cuda()
+    x, dh_at = normal(rng, (M, K), "bf16"), normal(rng, (M, len(at)), "bf16")
+    dh = torch.zeros(M, F, device="cuda", dtype=torch.bfloat16)
+    dh[:, at] = dh_at.cuda()
+    _, kept = g.gated_matmul(x.cuda(), w, save=True)
+    dx, dw = g.gated_matmul_backward(dh, x.cuda(), w, kept)
+    torch.cuda.synchronize()
+    got = [v[:, at] for v in ref.unkept(kept.cpu().numpy(), F)]
+    few = torch.from_numpy(ref.keep(*got))
+    both = at + [F + i for i in at]
+    check_gated_backward(dx.cpu(), dw[both].cpu(), dh_at, x, rows, few, "swiglu", "bf16", "bf16")
+    assert int((dw != 0).any(1).sum()) <= 2 * len(at)
+    del w, dw, dh

@@ -254,6 +254,14 @@ def test_quantize_special_rows():
     assert np.isnan(s[4]) and np.isnan(s[5])
 
 
+def test_quantize_rows_without_columns():
+    """Scales of the floor, no codes."""
+    import torch
+
+    q, s = quantized(torch.zeros(3, 0, device="cuda", dtype=torch.bfloat16))
+    assert q.shape == (3, 0) and np.array_equal(s, ref.quantize(np.zeros((3, 0)))[1])
+
+
 def test_quantize_leaves_what_lies_past_k():
     import torch
 
