@@ -95,12 +95,16 @@ _moe_args = [_c_int, _i64, _i64, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _p, _
 _i8_args = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _p, _i64, _c_int, _p]
 _i8_gated_args = [_i64, _i64, _i64, _p, _i64, _p, _p, _i64, _p, _c_int, _p, _i64, _c_int, _p]
 _gated_args = [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _c_int, _p, _i64, _p, _i64, _p]
+_backward_args = [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64,
+                  _c_int, _p, ctypes.c_size_t, _p]
+_gated_backward_args = [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _c_int, _p, _i64,
+                        _p, _i64, _p, _i64, _c_int, _p, ctypes.c_size_t, _p]
 for _name, _args in {
     "gemm_work": [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, ctypes.c_size_t, _p],
-    "gemm_backward": [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64, _p, _i64,
-                      _c_int, _p, ctypes.c_size_t, _p],
-    "gemm_gated_backward": [_c_int, _i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _c_int, _p,
-                            _i64, _p, _i64, _p, _i64, _c_int, _p, ctypes.c_size_t, _p],
+    "gemm_backward": _backward_args,
+    "gemm_backward_ex": [ctypes.c_char_p, *_backward_args],
+    "gemm_gated_backward": _gated_backward_args,
+    "gemm_gated_backward_ex": [ctypes.c_char_p, *_gated_backward_args],
     "gemm_i8": _i8_args,
     "gemm_i8_ex": [ctypes.c_char_p, *_i8_args],
     "gemm_i8_quantize": [_i64, _i64, _p, _i64, _c_int, _p, _i64, _p, _p],
@@ -126,7 +130,7 @@ _lib.gemm_moe_config_name.restype = ctypes.c_char_p
 _lib.gemm_moe_config_name.argtypes = [_c_int, _i64, _i64, _i64, _i64, _c_int]
 for _name in ("gemm_backward_work_size", "gemm_gated_backward_work_size"):
     getattr(_lib, _name).restype = ctypes.c_size_t
-    getattr(_lib, _name).argtypes = [_i64, _i64, _i64]
+    getattr(_lib, _name).argtypes = [ctypes.c_char_p, _i64, _i64, _i64]
 _lib.gemm_work_size.restype = ctypes.c_size_t
 _lib.gemm_work_size.argtypes = [_c_int, _i64, _i64, _i64]
 _lib.gemm_gated_kept_row.restype = ctypes.c_size_t
@@ -487,27 +491,44 @@ gemm_work_size = work_size
 def gemm_backward(type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, db_type, work=None,
                   work_bytes=0, stream=None) -> None:
     """Gradients of C = A . B^T: dA = dC . B and dB = dC^T . A."""
-    _check(_lib.gemm_backward(type, M, N, K, _ptr(dC), lddc, _ptr(A), lda, _ptr(B), ldb, _ptr(dA),
-                              ldda, _ptr(dB), lddb, db_type, _ptr(work), work_bytes,
-                              _stream(stream)))
+    gemm_backward_ex(None, type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, db_type,
+                     work, work_bytes, stream)
+
+
+def gemm_backward_ex(config, type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb, db_type,
+                     work=None, work_bytes=0, stream=None) -> None:
+    """As gemm_backward with the plan named (None = automatic)."""
+    cfg = None if config is None else config.encode()
+    _check(_lib.gemm_backward_ex(cfg, type, M, N, K, _ptr(dC), lddc, _ptr(A), lda, _ptr(B), ldb,
+                                 _ptr(dA), ldda, _ptr(dB), lddb, db_type, _ptr(work), work_bytes,
+                                 _stream(stream)))
 
 
 def gemm_gated_backward(type, M, F, K, dH, lddh, X, ldx, W, ldw, act, kept, ld_kept, dX, lddx, dW,
                         lddw, dw_type, work=None, work_bytes=0, stream=None) -> None:
     """Gradients of gemm_gated's X and W from H's and what it kept."""
-    _check(_lib.gemm_gated_backward(type, M, F, K, _ptr(dH), lddh, _ptr(X), ldx, _ptr(W), ldw, act,
-                                    _ptr(kept), ld_kept, _ptr(dX), lddx, _ptr(dW), lddw, dw_type,
-                                    _ptr(work), work_bytes, _stream(stream)))
+    gemm_gated_backward_ex(None, type, M, F, K, dH, lddh, X, ldx, W, ldw, act, kept, ld_kept, dX,
+                           lddx, dW, lddw, dw_type, work, work_bytes, stream)
 
 
-def backward_work_size(M, N, K) -> int:
-    """Bytes of workspace gemm_backward needs."""
-    return int(_lib.gemm_backward_work_size(M, N, K))
+def gemm_gated_backward_ex(config, type, M, F, K, dH, lddh, X, ldx, W, ldw, act, kept, ld_kept, dX,
+                           lddx, dW, lddw, dw_type, work=None, work_bytes=0, stream=None) -> None:
+    """As gemm_gated_backward with the plan named (None = automatic)."""
+    cfg = None if config is None else config.encode()
+    _check(_lib.gemm_gated_backward_ex(cfg, type, M, F, K, _ptr(dH), lddh, _ptr(X), ldx, _ptr(W),
+                                       ldw, act, _ptr(kept), ld_kept, _ptr(dX), lddx, _ptr(dW),
+                                       lddw, dw_type, _ptr(work), work_bytes, _stream(stream)))
 
 
-def gated_backward_work_size(M, F, K) -> int:
-    """Bytes of workspace gemm_gated_backward needs."""
-    return int(_lib.gemm_gated_backward_work_size(M, F, K))
+def backward_work_size(M, N, K, config=None) -> int:
+    """Bytes of workspace gemm_backward needs (for a plan named)."""
+    return int(_lib.gemm_backward_work_size(None if config is None else config.encode(), M, N, K))
+
+
+def gated_backward_work_size(M, F, K, config=None) -> int:
+    """Bytes of workspace gemm_gated_backward needs (for a plan named)."""
+    return int(_lib.gemm_gated_backward_work_size(None if config is None else config.encode(), M, F,
+                                                  K))
 
 
 def backward_config_name(M, N, K) -> str:
@@ -945,12 +966,12 @@ def _weight_dtype(dw, dw_dtype, dtype):
     return t
 
 
-def matmul_backward(dC, A, B, dA=None, dB=None, db_dtype=None):
+def matmul_backward(dC, A, B, dA=None, dB=None, db_dtype=None, config=None):
     """Gradients of matmul's C = A . B^T from dC (M x N): (dA, dB) with dA = dC .
     B (M x K) and dB = dC^T . A (N x K).  dC, A and B are all bfloat16 or all
     float16.  dA, dB: tensors to write, None for new ones, False where a
     gradient is not wanted (None is returned).  db_dtype: A's type (default) or
-    float32."""
+    float32.  config: the plan's name (None = automatic)."""
     _need(dC, "dC")
     dev, dtype = dC.device, dC.dtype
     code = _type(dtype, "dC", (GEMM_TYPE_BF16, GEMM_TYPE_F16))
@@ -965,18 +986,20 @@ def matmul_backward(dC, A, B, dA=None, dB=None, db_dtype=None):
     if dA is not None and dA.dtype != dtype:
         raise TypeError(f"dA must be {dtype}")
     dB = _grad(dB, (N, K), db_dtype, dev, "dB")
-    nbytes = _lib.gemm_backward_work_size(M, N, K)
+    cfg = None if config is None else config.encode()
+    nbytes = _lib.gemm_backward_work_size(cfg, M, N, K)
     work = _work(nbytes, dev)
-    _call(_lib.gemm_backward, dev, code, M, N, K, dC.data_ptr(), _ld(dC, 8), A.data_ptr(),
+    _call(_lib.gemm_backward_ex, dev, cfg, code, M, N, K, dC.data_ptr(), _ld(dC, 8), A.data_ptr(),
           _ld(A, 8), B.data_ptr(), _ld(B, 8), _ptr(dA), 0 if dA is None else _ld(dA, 8), _ptr(dB),
           0 if dB is None else _ld(dB, 8), _TYPES[db_dtype], _ptr(work), nbytes)
     return dA, dB
 
 
-def gated_matmul_backward(dh, x, W, kept, act="swiglu", dx=None, dw=None, dw_dtype=None):
+def gated_matmul_backward(dh, x, W, kept, act="swiglu", dx=None, dw=None, dw_dtype=None,
+                          config=None):
     """Gradients of gated_matmul's x and W from dh (M x F) and what it kept
-    (save=True): (dx, dW).  act as in the forward call; dx, dw and
-    dw_dtype as matmul_backward's dA, dB and db_dtype."""
+    (save=True): (dx, dW).  act as in the forward call; dx, dw,
+    dw_dtype and config as matmul_backward's dA, dB, db_dtype and config."""
     _need(x, "x")
     dev, dtype = x.device, x.dtype
     code = _type(dtype, "x", (GEMM_TYPE_BF16, GEMM_TYPE_F16))
@@ -991,9 +1014,10 @@ def gated_matmul_backward(dh, x, W, kept, act="swiglu", dx=None, dw=None, dw_dty
     if dx is not None and dx.dtype != dtype:
         raise TypeError(f"dx must be {dtype}")
     dw = _grad(dw, (2 * F, K), dw_dtype, dev, "dw")
-    nbytes = _lib.gemm_gated_backward_work_size(M, F, K)
+    cfg = None if config is None else config.encode()
+    nbytes = _lib.gemm_gated_backward_work_size(cfg, M, F, K)
     work = _work(nbytes, dev)
-    _call(_lib.gemm_gated_backward, dev, code, M, F, K, dh.data_ptr(), _ld(dh, 8), x.data_ptr(),
+    _call(_lib.gemm_gated_backward_ex, dev, cfg, code, M, F, K, dh.data_ptr(), _ld(dh, 8), x.data_ptr(),
           _ld(x, 8), W.data_ptr(), _ld(W, 8), _act(act), kept.data_ptr(),
           _ld(kept, 16), _ptr(dx), 0 if dx is None else _ld(dx, 8), _ptr(dw),
           0 if dw is None else _ld(dw, 8), _TYPES[dw_dtype], _ptr(work), nbytes)

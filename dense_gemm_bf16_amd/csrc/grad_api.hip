@@ -2,6 +2,8 @@
 // checks, the choice of tile and split, launch.  The contract of every entry
 // point is stated in include/gemm_bf16.h.  Nothing here allocates or throws.
 #include <stdio.h>
+#include <stdlib.h>
+#include <string.h>
 
 #include "../../include/gemm_bf16.h"
 #include "gemm_internal.h"
@@ -55,9 +57,21 @@ int64_t split_bytes(const GradShape& p, int splits) {
   return splits > 1 ? 4 * splits * part_floats(p) : 0;
 }
 
+// The ways that leave none of n steps' slices empty.
+int even_splits(int64_t n, int64_t s) {
+  if (s > n) s = n;
+  if (s <= 1) return 1;
+  const int64_t per = (n + s - 1) / s;
+  return (int)((n + per - 1) / per);
+}
+
 // The tile and splits whose launch a model finds cheapest: as long as its
 // longest workgroup, shorter where the GPU is part empty, or as all of them
 // over the places there are; and for splits the round trip of their fp32 sums.
+// Its constants were searched for the best choice over 52 products, each timed
+// in all plans that were in question: 0.5 % from the fastest plan there, 2.4 %
+// over 49 products of which 37 are others (25 % at worst).  gated_model.py
+// holds the same model and the times.
 GradPlan choose(const GradShape& x, const GradShape& w) {
   GradPlan best{nullptr, 1, 1};
   double best_t = 0;
@@ -85,18 +99,33 @@ GradPlan choose(const GradShape& x, const GradShape& w) {
       }
     }
   }
-  // (splits that leave no workgroup empty)
-  auto even = [](int64_t n, int s) {
-    const int64_t per = s > 1 ? (n + s - 1) / s : 1;
-    return s > 1 ? (int)((n + per - 1) / per) : 1;
-  };
-  best.split_x = even(steps[0], best.split_x);
-  best.split_w = even(steps[1], best.split_w);
+  best.split_x = even_splits(steps[0], best.split_x);
+  best.split_w = even_splits(steps[1], best.split_w);
   return best;
 }
 
-int64_t plan_bytes(const GradShape& x, const GradShape& w) {
-  const GradPlan p = choose(x, w);
+// The plan a call names ("b128x128_k4_k1"), or without a name the chosen one;
+// no tile: there is no such plan.
+GradPlan plan_of(const char* config, const GradShape& x, const GradShape& w) {
+  if (!config || !config[0]) return choose(x, w);
+  GradPlan p{nullptr, 1, 1};
+  for (const GradTile& t : kTiles) {
+    const size_t n = strlen(t.name);
+    if (strncmp(config, t.name, n) != 0 || strncmp(config + n, "_k", 2) != 0) continue;
+    char* end = nullptr;
+    const long sx = strtol(config + n + 2, &end, 10);
+    if (strncmp(end, "_k", 2) != 0) continue;
+    const long sw = strtol(end + 2, &end, 10);
+    if (*end || sx < 1 || sx > 64 || sw < 1 || sw > 64) continue;
+    p = GradPlan{&t, even_splits(steps_of(x), sx), even_splits(steps_of(w), sw)};
+    // (a grid holds fewer than 2^32 threads)
+    if (tiles_of(t, x) * p.split_x + tiles_of(t, w) * p.split_w >= 2 * k2G / t.threads - 8)
+      p.tile = nullptr;
+  }
+  return p;
+}
+
+int64_t plan_bytes(const GradPlan& p, const GradShape& x, const GradShape& w) {
   return split_bytes(x, p.split_x) + split_bytes(w, p.split_w);
 }
 
@@ -152,9 +181,9 @@ int store_of(int type) {
 }
 
 // Both products (a shape without rows or columns: none) and their sums.
-hipError_t grad_products(int type, const GradShape& x, const Operands& ox, const GradShape& w,
-                         const Operands& ow, int w_type, void* work, hipStream_t stream) {
-  const GradPlan plan = choose(x, w);
+hipError_t grad_products(const GradPlan& plan, int type, const GradShape& x, const Operands& ox,
+                         const GradShape& w, const Operands& ow, int w_type, void* work,
+                         hipStream_t stream) {
   const GradTile& t = *plan.tile;
   float* const px = (float*)work;
   float* const pw = px + split_bytes(x, plan.split_x) / 4;
@@ -201,9 +230,16 @@ const char* plan_name(const GradShape& x, const GradShape& w) {
   return g_plan_name;
 }
 
-// Parts of both gradients, or of either one alone.
-int64_t most_bytes(const GradShape& x, const GradShape& w) {
-  return larger(plan_bytes(x, w), larger(plan_bytes(x, kNoProduct), plan_bytes(kNoProduct, w)));
+// Parts of both gradients, or of either one alone; -1: no such plan.
+int64_t most_bytes(const char* config, const GradShape& x, const GradShape& w) {
+  int64_t most = 0;
+  const GradShape pairs[3][2] = {{x, w}, {x, kNoProduct}, {kNoProduct, w}};
+  for (const auto& p : pairs) {
+    const GradPlan plan = plan_of(config, p[0], p[1]);
+    if (!plan.tile) return -1;
+    most = larger(most, plan_bytes(plan, p[0], p[1]));
+  }
+  return most;
 }
 
 int64_t gate_bytes(int64_t M, int64_t F) { return up256(M * 2 * up8(F) * 2); }
@@ -213,9 +249,11 @@ int64_t gate_bytes(int64_t M, int64_t F) { return up256(M * 2 * up8(F) * 2); }
 
 extern "C" {
 
-size_t gemm_backward_work_size(int64_t M, int64_t N, int64_t K) {
+size_t gemm_backward_work_size(const char* config, int64_t M, int64_t N, int64_t K) {
   if (M < 0 || N < 0 || K < 0 || gemm::size_refused(M, N, K)) return 0;
-  return (size_t)gemm::most_bytes(gemm::input_shape(M, N, K), gemm::weight_shape(M, N, K));
+  const int64_t n =
+      gemm::most_bytes(config, gemm::input_shape(M, N, K), gemm::weight_shape(M, N, K));
+  return n > 0 ? (size_t)n : 0;
 }
 
 const char* gemm_backward_config_name(int64_t M, int64_t N, int64_t K) {
@@ -228,10 +266,10 @@ const char* gemm_gated_backward_config_name(int64_t M, int64_t F, int64_t K) {
   return gemm::plan_name(gemm::gated_input_shape(M, F, K), gemm::gated_weight_shape(M, F, K));
 }
 
-int gemm_backward(int type, int64_t M, int64_t N, int64_t K, const void* dC, int64_t lddc,
-                  const void* A, int64_t lda, const void* B, int64_t ldb, void* dA, int64_t ldda,
-                  void* dB, int64_t lddb, int db_type, void* work, size_t work_bytes,
-                  void* stream) {
+int gemm_backward_ex(const char* config, int type, int64_t M, int64_t N, int64_t K, const void* dC,
+                     int64_t lddc, const void* A, int64_t lda, const void* B, int64_t ldb, void* dA,
+                     int64_t ldda, void* dB, int64_t lddb, int db_type, void* work,
+                     size_t work_bytes, void* stream) {
   using namespace gemm;
   if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
   if (type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return GEMM_ERR_INVALID_ARG;
@@ -253,23 +291,34 @@ int gemm_backward(int type, int64_t M, int64_t N, int64_t K, const void* dC, int
   const GradShape pb = has_b ? weight_shape(M, N, K) : kNoProduct;
   if ((has_a && !runs(pa, true, lddc, ldb)) || (has_b && !runs(pb, false, lddc, lda)))
     return GEMM_ERR_UNSUPPORTED;
-  const int64_t need = plan_bytes(pa, pb);
+  const GradPlan plan = plan_of(config, pa, pb);
+  if (!plan.tile) return GEMM_ERR_UNSUPPORTED;
+  const int64_t need = plan_bytes(plan, pa, pb);
   if (need > 0 && (!work || (int64_t)work_bytes < need)) return GEMM_ERR_SCRATCH;
   const hipError_t e =
-      grad_products(type, pa, Operands{dC, B, lddc, ldb, 0, 0, 0, dA, ldda}, pb,
+      grad_products(plan, type, pa, Operands{dC, B, lddc, ldb, 0, 0, 0, dA, ldda}, pb,
                     Operands{dC, A, lddc, lda, 0, 0, 0, dB, lddb}, dB ? db_type : type, work,
                     (hipStream_t)stream);
   return e == hipSuccess ? GEMM_OK : hip_fail(e);
 }
 
-size_t gemm_gated_backward_work_size(int64_t M, int64_t F, int64_t K) {
-  if (M < 0 || F < 0 || K < 0 || gemm::size_refused(M, F, K)) return 0;
-  if (M > 0 && gemm::up8(F) > gemm::kStrideLimit / M) return 0;
-  return (size_t)(gemm::gate_bytes(M, F) + gemm::most_bytes(gemm::gated_input_shape(M, F, K),
-                                                           gemm::gated_weight_shape(M, F, K)));
+int gemm_backward(int type, int64_t M, int64_t N, int64_t K, const void* dC, int64_t lddc,
+                  const void* A, int64_t lda, const void* B, int64_t ldb, void* dA, int64_t ldda,
+                  void* dB, int64_t lddb, int db_type, void* work, size_t work_bytes,
+                  void* stream) {
+  return gemm_backward_ex(nullptr, type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb,
+                          db_type, work, work_bytes, stream);
 }
 
-int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* dH, int64_t lddh,
+size_t gemm_gated_backward_work_size(const char* config, int64_t M, int64_t F, int64_t K) {
+  if (M < 0 || F < 0 || K < 0 || gemm::size_refused(M, F, K)) return 0;
+  if (M > 0 && gemm::up8(F) > gemm::kStrideLimit / M) return 0;
+  const int64_t n = gemm::most_bytes(config, gemm::gated_input_shape(M, F, K),
+                                     gemm::gated_weight_shape(M, F, K));
+  return n < 0 ? 0 : (size_t)(gemm::gate_bytes(M, F) + n);
+}
+
+int gemm_gated_backward_ex(const char* config, int type, int64_t M, int64_t F, int64_t K, const void* dH, int64_t lddh,
                         const void* X, int64_t ldx, const void* W, int64_t ldw, int act,
                         const void* kept, int64_t ld_kept, void* dX, int64_t lddx, void* dW,
                         int64_t lddw, int dw_type, void* work, size_t work_bytes, void* stream) {
@@ -298,7 +347,9 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* d
   if ((has_x && !runs(px, true, 2 * Fp, ldw)) || (has_w && !runs(pw, false, 2 * Fp, ldx)))
     return GEMM_ERR_UNSUPPORTED;
   if (!has_x && !has_w) return GEMM_OK;
-  const int64_t gate = gate_bytes(M, F), need = gate + plan_bytes(px, pw);
+  const GradPlan plan = plan_of(config, px, pw);
+  if (!plan.tile) return GEMM_ERR_UNSUPPORTED;
+  const int64_t gate = gate_bytes(M, F), need = gate + plan_bytes(plan, px, pw);
   if (need > 0 && (!work || (int64_t)work_bytes < need)) return GEMM_ERR_SCRATCH;
   hipError_t e = hipSuccess;
   if (M > 0 && F > 0) {
@@ -307,10 +358,18 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* d
     e = launch_gate_grad(g, type == GEMM_TYPE_F16, (hipStream_t)stream);
   }
   if (e == hipSuccess)
-    e = grad_products(type, px, Operands{work, W, 2 * Fp, ldw, Fp, F * ldw, 0, dX, lddx}, pw,
+    e = grad_products(plan, type, px, Operands{work, W, 2 * Fp, ldw, Fp, F * ldw, 0, dX, lddx}, pw,
                       Operands{work, X, 2 * Fp, ldx, 0, 0, Fp, dW, lddw}, dW ? dw_type : type,
                       (uint8_t*)work + gate, (hipStream_t)stream);
   return e == hipSuccess ? GEMM_OK : hip_fail(e);
+}
+
+int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K, const void* dH, int64_t lddh,
+                        const void* X, int64_t ldx, const void* W, int64_t ldw, int act,
+                        const void* kept, int64_t ld_kept, void* dX, int64_t lddx, void* dW,
+                        int64_t lddw, int dw_type, void* work, size_t work_bytes, void* stream) {
+  return gemm_gated_backward_ex(nullptr, type, M, F, K, dH, lddh, X, ldx, W, ldw, act, kept,
+                                ld_kept, dX, lddx, dW, lddw, dw_type, work, work_bytes, stream);
 }
 
 }  // extern "C"

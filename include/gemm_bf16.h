@@ -554,7 +554,17 @@ int gemm_backward(int type, int64_t M, int64_t N, int64_t K,
                   const void* B, int64_t ldb, void* dA, int64_t ldda,
                   void* dB, int64_t lddb, int db_type,
                   void* work, size_t work_bytes, void* stream);
-size_t gemm_backward_work_size(int64_t M, int64_t N, int64_t K);
+size_t gemm_backward_work_size(const char* config, int64_t M, int64_t N, int64_t K);
+
+/* As gemm_backward with the plan named, in the form gemm_backward_config_name
+ * gives (1 to 64 ways; as many as there are K-steps of 64 at most); config NULL
+ * or "" = automatic, here and in the size of the workspace. */
+int gemm_backward_ex(const char* config, int type, int64_t M, int64_t N, int64_t K,
+                     const void* dC, int64_t lddc, const void* A, int64_t lda,
+                     const void* B, int64_t ldb, void* dA, int64_t ldda,
+                     void* dB, int64_t lddb, int db_type,
+                     void* work, size_t work_bytes, void* stream);
+
 /* The tile of both gradients' products, which share a launch, and the ways that
  * K of dA's and of dB's is split ("b128x128_k4_k1").  Per-thread static
  * storage. */
@@ -576,7 +586,13 @@ int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K,
                         const void* kept, int64_t ld_kept, void* dX, int64_t lddx,
                         void* dW, int64_t lddw, int dw_type,
                         void* work, size_t work_bytes, void* stream);
-size_t gemm_gated_backward_work_size(int64_t M, int64_t F, int64_t K);
+size_t gemm_gated_backward_work_size(const char* config, int64_t M, int64_t F, int64_t K);
+int gemm_gated_backward_ex(const char* config, int type, int64_t M, int64_t F, int64_t K,
+                           const void* dH, int64_t lddh, const void* X, int64_t ldx,
+                           const void* W, int64_t ldw, int act,
+                           const void* kept, int64_t ld_kept, void* dX, int64_t lddx,
+                           void* dW, int64_t lddw, int dw_type,
+                           void* work, size_t work_bytes, void* stream);
 const char* gemm_gated_backward_config_name(int64_t M, int64_t F, int64_t K);
 
 /* Human-readable text for a status code.  Static storage; never NULL. */

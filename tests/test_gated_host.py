@@ -32,8 +32,9 @@ def test_declared_functions_are_exported_and_bound(g):
     text = open(os.path.join(ROOT, "include", "gemm_bf16.h")).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     names = sorted(set(re.findall(r"\b(gemm_(?:i8|gated|backward|work)\w*)\s*\(", text)))
-    assert names == ["gemm_backward", "gemm_backward_config_name", "gemm_backward_work_size",
-                     "gemm_gated", "gemm_gated_backward", "gemm_gated_backward_config_name",
+    assert names == ["gemm_backward", "gemm_backward_config_name", "gemm_backward_ex",
+                     "gemm_backward_work_size", "gemm_gated", "gemm_gated_backward",
+                     "gemm_gated_backward_config_name", "gemm_gated_backward_ex",
                      "gemm_gated_backward_work_size", "gemm_gated_config_name", "gemm_gated_ex",
                      "gemm_gated_kept_row", "gemm_i8", "gemm_i8_config_at", "gemm_i8_config_name", "gemm_i8_ex",
                      "gemm_i8_gated", "gemm_i8_gated_ex", "gemm_i8_quantize", "gemm_work",
@@ -131,8 +132,8 @@ def test_quantize_refusals(g, bad, code):
 
 
 def backward(g, type=BF16, M=8, N=16, K=64, dC=P, lddc=16, A=P, lda=64, B=P, ldb=64, dA=P, ldda=64,
-             dB=P, lddb=64, db_type=BF16, work=P, nbytes=1 << 30):
-    return g._lib.gemm_backward(type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb,
+             dB=P, lddb=64, db_type=BF16, work=P, nbytes=1 << 30, config=None):
+    return g._lib.gemm_backward_ex(config, type, M, N, K, dC, lddc, A, lda, B, ldb, dA, ldda, dB, lddb,
                                 db_type, work, nbytes, None)
 
 
@@ -144,14 +145,20 @@ def backward(g, type=BF16, M=8, N=16, K=64, dC=P, lddc=16, A=P, lda=64, B=P, ldb
     (dict(dB=ODD), 2), (dict(work=ODD), 2), (dict(lddc=20), 2), (dict(lda=68), 2), (dict(ldb=68), 2),
     (dict(ldda=68), 2), (dict(lddb=68), 2), (dict(M=1 << 30), 3), (dict(K=1 << 30), 3),
     (dict(N=1 << 29, lddc=1 << 29), 3), (dict(lddc=1 << 40), 3), (dict(lddc=1 << 22), 3),
-    (dict(lda=1 << 24), 3), (dict(ldb=1 << 24), 3)])
+    (dict(lda=1 << 24), 3), (dict(ldb=1 << 24), 3), (dict(config=b"b64x64_k1_k1"), 3),
+    (dict(config=b"b128x128"), 3), (dict(config=b"b128x128_k1"), 3),
+    (dict(config=b"b128x128_k0_k1"), 3), (dict(config=b"b128x128_k1_k65"), 3),
+    (dict(config=b"b128x128_k1_k1x"), 3),
+    (dict(M=1 << 20, N=4096, K=1 << 17, lddc=4096, lda=1 << 17, ldb=1 << 17, ldda=1 << 17,
+          lddb=1 << 17, config=b"b128x128_k64_k1"), 3)])  # 2^32 threads
 def test_backward_refusals(g, bad, code):
     assert backward(g, **bad) == code
 
 
 def gated_backward(g, type=F16, M=8, F=9, K=64, dH=P, lddh=16, X=P, ldx=64, W=P, ldw=64, act=1,
-                   kept=P, ld_kept=96, dX=P, lddx=64, dW=P, lddw=64, dw_type=F32, work=P, nbytes=1 << 30):
-    return g._lib.gemm_gated_backward(type, M, F, K, dH, lddh, X, ldx, W, ldw, act, kept, ld_kept, dX,
+                   kept=P, ld_kept=96, dX=P, lddx=64, dW=P, lddw=64, dw_type=F32, work=P, nbytes=1 << 30,
+                   config=None):
+    return g._lib.gemm_gated_backward_ex(config, type, M, F, K, dH, lddh, X, ldx, W, ldw, act, kept, ld_kept, dX,
                                       lddx, dW, lddw, dw_type, work, nbytes, None)
 
 
@@ -164,7 +171,7 @@ def gated_backward(g, type=F16, M=8, F=9, K=64, dH=P, lddh=16, X=P, ldx=64, W=P,
     (dict(lddx=68), 2), (dict(lddw=68), 2), (dict(work=NUL), 6), (dict(nbytes=0), 6), (dict(M=1 << 30), 3),
     (dict(F=1 << 29, lddh=1 << 29, ld_kept=1 << 32), 3), (dict(F=(1 << 63) - 1), 3),
     (dict(M=1 << 20, F=1 << 16, lddh=1 << 16, ld_kept=1 << 19), 3), (dict(ldw=1 << 24), 3),
-    (dict(F=1 << 22, lddh=1 << 22, ld_kept=1 << 25), 3)])
+    (dict(F=1 << 22, lddh=1 << 22, ld_kept=1 << 25), 3), (dict(config=b"b128x128_k1"), 3)])
 def test_gated_backward_refusals(g, bad, code):
     assert gated_backward(g, **bad) == code
 
@@ -202,6 +209,12 @@ def test_workspaces(g):
     assert gated_backward(g, nbytes=need - 256, dX=NUL, dW=NUL) == 0  # nothing to do
     assert gated_backward(g, nbytes=need - 1) == 6 or need % 256 == 0
     assert g.gated_backward_work_size(0, 9, 64) == 0
+    # named: every part of every split; as many ways as there are steps of 64
+    assert g.backward_work_size(100, 200, 300, "b128x128_k1_k1") == 0
+    assert g.backward_work_size(100, 200, 300, "b128x128_k2_k1") == 4 * 2 * 100 * 300
+    assert g.backward_work_size(100, 200, 300, "b256x256_k9_k2") == 4 * (4 * 100 + 2 * 200) * 300
+    assert g.backward_work_size(100, 200, 300, "nope") == 0
+    assert g.gated_backward_work_size(100, 200, 300, "nope") == 0
 
 
 def test_empty_calls_launch_nothing(g):

@@ -222,6 +222,39 @@ def test_plans_that_the_gradients_run_as():
     assert seen >= {("b256x256", one, one), ("b256x256", one, two), ("b256x256", two, one)}, seen
 
 
+@pytest.mark.parametrize("config", ["b128x128_k1_k1", "b128x128_k3_k1", "b128x128_k1_k2",
+                                    "b128x128_k7_k6", "b256x256_k1_k1", "b256x256_k2_k3",
+                                    "b256x256_k14_k6"])
+def test_every_plan_is_exact_on_integers(config):
+    """Both tiles, any split of either product, on sizes that end inside tiles,
+    pieces and K-steps."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = np.random.default_rng(5)
+    M, N, K = 357, 421, 299
+    dc, a, b = (ints(rng, s, "bf16") for s in ((M, N), (M, K), (N, K)))
+    da, db = g.matmul_backward(dev(dc), dev(a, 2), dev(b), db_dtype=torch.float32, config=config)
+    DC = f64(dc)
+    assert np.array_equal(f64(db), DC.T @ f64(a))
+    want = torch.from_numpy(DC @ f64(b)).float().to(torch.bfloat16).double().numpy()
+    assert np.array_equal(f64(da), want)
+    # a gated product's, with dG and dU that are exact: g so large that the
+    # sigmoid is 1, so dg = dh u and du = dh g
+    F = 213
+    dh, x, w = ints(rng, (M, F), "bf16", 1), ints(rng, (M, K), "bf16"), ints(rng, (2 * F, K), "bf16", 1)
+    big = rng.integers(1, 3, (M, F)) * 128.0
+    u = rng.integers(-2, 3, (M, F)).astype(np.float64)
+    kept = torch.from_numpy(ref.keep(big, u)).cuda()
+    dx, dw = g.gated_matmul_backward(dev(dh), dev(x), dev(w, 2), kept, dw_dtype=torch.float32,
+                                     config=config)
+    d = np.concatenate([f64(dh) * u, f64(dh) * big], 1)
+    assert np.array_equal(f64(dw), d.T @ f64(x))
+    want = torch.from_numpy(d @ f64(w)).float().to(torch.bfloat16).double().numpy()
+    assert np.array_equal(f64(dx), want)
+
+
 @pytest.mark.parametrize("M, N, K", [(40, 5000, 100), (333, 777, 555), (1500, 100, 60), (2100, 2056, 700)])
 def test_product_gradients_on_normal_values(M, N, K):
     import torch
