@@ -25,7 +25,7 @@ constexpr int64_t kMaxIntK = 131071;  // 2^14 K stays below 2^31
 // whole takes at least as long as reading B.  Fitted to 483 products (M 1 to
 // 4096, B from 512 x 1024 to 28672 x 4096, integers plain and gated, bf16
 // gated), each timed in the shapes that were in question; its choice ran within
-// 2.3 % of the fastest of them (geometric mean; 36 % at worst).  gated_model.py
+// 2.4 % of the fastest of them (geometric mean; 35 % at worst).  gated_model.py
 // holds the same model, the sweep, its times and the fit, which gives these
 // constants.
 struct Cost {
@@ -41,35 +41,35 @@ const Shape kShapes[] = {
   {{#NAME, A, B, (C) * (D) * (E) * 64, (B) / (D) / 16 % 2 == 0,                           \
     &launch_gated_tile<A, B, C, D, E, S>}, E, RESIDENT, __VA_ARGS__},
     ROW(b256x256, 256, 256, 2, 4, 1, 2, 1,
-        {1.420f, 13.21f, 0.66f, 0.00f}, {1.337f, 13.14f, 0.80f, 0.00f})
+        {1.401f, 13.14f, 0.67f, 0.00f}, {1.343f, 12.98f, 0.80f, 0.00f})
     ROW(b256x128, 256, 128, 4, 2, 1, 3, 1,
-        {0.839f, 9.02f, 0.68f, 0.00f}, {0.878f, 7.35f, 0.74f, 0.00f})
+        {0.847f, 8.58f, 0.70f, 0.00f}, {0.883f, 7.26f, 0.74f, 0.00f})
     ROW(b128x128, 128, 128, 2, 2, 1, 2, 2,
-        {0.832f, 9.63f, 0.50f, 0.00f}, {0.904f, 6.89f, 0.53f, 0.00f})
+        {0.833f, 9.37f, 0.51f, 0.02f}, {0.907f, 6.92f, 0.52f, 0.00f})
     ROW(b128x128k2, 128, 128, 2, 2, 2, 2, 1,
-        {1.039f, 6.52f, 0.79f, 1.03f}, {1.095f, 5.36f, 0.82f, 0.98f})
+        {1.036f, 6.46f, 0.80f, 1.05f}, {1.071f, 5.93f, 0.83f, 0.44f})
     ROW(b64x128k2, 64, 128, 2, 2, 2, 3, 1,
-        {0.701f, 4.38f, 0.87f, 0.70f}, {0.750f, 3.63f, 0.88f, 0.75f})
+        {0.700f, 4.28f, 0.88f, 0.72f}, {0.744f, 3.76f, 0.89f, 0.55f})
     ROW(b64x64, 64, 64, 2, 2, 1, 4, 2,
-        {0.407f, 3.18f, 0.57f, 1.57f}, {0.421f, 2.63f, 0.59f, 1.59f})
+        {0.403f, 3.26f, 0.58f, 1.47f}, {0.418f, 2.64f, 0.60f, 1.51f})
     ROW(b64x64k2, 64, 64, 2, 2, 2, 4, 1,
-        {0.448f, 3.20f, 0.84f, 1.49f}, {0.477f, 2.43f, 0.84f, 2.19f})
+        {0.450f, 3.10f, 0.83f, 1.61f}, {0.459f, 2.73f, 0.86f, 1.97f})
     ROW(b32x128, 32, 128, 1, 4, 1, 3, 2,
-        {0.531f, 3.21f, 0.60f, 0.82f}, {0.606f, 0.00f, 0.55f, 2.34f})
+        {0.518f, 3.52f, 0.62f, 0.60f}, {0.592f, 0.35f, 0.56f, 2.17f})
     ROW(b32x64k4, 32, 64, 2, 2, 4, 3, 1,
-        {0.644f, 3.39f, 0.89f, 1.39f}, {0.692f, 3.08f, 0.86f, 1.93f})
+        {0.655f, 3.26f, 0.90f, 1.49f}, {0.690f, 3.11f, 0.88f, 1.84f})
     ROW(b32x32k4, 32, 32, 2, 2, 4, 4, 1,
-        {0.412f, 3.24f, 0.96f, 0.96f}, {0, 0, 0, 0})
+        {0.411f, 3.24f, 0.97f, 0.94f}, {0, 0, 0, 0})
 #undef ROW
 #define ROW(NAME, A, B, C, D, E, RESIDENT, ...)                                             \
   {{#NAME, 16 * (A), (E) * (B), (C) * 64, true, &launch_gated_row<A, B, C, D, E>}, C, RESIDENT, \
    __VA_ARGS__},
     ROW(r16x16, 1, 1, 8, 4, 16, 4,
-        {3.176f, 2.56f, 0.17f, 2.17f}, {2.885f, 4.16f, 0.18f, 2.10f})
+        {3.184f, 2.51f, 0.16f, 2.19f}, {2.873f, 4.15f, 0.18f, 2.09f})
     ROW(r16x8, 1, 1, 8, 4, 8, 4,
-        {2.207f, 2.48f, 0.15f, 2.21f}, {2.183f, 3.17f, 0.13f, 2.44f})
+        {2.213f, 2.44f, 0.15f, 2.22f}, {2.216f, 3.05f, 0.13f, 2.49f})
     ROW(r32x16, 2, 1, 8, 4, 16, 4,
-        {3.325f, 4.05f, 0.25f, 1.64f}, {3.576f, 4.19f, 0.20f, 2.33f})
+        {3.339f, 4.01f, 0.25f, 1.65f}, {3.152f, 6.31f, 0.25f, 1.39f})
 #undef ROW
 };
 constexpr double kStreamMBPerUs = 6.3, kStreamBaseUs = 2.2;
@@ -230,8 +230,14 @@ int dense_product(const char* config, int type, bool gated, int64_t M, int64_t N
     a.N = (int32_t)(gated ? rows_b / 2 : rows_b);
     a.tiles_n = (int32_t)tiles_n(s, rows_b);
     a.row_tiles = (int32_t)row_tiles;
-    // (one row of tiles: see the block products)
-    a.k_rot = row_tiles == 1 ? 3 : 0;
+    // Rows of a power-of-two stride would send all workgroups to the same
+    // memory channels: tile column j starts 3 j K-steps in where one row of
+    // tiles reads all of B (see the block products), j where several share B
+    // and its rows lie whole pages of 4 KB apart (bf16: 64, 128, 256 rows by
+    // 8192 x 8192 37.4, 44.0, 58.3 us without, 33.5, 40.0, 55.5 with, 4096^3
+    // 107.7, 101.9; integers: 4096^3 64.8, 59.5; larger ones level, and with
+    // other strides 0-2 % slower).
+    a.k_rot = row_tiles == 1 ? 3 : p.ldb % 4096 == 0 ? 1 : 0;
     return s.built.launch(a, (int)(row_tiles * a.tiles_n), (hipStream_t)stream, op_of(type),
                           store_of(c_type), gated, row_tiles == 1);
   };

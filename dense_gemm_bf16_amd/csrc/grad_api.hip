@@ -37,10 +37,10 @@ struct GradTile {
   hipError_t (*launch)(const GradPair&, hipStream_t, int op, int out_x, int out_w);
 };
 const GradTile kTiles[] = {
-    {"b256x256", 256, 256, 512, 1, 1.176, 20.3, 0.949, &launch_grad_pair<256, 256, 2, 4, 2>},
-    {"b128x128", 128, 128, 256, 2, 0.878, 10.3, 0.425, &launch_grad_pair<128, 128, 2, 2, 2>},
+    {"b256x256", 256, 256, 512, 1, 1.277, 12.3, 0.675, &launch_grad_pair<256, 256, 2, 4, 2>},
+    {"b128x128", 128, 128, 256, 2, 0.841, 6.1, 0.806, &launch_grad_pair<128, 128, 2, 2, 2>},
 };
-constexpr double kSumUs = 0.26, kSumUsPerMB = 0.366, kTail = 0.273;
+constexpr double kSumUs = 3.89, kSumUsPerMB = 0.555, kTail = 0.136;
 
 struct GradPlan {
   const GradTile* tile;
@@ -70,7 +70,7 @@ int even_splits(int64_t n, int64_t s) {
 // over the places there are; and for splits the round trip of their fp32 sums.
 // Its constants were searched for the best choice over 46 products (1 to 8192
 // tokens, 256 to 14336 x 128 to 4096), each timed in the plans that were in
-// question: 0.7 % from the fastest of them, and 1.2 % over 46 other products
+// question: 0.9 % from the fastest of them, and 0.8 % over 46 other products
 // (16 % at worst).  gated_model.py holds the same model, the sweep, its times
 // and the search.
 GradPlan choose(const GradShape& x, const GradShape& w) {
