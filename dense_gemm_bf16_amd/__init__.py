@@ -1017,8 +1017,8 @@ def gated_matmul_backward(dh, x, W, kept, act="swiglu", dx=None, dw=None, dw_dty
     cfg = None if config is None else config.encode()
     nbytes = _lib.gemm_gated_backward_work_size(cfg, M, F, K)
     work = _work(nbytes, dev)
-    _call(_lib.gemm_gated_backward_ex, dev, cfg, code, M, F, K, dh.data_ptr(), _ld(dh, 8), x.data_ptr(),
-          _ld(x, 8), W.data_ptr(), _ld(W, 8), _act(act), kept.data_ptr(),
+    _call(_lib.gemm_gated_backward_ex, dev, cfg, code, M, F, K, dh.data_ptr(), _ld(dh, 8),
+          x.data_ptr(), _ld(x, 8), W.data_ptr(), _ld(W, 8), _act(act), kept.data_ptr(),
           _ld(kept, 16), _ptr(dx), 0 if dx is None else _ld(dx, 8), _ptr(dw),
           0 if dw is None else _ld(dw, 8), _TYPES[dw_dtype], _ptr(work), nbytes)
     return dx, dw

@@ -22,12 +22,18 @@ constexpr int64_t kMaxIntK = 131071;  // 2^14 K stays below 2^31
 // each make passes of 256 * resident; a pass costs steps * step + tile (steps:
 // K-steps of a workgroup's wave group; tile: first loads and epilogue), a last
 // pass with a fraction f of its workgroups part + (1 - part) * f of that; the
-// whole takes at least as long as reading B.  Fitted to 483 products (M 1 to
-// 4096, B from 512 x 1024 to 28672 x 4096, integers plain and gated, bf16
-// gated), each timed in the shapes that were in question; its choice ran within
-// 2.4 % of the fastest of them (geometric mean; 35 % at worst).  gated_model.py
-// holds the same model, the sweep, its times and the fit, which gives these
-// constants.
+// whole takes at least as long as reading B.  Where the last pass would be part
+// empty, the columns that fill whole passes may go to one shape and the rest to
+// a second launch, if the model finds that 7 % cheaper, 2.5 us for the launch
+// counted (the model's error is about that: of 10002 rows of B in bf16 2048 rows
+// of A took 97 us in two launches and 112 in one, but 777 rows, which a margin of
+// 3 % splits too, 63 and 53).
+//
+// Fitted to 483 products (M 1 to 4096, B from 512 x 1024 to 28672 x 4096,
+// integers plain and gated, bf16 gated), each timed in the shapes that were in
+// question; its choice ran within 2.4 % of the fastest of them (geometric mean;
+// 35 % at worst).  gated_model.py holds the same model, the sweep, its times and
+// the fit, which gives these constants.
 struct Cost {
   float step, tile, part, base;  // us, us, share, us
 };

@@ -119,8 +119,12 @@ GradPlan plan_of(const char* config, const GradShape& x, const GradShape& w) {
     const long sw = strtol(end + 2, &end, 10);
     if (*end || sx < 1 || sx > 64 || sw < 1 || sw > 64) continue;
     p = GradPlan{&t, even_splits(steps_of(x), sx), even_splits(steps_of(w), sw)};
-    // (a grid holds fewer than 2^32 threads)
-    if (tiles_of(t, x) * p.split_x + tiles_of(t, w) * p.split_w >= 2 * k2G / t.threads - 8)
+    // (a grid holds fewer than 2^32 threads: of the products, and of the sums,
+    // 1024 columns a workgroup of 256)
+    const int64_t sums = (p.split_x > 1 ? part_floats(x) / 1024 + 1 : 0) +
+                         (p.split_w > 1 ? part_floats(w) / 1024 + 1 : 0);
+    if (tiles_of(t, x) * p.split_x + tiles_of(t, w) * p.split_w >= 2 * k2G / t.threads - 8 ||
+        sums >= 2 * k2G / 256)
       p.tile = nullptr;
   }
   return p;
@@ -135,7 +139,7 @@ int64_t plan_bytes(const GradPlan& p, const GradShape& x, const GradShape& w) {
 bool runs(const GradShape& p, bool a_rows_m, int64_t lda, int64_t ldb) {
   for (const GradTile& t : kTiles)
     if ((a_rows_m ? t.bm : 64) * lda * 2 >= kRangeLimit || 64 * ldb * 2 >= kRangeLimit ||
-        tiles_of(t, p) >= k2G / t.threads)
+        tiles_of(t, p) >= k2G / t.threads - 8)
       return false;
   return true;
 }
@@ -319,10 +323,11 @@ size_t gemm_gated_backward_work_size(const char* config, int64_t M, int64_t F, i
   return n < 0 ? 0 : (size_t)(gemm::gate_bytes(M, F) + n);
 }
 
-int gemm_gated_backward_ex(const char* config, int type, int64_t M, int64_t F, int64_t K, const void* dH, int64_t lddh,
-                        const void* X, int64_t ldx, const void* W, int64_t ldw, int act,
-                        const void* kept, int64_t ld_kept, void* dX, int64_t lddx, void* dW,
-                        int64_t lddw, int dw_type, void* work, size_t work_bytes, void* stream) {
+int gemm_gated_backward_ex(const char* config, int type, int64_t M, int64_t F, int64_t K,
+                           const void* dH, int64_t lddh, const void* X, int64_t ldx, const void* W,
+                           int64_t ldw, int act, const void* kept, int64_t ld_kept, void* dX,
+                           int64_t lddx, void* dW, int64_t lddw, int dw_type, void* work,
+                           size_t work_bytes, void* stream) {
   using namespace gemm;
   if (M < 0 || F < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
   if (type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return GEMM_ERR_INVALID_ARG;
@@ -331,17 +336,18 @@ int gemm_gated_backward_ex(const char* config, int type, int64_t M, int64_t F, i
   const int64_t Fp = up8(F < k2G ? F : k2G), kept_f = (Fp + 15) / 16 * 16;
   // (a workgroup of 256 for 2048 values of dGU: a grid holds fewer than 2^32 threads)
   if (size_refused(M, F, K) || (M > 0 && Fp / 8 >= 2 * k2G / M) || lddh >= kStrideLimit ||
-      ldx >= kStrideLimit || ldw >= kStrideLimit || ld_kept >= kStrideLimit || lddx >= kStrideLimit ||
-      lddw >= kStrideLimit)
+      ldx >= kStrideLimit || ldw >= kStrideLimit || ld_kept >= kStrideLimit ||
+      lddx >= kStrideLimit || lddw >= kStrideLimit)
     return GEMM_ERR_UNSUPPORTED;
   const bool has_x = dX && M > 0 && K > 0, has_w = dW && F > 0 && K > 0;
-  if (lddh < F || ld_kept < 6 * kept_f || (dX && (ldw < K || lddx < K)) || (dW && (ldx < K || lddw < K)))
+  if (lddh < F || ld_kept < 6 * kept_f || (dX && (ldw < K || lddx < K)) ||
+      (dW && (ldx < K || lddw < K)))
     return GEMM_ERR_INVALID_ARG;
   if ((has_x || has_w) && M > 0 && F > 0 && (!dH || !kept || (has_x && !W) || (has_w && !X)))
     return GEMM_ERR_INVALID_ARG;
   if (misaligned(dH, 16) || misaligned(X, 16) || misaligned(W, 16) || misaligned(kept, 16) ||
-      misaligned(dX, 16) || misaligned(dW, 16) || misaligned(work, 16) || (lddh & 7) || (ld_kept & 15) ||
-      (dX && ((ldw | lddx) & 7)) || (dW && ((ldx | lddw) & 7)))
+      misaligned(dX, 16) || misaligned(dW, 16) || misaligned(work, 16) || (lddh & 7) ||
+      (ld_kept & 15) || (dX && ((ldw | lddx) & 7)) || (dW && ((ldx | lddw) & 7)))
     return GEMM_ERR_MISALIGNED;
   const GradShape px = has_x ? gated_input_shape(M, F, K) : kNoProduct;
   const GradShape pw = has_w ? gated_weight_shape(M, F, K) : kNoProduct;

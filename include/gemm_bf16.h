@@ -452,8 +452,9 @@ size_t gemm_work_size(int type, int64_t M, int64_t N, int64_t K);
  * and SB (N) contiguous; A and B 16-byte aligned with lda and ldb multiples of
  * 16, C 16-byte aligned with ldc a multiple of 8, scales 4-byte aligned.  Any
  * M, N, K >= 0; K == 0 sets C to zeros (times the scales).  Elements past K in
- * a row are not used whatever they hold.  Scales may be any fp32 value.  Limits
- * of rows and grids, streams and errors as for gemm_fp8; no workspace. */
+ * a row are not used whatever they hold.  Scales may be any fp32 value.  C must
+ * not overlap an input (here and in the calls below that write one).  Limits of
+ * rows and grids, streams and errors as for gemm_fp8; no workspace. */
 int gemm_i8(int64_t M, int64_t N, int64_t K,
             const void* A, int64_t lda, const float* SA,
             const void* B, int64_t ldb, const float* SB,
@@ -577,9 +578,9 @@ const char* gemm_backward_config_name(int64_t M, int64_t N, int64_t K);
  *   dX (M x K) = dG W_g + dU W_u     dW (2 F x K) = [dG^T X; dU^T X]
  *
  * dG and dU are rounded to `type` before the two products; sums are fp32, in an
- * order fixed by the sizes.  dX or dW may be NULL.  Rows of dH are read up to F rounded up to a multiple of 8
- * (within lddh).  The rest, and `work`, as for gemm_backward; F is below 2^29,
- * and M * ceil(F / 8) below 2^32. */
+ * order fixed by the sizes.  dX or dW may be NULL.  Rows of dH are read up to F
+ * rounded up to a multiple of 8 (within lddh).  The rest, and `work`, as for
+ * gemm_backward; F is below 2^29, and M * ceil(F / 8) below 2^32. */
 int gemm_gated_backward(int type, int64_t M, int64_t F, int64_t K,
                         const void* dH, int64_t lddh, const void* X, int64_t ldx,
                         const void* W, int64_t ldw, int act,

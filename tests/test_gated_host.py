@@ -215,6 +215,10 @@ def test_workspaces(g):
     assert g.backward_work_size(100, 200, 300, "b256x256_k9_k2") == 4 * (4 * 100 + 2 * 200) * 300
     assert g.backward_work_size(100, 200, 300, "nope") == 0
     assert g.gated_backward_work_size(100, 200, 300, "nope") == 0
+    # sums of 2^36 floats are more than a grid holds; unsplit they are none
+    assert g.backward_work_size(1 << 29, 128, 128, "b256x256_k2_k1") == 0
+    assert backward(g, M=1 << 29, N=128, K=128, lddc=128, lda=128, ldb=128, ldda=128, lddb=128,
+                    dB=NUL, nbytes=1 << 62, config=b"b256x256_k2_k1") == 3
 
 
 def test_empty_calls_launch_nothing(g):

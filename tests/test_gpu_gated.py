@@ -467,6 +467,34 @@ def test_a_layer_forward_and_backward(M, F, K, N, t):
     check_gated_backward(dx, dw1, dh.cpu(), x, w1, kept, "swiglu", t, "f32")
 
 
+@pytest.mark.parametrize("M, F, K, N", [(0, 8, 9, 10), (5, 0, 9, 10), (5, 8, 0, 10), (5, 8, 9, 0),
+                                        (0, 0, 0, 0)])
+def test_layers_without_rows_or_columns(M, F, K, N):
+    """Sums of nothing are zeros, in y and in every gradient."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    def some(*shape):
+        return torch.ones(*shape, device="cuda", dtype=torch.bfloat16)
+
+    x, w1, w2 = dev(some(M, K).cpu()), dev(some(2 * F, K).cpu()), dev(some(N, F).cpu())
+    y, h, kept = g.gated_mlp(x, w1, w2, save=True)
+    assert y.shape == (M, N) and h.shape == (M, F)
+    if F == 0 or K == 0:
+        assert (y == 0).all() and (h == 0).all()
+    dx, dw1, dw2 = g.gated_mlp_backward(dev(some(M, N).cpu()), x, w1, w2, h, kept,
+                                          dw_dtype=torch.float32)
+    assert dx.shape == x.shape and dw1.shape == w1.shape and dw2.shape == w2.shape
+    if M == 0 or N == 0:
+        assert (dx == 0).all() and (dw1 == 0).all() and (dw2 == 0).all()
+    q, s = g.quantize_int8(some(2 * F, K)), g.quantize_int8(some(N, F))
+    y = g.gated_mlp_int8(x, *q, *s)
+    assert y.shape == (M, N)
+    if F == 0 or K == 0:
+        assert (y == 0).all()
+
+
 def test_a_layer_in_8_bit_integers():
     """Bit for bit the three operators in a row, and near the layer over the
     real weights: codes are off by half a step, 1/254 of a row's largest value,
