@@ -338,61 +338,87 @@ __device__ __forceinline__ float gate(float g, float u, bool geglu) {
   }
 }
 
+// Where a wave's sums lie in its tile.  kQuads: quad (i, j) is row i * 16 + lane
+// % 16, columns (wn * FN + j) * 16 + 4 (lane / 16) .. + 3.  kHalves (of gated
+// tiles whose waves hold an odd number of fragments, see finish_gated): row (2 i
+// + lane / 32) * 16 + lane % 16, columns (wn * FN + j) * 8 + 4 (lane / 16 % 2) ..
+// + 3.
+enum : int { kQuads = 0, kHalves = 1 };
+template <int PLACE, int FN>
+struct Place {
+  __device__ static int row(int i, int lane) {
+    return (PLACE == kHalves ? 2 * i + (lane >> 5) : i) * 16 + (lane & 15);
+  }
+  __device__ static int quad(int wn, int j, int lane) {  // column / 4
+    return PLACE == kHalves ? (wn * FN + j) * 2 + (lane >> 4 & 1) : (wn * FN + j) * 4 + (lane >> 4);
+  }
+};
+
+// Byte offset of 16-byte piece c of row r, rows of PIECES pieces staged in LDS:
+// XORed with the bits of the row that tell apart rows of one 256-byte stretch of
+// banks.
+template <int PIECES>
+__device__ __forceinline__ uint32_t staged_at(int r, int c) {
+  constexpr int kGroup = (PIECES & -PIECES) < 16 ? PIECES & -PIECES : 16;
+  constexpr int kShift = kGroup == 16 ? 0 : kGroup == 8 ? 1 : kGroup == 4 ? 2 : kGroup == 2 ? 3 : 4;
+  return (uint32_t)((r * PIECES + (c ^ ((r >> kShift) & (kGroup - 1)))) << 4);
+}
+
 // A workgroup's BM x COLS values, staged in LDS by rows and stored in whole
 // 16-byte pieces, COLS * size bytes of a row by consecutive lanes.  Waves with
-// `mine` write v[i][j]: row wm * WAVE_M + i * 16 + lane % 16, columns (wn * FN +
-// j) * 16 + 4 (lane / 16) .. + 3.  Every wave of the workgroup calls it; the
-// LDS region is free when it is called and in use when it returns.
-template <int BM, int COLS, int THREADS, int OUT, int FM, int FN>
+// `mine` write the quads v[i][j] of their WAVE_M rows (see Place), in PASSES of
+// FM / PASSES of them where the rows do not fit the region at once.  Every wave
+// of the workgroup calls it; the LDS region is free when it is called and in use
+// when it returns.
+template <int BM, int WAVE_M, int COLS, int THREADS, int OUT, int PLACE, int PASSES, int FM, int FN>
 __device__ __forceinline__ void store_staged(lds_u8* region, const f32x4 (&v)[FM][FN], bool mine,
                                              int wm, int wn, int lane, void* out, int64_t ld,
                                              int m0, int m_end, int n0, int N) {
-  constexpr int kE = OUT == kStoreF32 ? 4 : 2, kPer = 16 / kE;
-  constexpr int kRB = COLS * kE, kChunks = kRB / 16;
-  constexpr int kMask = kChunks < 16 ? kChunks - 1 : 15;
-  static_assert(kChunks >= 4 && (kChunks & (kChunks - 1)) == 0, "a power of two");
-  static_assert(THREADS % kChunks == 0, "whole rows a pass");
-  // rows of 64 and 128 bytes: the bits of the row that tell rows of one
-  // 256-byte stretch of banks from another
-  auto at = [](int r, int c) {
-    const int sw = kChunks >= 16 ? r : kChunks == 8 ? r >> 1 : r >> 2;
-    return (uint32_t)(r * kRB + ((c ^ (sw & kMask)) << 4));
-  };
-  if (mine) {
+  constexpr int kE = OUT == kStoreF32 ? 4 : 2, kPer = 16 / kE, kPieces = COLS / kPer;
+  constexpr int kRows = BM / PASSES, kWaveRows = WAVE_M / PASSES, kQ = FM / PASSES;
+  static_assert(FM % PASSES == 0, "whole passes");
+  using At = Place<PLACE, FN>;
 #pragma unroll
-    for (int i = 0; i < FM; ++i) {
-      const int r = (wm * FM + i) * 16 + (lane & 15);
+  for (int pass = 0; pass < PASSES; ++pass) {
+    if (pass > 0) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    if (mine) {
 #pragma unroll
-      for (int j = 0; j < FN; ++j) {
-        const int q = (wn * FN + j) * 4 + (lane >> 4);  // column / 4
-        if constexpr (kE == 4)
-          *(__attribute__((address_space(3))) f32x4*)(region + at(r, q)) = v[i][j];
-        else
-          *(__attribute__((address_space(3))) u32x2*)(region + at(r, q >> 1) + ((q & 1) << 3)) =
-              pack_quad<OUT>(v[i][j]);
+      for (int i = 0; i < kQ; ++i) {
+        const int r = wm * kWaveRows + At::row(i, lane);
+#pragma unroll
+        for (int j = 0; j < FN; ++j) {
+          const int q = At::quad(wn, j, lane);
+          const f32x4& x = v[pass * kQ + i][j];
+          if constexpr (kE == 4)
+            *(__attribute__((address_space(3))) f32x4*)(region + staged_at<kPieces>(r, q)) = x;
+          else
+            *(__attribute__((address_space(3))) u32x2*)(region + staged_at<kPieces>(r, q >> 1) +
+                                                        ((q & 1) << 3)) = pack_quad<OUT>(x);
+        }
       }
     }
-  }
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  const int c = (int)threadIdx.x % kChunks, col = n0 + c * kPer;
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 #pragma unroll
-  for (int r0 = 0; r0 < BM; r0 += THREADS / kChunks) {
-    const int r = r0 + (int)threadIdx.x / kChunks;
-    if (BM % (THREADS / kChunks) != 0 && r >= BM) break;
-    const u32x4 x = *(const lds_u32x4*)(region + at(r, c));
-    if (m0 + r >= m_end || col >= N) continue;
-    uint8_t* dst = (uint8_t*)out + ((int64_t)(m0 + r) * ld + col) * kE;
-    if (col + kPer <= N) {
-      __builtin_nontemporal_store(x, (u32x4*)dst);
-      continue;
-    }
+    for (int p0 = 0; p0 < kRows * kPieces; p0 += THREADS) {
+      const int p = p0 + (int)threadIdx.x;
+      if (kRows * kPieces % THREADS != 0 && p >= kRows * kPieces) break;
+      const int r = p / kPieces, c = p % kPieces, col = n0 + c * kPer;
+      const int m = m0 + r / kWaveRows * WAVE_M + pass * kWaveRows + r % kWaveRows;
+      const u32x4 x = *(const lds_u32x4*)(region + staged_at<kPieces>(r, c));
+      if (m >= m_end || col >= N) continue;
+      uint8_t* dst = (uint8_t*)out + ((int64_t)m * ld + col) * kE;
+      if (col + kPer <= N) {
+        __builtin_nontemporal_store(x, (u32x4*)dst);
+        continue;
+      }
 #pragma unroll
-    for (int e = 0; e < kPer; ++e) {
-      if (col + e >= N) break;
-      if constexpr (kE == 4)
-        ((uint32_t*)dst)[e] = x[e];
-      else
-        ((uint16_t*)dst)[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+      for (int e = 0; e < kPer; ++e) {
+        if (col + e >= N) break;
+        if constexpr (kE == 4)
+          ((uint32_t*)dst)[e] = x[e];
+        else
+          ((uint16_t*)dst)[e] = (uint16_t)(x[e >> 1] >> (16 * (e & 1)));
+      }
     }
   }
 }
@@ -421,45 +447,39 @@ __device__ __forceinline__ float kept_value(uint32_t high, uint32_t third) {
 
 // A workgroup's g (up 0) or u (up 1) into `kept`, staged as store_staged
 // stages H.  The planes' rows are padded, so pieces are stored whole.
-template <int BM, int COLS, int THREADS, int FM, int FN>
+template <int BM, int COLS, int THREADS, int PLACE, int FM, int FN>
 __device__ __forceinline__ void store_kept(lds_u8* region, const BlockArgs& a,
-                                           const f32x4 (&acc)[FM][2 * FN], int up, bool mine,
-                                           int wm, int wn, int lane, int m0, int m_end, int f0) {
-  // 16-byte piece c of row r, rows of 2^LOG pieces
-  auto at = [](int r, int c, auto log) {
-    constexpr int kLog = decltype(log)::value;
-    const int sw = (r >> (kLog >= 4 ? 0 : 4 - kLog)) & ((1 << (kLog > 4 ? 4 : kLog)) - 1);
-    return (uint32_t)((r << (kLog + 4)) + ((c ^ sw) << 4));
-  };
-  constexpr int kLogHigh = COLS == 128 ? 4 : COLS == 64 ? 3 : 2;
-  static_assert(COLS == 8 << kLogHigh, "32, 64 or 128 columns");
-  const std::integral_constant<int, kLogHigh> high{};
-  const std::integral_constant<int, kLogHigh - 1> third{};
+                                           const f32x4 (&v)[FM][FN], int up, bool mine, int wm,
+                                           int wn, int lane, int m0, int m_end, int f0) {
+  constexpr int kWaveM = (PLACE == kHalves ? 32 : 16) * FM;
+  using At = Place<PLACE, FN>;
+  const std::integral_constant<int, COLS / 8> high{};
+  const std::integral_constant<int, COLS / 16> third{};
   lds_u8* const region3 = region + BM * COLS * 2;
   if (mine) {
 #pragma unroll
     for (int i = 0; i < FM; ++i) {
-      const int r = (wm * FM + i) * 16 + (lane & 15);
+      const int r = wm * kWaveM + At::row(i, lane);
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const int q = (wn * FN + j) * 4 + (lane >> 4);  // column / 4
-        const f32x4& v = acc[i][2 * j + up];
-        *(__attribute__((address_space(3))) u32x2*)(region + at(r, q >> 1, high) + ((q & 1) << 3)) =
-            kept_high(v);
-        *(__attribute__((address_space(3))) uint32_t*)(region3 + at(r, q >> 2, third) +
-                                                       ((q & 3) << 2)) = kept_third(v);
+        const int q = At::quad(wn, j, lane);
+        *(__attribute__((address_space(3))) u32x2*)(region + staged_at<COLS / 8>(r, q >> 1) +
+                                                    ((q & 1) << 3)) = kept_high(v[i][j]);
+        *(__attribute__((address_space(3))) uint32_t*)(region3 + staged_at<COLS / 16>(r, q >> 2) +
+                                                       ((q & 3) << 2)) = kept_third(v[i][j]);
       }
     }
   }
   asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  auto rows = [&](auto log, const lds_u8* from, int per, int64_t plane, int bytes) {
-    constexpr int kPieces = 1 << decltype(log)::value, kRows = THREADS / kPieces;
-    const int c = (int)threadIdx.x % kPieces, col = f0 + c * per;
+  auto rows = [&](auto pieces, const lds_u8* from, int per, int64_t plane, int bytes)
+      __attribute__((always_inline)) {
+    constexpr int kPieces = decltype(pieces)::value;
 #pragma unroll
-    for (int r0 = 0; r0 < BM; r0 += kRows) {
-      const int r = r0 + (int)threadIdx.x / kPieces;
-      if (BM % kRows != 0 && r >= BM) break;
-      const u32x4 x = *(const lds_u32x4*)(from + at(r, c, log));
+    for (int p0 = 0; p0 < BM * kPieces; p0 += THREADS) {
+      const int p = p0 + (int)threadIdx.x;
+      if (BM * kPieces % THREADS != 0 && p >= BM * kPieces) break;
+      const int r = p / kPieces, c = p % kPieces, col = f0 + c * per;
+      const u32x4 x = *(const lds_u32x4*)(from + staged_at<kPieces>(r, c));
       if (m0 + r < m_end && col < a.N)
         __builtin_nontemporal_store(
             x, (u32x4*)(a.kept + (int64_t)(m0 + r) * a.ld_kept + plane +
@@ -471,36 +491,65 @@ __device__ __forceinline__ void store_kept(lds_u8* region, const BlockArgs& a,
 }
 
 // H = act(g) * u (rounded once, from the unrounded sums) and, where asked
-// for, g and u to `kept`.  Waves with `mine` hold the sums, g in the even
-// fragments of their columns and u in the odd ones.
+// for, g and u to `kept`.  Waves with `mine` hold the sums: with an even number
+// of fragments of B, g in the even ones and u in the odd ones; else g in the
+// first eight rows of each and u in the other eight, of which two fragments'
+// halves are exchanged, so that a lane again holds both of an element.
 template <typename Cfg, int OP, int OUT, int THREADS>
 __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
                                              f32x4 (&acc)[Cfg::kFragM][Cfg::kFragN], int m0,
                                              int m_end, int f0, int wm, int wn, int lane,
                                              bool mine) {
-  constexpr int FM = Cfg::kFragM, FN = Cfg::kFragN / 2, BM = Cfg::kBM, COLS = Cfg::kBN / 2;
-  f32x4 h[FM][FN];
+  constexpr int PLACE = Cfg::kFragN % 2 == 0 ? kQuads : kHalves;
+  constexpr int FM = PLACE == kHalves ? Cfg::kFragM / 2 : Cfg::kFragM;
+  constexpr int FN = PLACE == kHalves ? Cfg::kFragN : Cfg::kFragN / 2;
+  constexpr int BM = Cfg::kBM, COLS = Cfg::kBN / 2;
+  using At = Place<PLACE, FN>;
+  f32x4 g[FM][FN], u[FM][FN], h[FM][FN];
   if (mine) {
+#pragma unroll
+    for (int i = 0; i < FM; ++i)
+#pragma unroll
+      for (int j = 0; j < FN; ++j) {
+        if constexpr (PLACE == kHalves) {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            // (copies: the compiler casts the bits of a vector's first element
+            // whichever one is named)
+            const float first = acc[2 * i][j][r], second = acc[2 * i + 1][j][r];
+            const u32x2 x = __builtin_bit_cast(
+                u32x2, __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, first),
+                                                        __builtin_bit_cast(uint32_t, second),
+                                                        false, false));
+            const uint32_t bits_g = x[0], bits_u = x[1];
+            g[i][j][r] = __builtin_bit_cast(float, bits_g);
+            u[i][j][r] = __builtin_bit_cast(float, bits_u);
+          }
+        } else {
+          g[i][j] = acc[i][2 * j];
+          u[i][j] = acc[i][2 * j + 1];
+        }
+      }
     if constexpr (OP == kOpI8) {
       f32x4 sg[FN], su[FN];
 #pragma unroll
       for (int j = 0; j < FN; ++j) {
-        const int f = f0 + (wn * FN + j) * 16 + 4 * (lane >> 4);
+        const int f = f0 + At::quad(wn, j, lane) * 4;
         sg[j] = column_scales(a.SB, f, a.N);
         su[j] = column_scales(a.SB + a.up_sb, f, a.N);
       }
 #pragma unroll
       for (int i = 0; i < FM; ++i) {
-        const int m = m0 + (wm * FM + i) * 16 + (lane & 15);
+        const int m = m0 + wm * Cfg::kWaveM + At::row(i, lane);
         const float sa = m < m_end ? a.SA[m] : 0.0f;
 #pragma unroll
         for (int j = 0; j < FN; ++j) {
-          const i32x4 g = __builtin_bit_cast(i32x4, acc[i][2 * j]);
-          const i32x4 u = __builtin_bit_cast(i32x4, acc[i][2 * j + 1]);
+          const i32x4 ig = __builtin_bit_cast(i32x4, g[i][j]);
+          const i32x4 iu = __builtin_bit_cast(i32x4, u[i][j]);
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            acc[i][2 * j][r] = (float)g[r] * sa * sg[j][r];
-            acc[i][2 * j + 1][r] = (float)u[r] * sa * su[j][r];
+            g[i][j][r] = (float)ig[r] * sa * sg[j][r];
+            u[i][j][r] = (float)iu[r] * sa * su[j][r];
           }
         }
       }
@@ -512,8 +561,7 @@ __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
 #pragma unroll
         for (int j = 0; j < FN; ++j)
 #pragma unroll
-          for (int r = 0; r < 4; ++r)
-            h[i][j][r] = gate<OUT>(acc[i][2 * j][r], acc[i][2 * j + 1][r], geglu);
+          for (int r = 0; r < 4; ++r) h[i][j][r] = gate<OUT>(g[i][j][r], u[i][j][r], geglu);
     };
     if (a.geglu != 0)
       gates(true);
@@ -522,15 +570,14 @@ __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
   }
   // every wave is done with the ring
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-  store_staged<BM, COLS, THREADS, OUT>(region, h, mine, wm, wn, lane, a.C, a.ldc, m0, m_end, f0,
-                                       a.N);
+  store_staged<BM, Cfg::kWaveM, COLS, THREADS, OUT, PLACE, 1>(region, h, mine, wm, wn, lane, a.C,
+                                                              a.ldc, m0, m_end, f0, a.N);
   if constexpr (OP != kOpI8) {
     if (a.kept != nullptr) {
-#pragma unroll
-      for (int up = 0; up < 2; ++up) {
-        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        store_kept<BM, COLS, THREADS, FM, FN>(region, a, acc, up, mine, wm, wn, lane, m0, m_end, f0);
-      }
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      store_kept<BM, COLS, THREADS, PLACE>(region, a, g, 0, mine, wm, wn, lane, m0, m_end, f0);
+      asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      store_kept<BM, COLS, THREADS, PLACE>(region, a, u, 1, mine, wm, wn, lane, m0, m_end, f0);
     }
   }
 }
@@ -547,7 +594,8 @@ __device__ __forceinline__ void finish_gated(const BlockArgs& a, lds_u8* region,
 // MODE kGated: a tile's BN rows of B are BN / 2 rows of the gate and the BN /
 // 2 of the same columns of the up projection, 16 and 16 in turn, so that a
 // wave holds g and u of one element of H in the same lane and register and
-// the activation costs no exchange.  NT: B's loads non-temporal, for one row
+// the activation costs no exchange (8 and 8 where a wave's fragments of B are
+// odd in number: one exchange between half waves then).  NT: B's loads non-temporal, for one row
 // of tiles, where no other workgroup reads the same B.
 //
 // LAYOUT kNN, kTN: an operand whose rows lie along K is staged in pieces of 64
@@ -599,7 +647,7 @@ __device__ __forceinline__ void block_tile(const BlockArgs& a, int block, lds_u8
   constexpr int NB = Tile::kScaleCols, SA = Tile::kRowScales, SS = Tile::kScaleSlots;
   constexpr int kInFlight = (S - 2) * (L + (kScaled ? 1 : 0));
   static_assert(RPI % 16 == 0, "the swizzle repeats every 16 rows");
-  static_assert(kScaleBlock % Cfg::kWaveN == 0, "a wave's columns share one scale");
+  static_assert(!kScaled || kScaleBlock % Cfg::kWaveN == 0, "a wave's columns share one scale");
   static_assert(SA / 64 <= W, "one wave loads 64 row scales");
   static_assert(kInFlight < 64, "vmcnt range");
 
@@ -643,7 +691,9 @@ __device__ __forceinline__ void block_tile(const BlockArgs& a, int block, lds_u8
   }
   constexpr bool kPairs = MODE == kGated;
   constexpr int kCols = kPairs ? BN / 2 : BN;  // columns of C
-  static_assert(!kPairs || (RPI % 32 == 0 && FN % 2 == 0), "16 and 16 rows of B in turn");
+  constexpr bool kEights = kPairs && FN % 2 != 0;  // 8 and 8 rows of B in turn, not 16 and 16
+  static_assert(!kPairs || (kEights ? RPI % 16 == 0 && FM % 2 == 0 && WK == 1 : RPI % 32 == 0),
+                "whole pairs");
   const int tn = in / gsz, n0 = tn * kCols;
   RowTile tile;
   if (a.offsets) {
@@ -663,7 +713,7 @@ __device__ __forceinline__ void block_tile(const BlockArgs& a, int block, lds_u8
                               : make_rsrc(a.A + (int64_t)m0 * a.lda, (uint32_t)(rows_a * a.lda));
   // (gated: a wave loads 8 rows at a time, all of the gate or all of the up
   // projection)
-  const int64_t up = kPairs ? ((wave >> 1) & 1) * a.up_b : 0;
+  const int64_t up = kPairs ? (kEights ? wave & 1 : (wave >> 1) & 1) * a.up_b : 0;
   const u32x4 rsrc_b = make_rsrc(a.B + tile.expert * a.stride_b + up + (int64_t)n0 * a.ldb,
                                  (uint32_t)(rows_b * a.ldb));
   const int r0 = tid / 8;
@@ -683,7 +733,7 @@ __device__ __forceinline__ void block_tile(const BlockArgs& a, int block, lds_u8
       const int src = row < rows_a ? (gather ? source_row(a, m0 + row) : row) : -1;
       voff[i] = src >= 0 ? (uint32_t)(src * (int)a.lda + chunk * 16) : kOOB;
     } else {
-      const int src = kPairs ? row / 32 * 16 + row % 16 : row;
+      const int src = kEights ? row / 16 * 8 + row % 8 : kPairs ? row / 32 * 16 + row % 16 : row;
       voff[i] = src < rows_b ? (uint32_t)(src * (int)a.ldb + chunk * 16) : kOOB;
     }
   }
@@ -1116,8 +1166,17 @@ __device__ __forceinline__ void block_tile(const BlockArgs& a, int block, lds_u8
     finish_gated<Cfg, OP, OUT, T>(a, smem, acc, m0, tile.end, n0, wm, wn, lane, true);
   } else {
     scale_sums<OP, FM, FN>(a, acc, tile.end, m0 + wm * Cfg::kWaveM, n0 + wn * Cfg::kWaveN, lane);
-    finish_tile<Cfg, OUT, false>(c, smem, wave, m0, n0, acc, m0 + wm * Cfg::kWaveM,
-                                 n0 + wn * Cfg::kWaveN, lane, 0);
+    if constexpr ((Cfg::kWaveN & (Cfg::kWaveN - 1)) != 0) {
+      // (a wave's rows are no power of two: staged by the workgroup)
+      constexpr int kPasses = BM * BN * (OUT == kStoreF32 ? 4 : 2) <= Cfg::kLdsBytes ? 1 : 2;
+      static_assert(BM * BN * (OUT == kStoreF32 ? 4 : 2) / kPasses <= Cfg::kLdsBytes, "fits the ring");
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+      store_staged<BM, Cfg::kWaveM, BN, T, OUT, kQuads, kPasses>(smem, acc, true, wm, wn, lane, a.C,
+                                                                 a.ldc, m0, tile.end, n0, a.N);
+    } else {
+      finish_tile<Cfg, OUT, false>(c, smem, wave, m0, n0, acc, m0 + wm * Cfg::kWaveM,
+                                   n0 + wn * Cfg::kWaveN, lane, 0);
+    }
   }
 }
 

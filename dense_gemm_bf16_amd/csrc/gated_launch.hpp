@@ -49,8 +49,8 @@ hipError_t launch_gated_tile(const BlockArgs& a, int grid, hipStream_t s, int op
                              bool gated, bool stream_b) {
   return by_gated_types(op, out, gated, [&](auto o, auto t, auto m) {
     constexpr int kOp = decltype(o)::value, kOut = decltype(t)::value, kMode = decltype(m)::value;
-    if constexpr (kMode == kGated && BN / WN / 16 % 2 != 0) {
-      return hipErrorInvalidValue;  // a wave holds whole pairs of fragments
+    if constexpr (kMode == kGated && BN / WN / 16 % 2 != 0 && BM / WM / 16 % 2 != 0) {
+      return hipErrorInvalidValue;  // a wave holds no whole pairs of fragments
     } else {
       const dim3 threads(WM * WN * WK * 64);
       if constexpr (BM <= 64) {
@@ -79,11 +79,16 @@ hipError_t launch_gated_row(const BlockArgs& a, int grid, hipStream_t s, int op,
   });
 }
 
+// The block products' tiles, and one between the two largest: its workgroups
+// fill a last pass that those of 256 x 256 would leave a third empty or more.
+#define GATED_TILES(X)               \
+  BLOCK_TILES(X)                     \
+  X(b256x192, 256, 192, 2, 4, 1, 2)
 #define GATED_DECLARE(NAME, A, B, C, D, E, S)                                                 \
   extern template hipError_t launch_gated_tile<A, B, C, D, E, S>(const BlockArgs&, int,       \
                                                                  hipStream_t, int, int, bool, \
                                                                  bool);
-BLOCK_TILES(GATED_DECLARE)
+GATED_TILES(GATED_DECLARE)
 #undef GATED_DECLARE
 // The row kernel's shapes here: X(name, fragments of A and of B, waves, steps
 // ahead, rows of B in a fragment).

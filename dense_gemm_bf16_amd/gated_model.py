@@ -50,6 +50,7 @@ SECOND_LAUNCH_US, SPLIT_GAIN = 2.5, 0.93
 # in the library's order, which decides ties
 SHAPES = {
     "b256x256": (256, 256, 1, 1),
+    "b256x192": (256, 192, 1, 1),
     "b256x128": (256, 128, 1, 1),
     "b128x128": (128, 128, 1, 2),
     "b128x128k2": (128, 128, 2, 1),

@@ -101,7 +101,7 @@ def test_library_picks_the_models_shape(gm):
             g.gated_config_name(g.GEMM_TYPE_I8 if size == 1 else g.GEMM_TYPE_F16, M, N, K)
         assert got == want, (kind, M, N, K)
         split += "+" in got
-    assert split > 50
+    assert split > 20
 
 
 def test_library_picks_near_the_models_plan(gm, records):

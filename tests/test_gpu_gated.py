@@ -9,7 +9,7 @@ from block_ref import HALF_STEP, TINY, U, check_rounded, dtype, padded
 
 pytestmark = pytest.mark.gpu
 
-GATED = ["b256x256", "b256x128", "b128x128", "b128x128k2", "b64x128k2", "b64x64", "b64x64k2",
+GATED = ["b256x256", "b256x192", "b256x128", "b128x128", "b128x128k2", "b64x128k2", "b64x64", "b64x64k2",
          "b32x128", "b32x64k4", "r16x16", "r16x8", "r32x16"]
 
 

@@ -10,7 +10,7 @@ from block_ref import check_rounded, dtype, padded
 
 pytestmark = pytest.mark.gpu
 
-CONFIGS = ["b256x256", "b256x128", "b128x128", "b128x128k2", "b64x128k2", "b64x64", "b64x64k2",
+CONFIGS = ["b256x256", "b256x192", "b256x128", "b128x128", "b128x128k2", "b64x128k2", "b64x64", "b64x64k2",
            "b32x128", "b32x64k4", "b32x32k4", "r16x16", "r16x8", "r32x16"]
 GATED = [c for c in CONFIGS if c != "b32x32k4"]
 
