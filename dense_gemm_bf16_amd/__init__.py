@@ -860,12 +860,14 @@ def quantize_int8(x):
     """8-bit integers and fp32 scales of x (M x K, bfloat16, float16 or
     float32), one scale for each row: (q, S), S of M entries, as matmul_int8
     takes them for tokens and, of a weight's rows, for channels.  q's rows are
-    padded to 16 bytes."""
+    padded to 16 bytes, from 1024 columns on to 128 (whole lines: 1 x 10240 x
+    4104 16.6 -> 13.5 us, 8192 rows 328 -> 290)."""
     _need(x, "x")
     if x.dim() != 2:
         raise ValueError("x must have two dimensions")
     M, K = x.shape
-    q = torch.empty(M, max(16, -(-K // 16) * 16), device=x.device, dtype=torch.int8)
+    unit = 128 if K >= 1024 else 16
+    q = torch.empty(M, max(16, -(-K // unit) * unit), device=x.device, dtype=torch.int8)
     S = torch.empty(M, device=x.device, dtype=torch.float32)
     _call(_lib.gemm_i8_quantize, x.device, M, K, x.data_ptr(), _ld(x, 1),
           _type(x.dtype, "x", _FLOATS), q.data_ptr(), q.shape[1], S.data_ptr())

@@ -28,6 +28,7 @@
 // TFLOP/s, the matrix cores 58 % busy; 1 x 8192 x 8192 12-13 us (memory); 64,
 // 128, 256 rows by 8192 x 8192 15, 20.5, 29 us (the L2: tile traffic of 13-15
 // TB/s when the lines come in from the fabric, whatever the ring's depth).
+// Rows that do not start on 128-byte lines cost 10-40 % where loads bound it.
 // Integers, without the FMAs of every step: 8192 x 10240 x 8192 501-571 us by
 // the clock (2400-2740 TOP/s, matrix cores 74 % busy), 128, 256 rows by 8192 x
 // 8192 17.8, 23.9 us.  Gated bf16, 8192 x 14336 x 4096: 1338-1368 us (1410-1440

@@ -68,8 +68,8 @@ hipError_t launch_quantize_int8(const Int8QuantArgs& a, int x_type, hipStream_t 
 struct GateGradArgs {
   const void* dH;       // M rows of F, read to F rounded up to 8
   const uint8_t* kept;  // M rows of what the forward call kept of g and u
-  void* dGU;            // M rows of dg (Fp) and du (Fp)
-  int64_t M, Fp, lddh, ld_kept, kept_f;
+  void* dGU;            // M rows of dg (the first Fp of ld columns) and du (of the next ld)
+  int64_t M, Fp, ld, lddh, ld_kept, kept_f;
   int geglu;
 };
 hipError_t launch_gate_grad(const GateGradArgs& a, bool half, hipStream_t s);

@@ -51,9 +51,9 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateGradArgs a) {
     du[j] = (T)(d * (g * s));
     dg[j] = (T)(d * u * __builtin_fmaf(c * dz, e * r * r, s));
   }
-  T* out = (T*)a.dGU + m * 2 * a.Fp + f;
+  T* out = (T*)a.dGU + m * 2 * a.ld + f;
   *(t8*)out = dg;
-  *(t8*)(out + a.Fp) = du;
+  *(t8*)(out + a.ld) = du;
 }
 
 // Four columns a thread; the parts' loads do not wait for one another.
