@@ -21,21 +21,22 @@ constexpr int64_t kMaxIntK = 131071;  // 2^14 K stays below 2^31
 // time makes cheapest.  `units` workgroups on CUs that hold `resident` of them
 // each make passes of 256 * resident; a pass costs steps * step + tile (steps:
 // K-steps of a workgroup's wave group; tile: first loads and epilogue), a last
-// pass with a fraction f of its workgroups part + (1 - part) * f of that; the
-// whole takes at least as long as reading B.  Where the last pass would be part
-// empty, the columns that fill whole passes may go to one shape and the rest to
-// a second launch, if the model finds that 7 % cheaper, 2.5 us for the launch
-// counted (the model's error is about that: of 10002 rows of B in bf16 2048 rows
-// of A took 97 us in two launches and 112 in one, but 777 rows, which a margin of
-// 3 % splits too, 63 and 53).
+// pass with a fraction f of its workgroups, up to n on a CU, part + stair * (n -
+// 1) / (resident - 1) + (1 - part - stair) * f of that (without the stair, 256
+// workgroups of a shape of which a CU holds four were taken to be 1.4 times as
+// slow as 128); the whole takes at least as long as reading B.  Where the last
+// pass would be part empty, the columns that fill whole passes may go to one
+// shape and the rest to a second launch, if the model finds that 4 % cheaper, 2.5
+// us for the launch counted.  (Of 70 products that might, those it finds 7 to 15 %
+// cheaper ran 9 % faster, 4 to 7 % 3 %, 2 to 4 % as fast.)
 //
-// Fitted to 483 products (M 1 to 4096, B from 512 x 1024 to 28672 x 4096,
-// integers plain and gated, bf16 gated), each timed in the shapes that were in
-// question; its choice ran within 2.1 % of the fastest of them (geometric mean;
-// 35 % at worst).  gated_model.py holds the same model, the sweep, its times and
-// the fit, which gives these constants.
+// Fitted to 591 products (M 1 to 4096, B from 512 x 1024 to 28672 x 4096 and down
+// to 128 bytes deep, integers plain and gated, bf16 gated), each timed in the
+// shapes that were in question; its choice ran within 1.2 % of the fastest of
+// them (geometric mean; 27 % at worst).  gated_model.py holds the same model, the
+// sweep, its times and the fit, which gives these constants.
 struct Cost {
-  float step, tile, part, base;  // us, us, share, us
+  float step, tile, part, stair, base;  // us, us, share, share, us
 };
 struct Shape {
   GatedConfig built;
@@ -47,41 +48,41 @@ const Shape kShapes[] = {
   {{#NAME, A, B, (C) * (D) * (E) * 64, (B) / (D) / 16 % 2 == 0 || (A) / (C) / 16 % 2 == 0, \
     &launch_gated_tile<A, B, C, D, E, S>}, E, RESIDENT, __VA_ARGS__},
     ROW(b256x256, 256, 256, 2, 4, 1, 2, 1,
-        {1.405f, 13.12f, 0.68f, 0.00f}, {1.349f, 12.76f, 0.79f, 0.00f})
+        {1.453f, 12.12f, 0.65f, 0.00f, 0.00f}, {1.418f, 8.37f, 0.80f, 0.00f, 0.00f})
     ROW(b256x192, 256, 192, 2, 4, 1, 2, 1,
-        {1.073f, 11.04f, 0.71f, 0.00f}, {1.127f, 10.44f, 0.71f, 0.00f})
+        {1.087f, 10.04f, 0.72f, 0.00f, 0.00f}, {1.155f, 7.06f, 0.72f, 0.00f, 1.29f})
     ROW(b256x128, 256, 128, 4, 2, 1, 3, 1,
-        {0.827f, 8.51f, 0.72f, 0.00f}, {0.865f, 7.13f, 0.76f, 0.00f})
+        {0.864f, 6.62f, 0.71f, 0.00f, 0.95f}, {0.891f, 4.29f, 0.76f, 0.00f, 1.49f})
     ROW(b128x128, 128, 128, 2, 2, 1, 2, 2,
-        {0.839f, 8.80f, 0.50f, 0.41f}, {0.900f, 6.83f, 0.53f, 0.00f})
+        {0.963f, 5.41f, 0.46f, 0.24f, 2.44f}, {1.012f, 2.61f, 0.48f, 0.26f, 2.87f})
     ROW(b128x128k2, 128, 128, 2, 2, 2, 2, 1,
-        {1.031f, 6.29f, 0.80f, 1.17f}, {1.070f, 5.99f, 0.84f, 0.42f})
+        {1.051f, 5.45f, 0.80f, 0.00f, 1.72f}, {1.091f, 4.07f, 0.84f, 0.00f, 1.90f})
     ROW(b64x128k2, 64, 128, 2, 2, 2, 3, 1,
-        {0.695f, 4.21f, 0.89f, 0.84f}, {0.753f, 3.57f, 0.88f, 0.61f})
+        {0.714f, 3.47f, 0.86f, 0.00f, 1.57f}, {0.761f, 2.45f, 0.85f, 0.00f, 1.94f})
     ROW(b64x64, 64, 64, 2, 2, 1, 4, 2,
-        {0.406f, 3.09f, 0.58f, 1.63f}, {0.419f, 2.58f, 0.60f, 1.56f})
+        {0.430f, 2.40f, 0.58f, 0.23f, 2.00f}, {0.449f, 1.55f, 0.60f, 0.31f, 2.28f})
     ROW(b64x64k2, 64, 64, 2, 2, 2, 4, 1,
-        {0.445f, 3.10f, 0.84f, 1.63f}, {0.462f, 2.65f, 0.86f, 1.98f})
+        {0.461f, 2.73f, 0.83f, 0.00f, 1.80f}, {0.471f, 2.33f, 0.87f, 0.00f, 1.99f})
     ROW(b32x128, 32, 128, 1, 4, 1, 3, 2,
-        {0.519f, 3.22f, 0.62f, 0.84f}, {0.597f, 0.00f, 0.56f, 2.30f})
+        {0.550f, 2.17f, 0.58f, 0.25f, 1.90f}, {0.589f, 1.16f, 0.57f, 0.27f, 2.23f})
     ROW(b32x64k4, 32, 64, 2, 2, 4, 3, 1,
-        {0.655f, 3.26f, 0.90f, 1.50f}, {0.694f, 3.06f, 0.88f, 1.85f})
+        {0.666f, 3.12f, 0.89f, 0.00f, 1.61f}, {0.699f, 2.92f, 0.88f, 0.00f, 1.86f})
     ROW(b32x32k4, 32, 32, 2, 2, 4, 4, 1,
-        {0.410f, 3.23f, 0.96f, 0.95f}, {0, 0, 0, 0})
+        {0.425f, 3.00f, 0.95f, 0.00f, 1.15f}, {0, 0, 0, 0, 0})
 #undef ROW
 #define ROW(NAME, A, B, C, D, E, RESIDENT, ...)                                             \
   {{#NAME, 16 * (A), (E) * (B), (C) * 64, true, &launch_gated_row<A, B, C, D, E>}, C, RESIDENT, \
    __VA_ARGS__},
     ROW(r16x16, 1, 1, 8, 4, 16, 4,
-        {3.204f, 2.43f, 0.16f, 2.23f}, {2.907f, 4.06f, 0.18f, 2.11f})
+        {3.922f, 0.00f, 0.22f, 0.61f, 2.59f}, {3.725f, 0.25f, 0.25f, 0.70f, 2.52f})
     ROW(r16x8, 1, 1, 8, 4, 8, 4,
-        {2.208f, 2.44f, 0.15f, 2.22f}, {2.229f, 3.09f, 0.13f, 2.49f})
+        {2.512f, 1.28f, 0.23f, 0.53f, 2.30f}, {2.544f, 1.27f, 0.21f, 0.52f, 2.60f})
     ROW(r32x16, 2, 1, 8, 4, 16, 4,
-        {3.375f, 3.91f, 0.24f, 1.71f}, {3.170f, 6.38f, 0.25f, 1.34f})
+        {4.322f, 0.00f, 0.25f, 0.49f, 2.55f}, {4.579f, 0.09f, 0.25f, 0.59f, 2.54f})
 #undef ROW
 };
 constexpr double kStreamMBPerUs = 6.3, kStreamBaseUs = 2.2;
-constexpr double kSecondLaunchUs = 2.5, kSplitGain = 0.93;
+constexpr double kSecondLaunchUs = 2.5, kSplitGain = 0.96;
 
 // A product as the choice sees it: rows of A and of B, bytes of a row and from
 // row to row, and whether B's rows are paired.
@@ -103,12 +104,13 @@ bool fits(const Shape& s, const Product& p, int64_t rows_b) {
 
 double model_time(const Shape& s, const Product& p, int64_t rows_b) {
   const Cost& c = p.ints ? s.ints : s.halves;
-  const double units =
-      (double)((p.M + s.built.bm - 1) / s.built.bm) * (double)tiles_n(s, rows_b);
-  const double pass = 256.0 * s.resident;
-  double passes = (double)(int64_t)(units / pass);
-  const double rest = units / pass - passes;
-  if (rest > 0) passes += c.part + (1 - c.part) * rest;
+  const int64_t units = (p.M + s.built.bm - 1) / s.built.bm * tiles_n(s, rows_b);
+  const int64_t pass = 256 * s.resident, rest = units % pass;
+  double passes = (double)(units / pass);
+  if (rest > 0)
+    passes += c.part +
+              c.stair * (double)((rest - 1) / 256) / (s.resident > 1 ? s.resident - 1 : 1) +
+              (1 - (double)c.part - c.stair) * (double)rest / (double)pass;
   const int64_t k_steps = (p.k_bytes + kStepBytes - 1) / kStepBytes;
   const double steps = (double)((k_steps + s.k_groups - 1) / s.k_groups);
   const double t = passes * (steps * c.step + c.tile) + c.base;

@@ -2,7 +2,7 @@
 gated products, and of tile and splits for the gradients.
 
 ``csrc/gated_api.hip`` runs the shape whose launch the first model finds
-cheapest (or two shapes side by side where that is 7 % cheaper),
+cheapest (or two shapes one after the other where that is 4 % cheaper),
 ``csrc/grad_api.hip`` the plan that the second finds cheapest.  This module
 holds the same models in Python, the sweeps that time every shape and plan on
 the GPU, and the fits of the models' constants to those times, so the constants
@@ -11,10 +11,11 @@ compiled into the library can be derived again and checked.
 Products (microseconds).  ``units`` workgroups run on CUs that hold
 ``resident`` of them each, in passes of 256 * resident.  A pass costs steps *
 step + tile (steps: 128-byte K-steps of a wave group; tile: first loads and
-epilogue); a last pass with a fraction f of its workgroups costs part + (1 -
-part) * f of that; a launch adds base.  Reading B at 6.3 TB/s (and 2.2 us) is a
-floor, joined as fourth powers.  Each shape has its four constants twice, for
-8-bit integers and for 16-bit types; a gated product counts B's rows, two for
+epilogue); a last pass with a fraction f of its workgroups, up to n of them on a
+CU, costs part + stair * (n - 1) / (resident - 1) + (1 - part - stair) * f of
+that; a launch adds base.  Reading B at 6.3 TB/s (and 2.2 us) is a floor, joined
+as fourth powers.  Each shape has its five constants twice, for 8-bit integers
+and for 16-bit types; a gated product counts B's rows, two for
 each of its columns.  Least squares on log time, each shape by itself, over the
 times within 2.5 of the product's fastest.
 
@@ -44,7 +45,7 @@ DATA = os.path.join(_HERE, "plan_model_data", "gated_shapes.json")
 CUS = 256
 STEP_BYTES = 128
 STREAM_MB_PER_US, STREAM_BASE_US = 6.3, 2.2
-SECOND_LAUNCH_US, SPLIT_GAIN = 2.5, 0.93
+SECOND_LAUNCH_US, SPLIT_GAIN = 2.5, 0.96
 
 # name -> (rows of A, rows of B, wave groups along K, workgroups a CU holds),
 # in the library's order, which decides ties
@@ -70,11 +71,12 @@ KINDS = {"i8": (1, False), "i8 gated": (1, True), "bf16 gated": (2, True)}
 
 
 def launch_us(constants, shape, M, rows_b, k_bytes) -> float:
-    step, tile, part, base = constants
+    step, tile, part, stair, base = constants
     bm, bn, groups, resident = SHAPES[shape]
-    passes, rest = divmod(-(-M // bm) * -(-rows_b // bn) / (CUS * resident), 1)
+    passes, rest = divmod(-(-M // bm) * -(-rows_b // bn), CUS * resident)
     if rest > 0:
-        passes += part + (1 - part) * rest
+        passes += part + stair * ((rest - 1) // CUS) / max(resident - 1, 1) + \
+            (1 - part - stair) * rest / (CUS * resident)
     steps = -(-(-(-k_bytes // STEP_BYTES)) // groups)
     t = passes * (steps * step + tile) + base
     floor = rows_b * k_bytes * 1e-6 / STREAM_MB_PER_US + STREAM_BASE_US
@@ -130,16 +132,17 @@ def fit(records):
             if len(rows) < 8:
                 continue
 
-            def of(v):
-                return abs(v[0]), abs(v[1]), min(abs(v[2]), 1.0), abs(v[3])
+            def of(v, many=SHAPES[shape][3] > 1):
+                part = min(abs(v[2]), 1.0)
+                return abs(v[0]), abs(v[1]), part, min(abs(v[4]), 1 - part) if many else 0.0, abs(v[3])
 
             def off(v):
                 return [w * (math.log(launch_us(of(v), shape, M, n, kb)) - us)
                         for M, n, kb, us, w in rows]
 
-            best = min((least_squares(off, x0) for x0 in (
-                (0.5, 3, 0.6, 2), (1.5, 6, 0.7, 2), (0.3, 1, 0.3, 2.5), (2.4, 1.1, 0.3, 3))),
-                       key=lambda z: z.cost)
+            best = min((least_squares(off, (*x0, stair)) for x0 in (
+                (0.5, 3, 0.6, 2), (1.5, 6, 0.7, 2), (0.3, 1, 0.3, 2.5), (2.4, 1.1, 0.3, 3))
+                        for stair in (0.2,)), key=lambda z: z.cost)
             out[size][shape] = of(best.x)
     return out
 
@@ -230,7 +233,8 @@ def search(records, start, rounds=2500, seed=1):
 # ------------------------------------------------------------------ timing
 
 SWEEP = [(N, K) for N, K in ((8192, 8192), (28672, 4096), (4096, 4096), (2048, 1024), (600, 1000),
-                             (10002, 2056), (1024, 8192), (1024, 4096), (512, 1024))]
+                             (10002, 2056), (1024, 8192), (1024, 4096), (512, 1024), (2000, 128),
+                            (9000, 320))]
 SWEEP_M = (1, 6, 16, 24, 32, 48, 64, 100, 128, 200, 256, 400, 512, 777, 1024, 1500, 2048, 4096)
 SWEEP_GRADS = [(1000, 1365, 520), (100, 2000, 700), (8192, 1024, 1024), (2048, 2048, 1024),
                (512, 5001, 2055), (4096, 2048, 512), (16, 4096, 2048), (1, 1000, 1000),
@@ -371,7 +375,8 @@ def main(argv=None) -> int:
     for size, by in constants.items():
         print("8-bit integers" if size == 1 else "16-bit types")
         for shape, c in by.items():
-            print(f"  {shape:12s} step {c[0]:.3f} tile {c[1]:.2f} part {c[2]:.2f} base {c[3]:.2f}")
+            print(f"  {shape:12s} step {c[0]:.3f} tile {c[1]:.2f} part {c[2]:.2f} "
+                  f"stair {c[3]:.2f} base {c[4]:.2f}")
     quality = choice_quality(constants, data["products"])
     for kind in KINDS:
         q = [v for v, k in quality if k == kind]

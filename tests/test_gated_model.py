@@ -35,14 +35,14 @@ def compiled(gm):
     """{bytes: {shape: constants}} as written in gated_api.hip."""
     text = open(os.path.join(CSRC, "gated_api.hip")).read()
     number = r"([\d.]+)f?"
-    four = r"\{%s, %s, %s, %s\}" % ((number,) * 4)
-    rows = re.findall(r"ROW\((\w+), [^{]*?(\d+),\s*%s, %s\)" % (four, four), text)
+    five = r"\{%s, %s, %s, %s, %s\}" % ((number,) * 5)
+    rows = re.findall(r"ROW\((\w+), [^{]*?(\d+),\s*%s, %s\)" % (five, five), text)
     out = {1: {}, 2: {}}
     for name, resident, *c in rows:
         assert gm.SHAPES[name][3] == int(resident), name
-        out[1][name] = tuple(float(v) for v in c[:4])
+        out[1][name] = tuple(float(v) for v in c[:5])
         if name != gm.NOT_GATED:  # 16-bit products are gated ones
-            out[2][name] = tuple(float(v) for v in c[4:])
+            out[2][name] = tuple(float(v) for v in c[5:])
     return out
 
 
@@ -56,12 +56,12 @@ def compiled_gradients():
 
 
 def test_compiled_constants_are_the_fit(gm, records):
-    assert len(records["products"]) == 483
+    assert len(records["products"]) == 591
     fitted, written = gm.fit(records["products"]), compiled(gm)
     for size in (1, 2):
         assert list(written[size]) == list(fitted[size])
         for shape, c in written[size].items():
-            for digits, a, b in zip((3, 2, 2, 2), fitted[size][shape], c):
+            for digits, a, b in zip((3, 2, 2, 2, 2), fitted[size][shape], c):
                 assert abs(a - b) <= 0.75 * 10 ** -digits, (size, shape, fitted[size][shape], c)
 
 
@@ -69,7 +69,7 @@ def test_choices_are_near_the_fastest(gm, records):
     quality = gm.choice_quality(compiled(gm), records["products"])
     for kind in gm.KINDS:
         q = [v for v, k in quality if k == kind]
-        assert len(q) == 161 and gm.geomean(q) < 1.026 and max(q) < 1.4
+        assert len(q) == 197 and gm.geomean(q) < 1.015 and max(q) < 1.35
     q = gm.grad_quality(compiled_gradients(), records["gradients"])
     assert len(q) == 92 and gm.geomean(q) < 1.0115 and max(q) < 1.2
 

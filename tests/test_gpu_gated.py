@@ -97,6 +97,25 @@ def test_gated_automatic_shapes(M, F, K):
         assert np.array_equal(f64(alone), f64(h))  # keeping g and u changes nothing
 
 
+@pytest.mark.parametrize("M, F, K", [(2507, 3315, 6400), (985, 8385, 2560), (3055, 2749, 2176)])
+def test_two_launches(M, F, K):
+    """Products whose last columns run in a second shape: sums of small integers
+    are exact, so h, g and u are bit for bit what one shape gives."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    assert "+" in g.gated_config_name(g.GEMM_TYPE_BF16, M, F, K)
+    torch.manual_seed(F)
+    x = torch.randint(-3, 4, (M, K), device="cuda").bfloat16()
+    w = torch.randint(-3, 4, (2 * F, K), device="cuda").bfloat16() / 64
+    h, kept = g.gated_matmul(x, w, save=True)
+    one, kept_one = g.gated_matmul(x, w, save=True, config="b128x128")
+    assert torch.equal(h, one)
+    for a, b in zip(ref.unkept(kept.cpu().numpy(), F), ref.unkept(kept_one.cpu().numpy(), F)):
+        assert np.array_equal(a, b)
+
+
 def test_gated_large_and_special_values():
     """Gates far out on both sides, past where the power overflows; infinities
     and NaN reach their own elements only."""

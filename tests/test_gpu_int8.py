@@ -114,6 +114,27 @@ def test_automatic_shapes(M, N, K):
         assert np.array_equal(product(a, sa, b, sb, out), rounded(want, out))
 
 
+@pytest.mark.parametrize("M, N, K", [(2507, 6630, 6400), (985, 16770, 2560), (3055, 5498, 2176)])
+def test_two_launches(M, N, K):
+    """Products whose last columns run in a second shape: bit for bit what one
+    shape gives, plain and gated."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    torch.manual_seed(M)
+    a = torch.randint(-128, 128, (M, K), device="cuda", dtype=torch.int8)
+    b = torch.randint(-128, 128, (N, K), device="cuda", dtype=torch.int8)
+    sa, sb = torch.rand(M, device="cuda") / 64, torch.rand(N, device="cuda") / 64
+    assert "+" in g.i8_config_name(M, N, K)
+    assert "+" in g.gated_config_name(g.GEMM_TYPE_I8, M, N // 2, K)
+    for t in (torch.float32, torch.bfloat16):
+        c = g.matmul_int8(a, sa, b, sb, out_dtype=t)
+        assert torch.equal(c, g.matmul_int8(a, sa, b, sb, out_dtype=t, config="b128x128"))
+        h = g.gated_matmul_int8(a, sa, b, sb, out_dtype=t)
+        assert torch.equal(h, g.gated_matmul_int8(a, sa, b, sb, out_dtype=t, config="b128x128"))
+
+
 def test_special_scales():
     """Zero, infinite and NaN scales reach their own row or column only."""
     rng = np.random.default_rng(5)
