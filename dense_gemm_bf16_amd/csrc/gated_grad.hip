@@ -13,7 +13,7 @@
 // 1365: 5.6 us).
 //
 // And the sum of a split product's parts, in their order: bound by memory too
-// (0.56 us a MB of parts and 3.9 for the launch).
+// (0.6 us a MB of parts and 3.4 for the launch).
 #include "block_internal.h"
 
 namespace gemm {

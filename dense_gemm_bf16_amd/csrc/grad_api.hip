@@ -38,10 +38,10 @@ struct GradTile {
   hipError_t (*launch)(const GradPair&, hipStream_t, int op, int out_x, int out_w);
 };
 const GradTile kTiles[] = {
-    {"b256x256", 256, 256, 512, 1, 1.277, 12.3, 0.675, &launch_grad_pair<256, 256, 2, 4, 2>},
-    {"b128x128", 128, 128, 256, 2, 0.841, 6.1, 0.806, &launch_grad_pair<128, 128, 2, 2, 2>},
+    {"b256x256", 256, 256, 512, 1, 1.226, 9.0, 0.970, &launch_grad_pair<256, 256, 2, 4, 2>},
+    {"b128x128", 128, 128, 256, 2, 0.782, 5.8, 0.901, &launch_grad_pair<128, 128, 2, 2, 2>},
 };
-constexpr double kSumUs = 3.89, kSumUsPerMB = 0.555, kTail = 0.136;
+constexpr double kSumUs = 3.41, kSumUsPerMB = 0.584, kTail = 0.119;
 
 struct GradPlan {
   const GradTile* tile;
@@ -69,10 +69,10 @@ int even_splits(int64_t n, int64_t s) {
 // The tile and splits whose launch a model finds cheapest: as long as its
 // longest workgroup, shorter where the GPU is part empty, or as all of them
 // over the places there are; and for splits the round trip of their fp32 sums.
-// Its constants were searched for the best choice over 46 products (1 to 8192
-// tokens, 256 to 14336 x 128 to 4096), each timed in the plans that were in
-// question: 0.9 % from the fastest of them, and 0.8 % over 46 other products
-// (16 % at worst).  gated_model.py holds the same model, the sweep, its times
+// Its constants were searched for the best choice over 50 products (1 to 8192
+// tokens, 256 to 14336 x 128 to 8192), each timed in the plans that were in
+// question: 0.9 % from the fastest of them, and 0.9 % over 50 other products
+// (22 % at worst).  gated_model.py holds the same model, the sweep, its times
 // and the search.
 GradPlan choose(const GradShape& x, const GradShape& w) {
   GradPlan best{nullptr, 1, 1};

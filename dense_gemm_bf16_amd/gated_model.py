@@ -238,7 +238,9 @@ SWEEP = [(N, K) for N, K in ((8192, 8192), (28672, 4096), (4096, 4096), (2048, 1
 SWEEP_M = (1, 6, 16, 24, 32, 48, 64, 100, 128, 200, 256, 400, 512, 777, 1024, 1500, 2048, 4096)
 SWEEP_GRADS = [(1000, 1365, 520), (100, 2000, 700), (8192, 1024, 1024), (2048, 2048, 1024),
                (512, 5001, 2055), (4096, 2048, 512), (16, 4096, 2048), (1, 1000, 1000),
-               (333, 8000, 4096), (2048, 5461, 2048), (1024, 14336, 4096), (4096, 5376, 2048)]
+               (333, 8000, 4096), (2048, 5461, 2048), (1024, 14336, 4096), (4096, 5376, 2048),
+               (1, 14336, 4096), (16, 14336, 4096), (64, 14336, 4096), (200, 14336, 4096),
+               (512, 14336, 4096), (4, 8192, 8192), (128, 8192, 8192), (32, 10000, 5000)]
 
 
 def _replay_us(run, sets):

@@ -71,7 +71,7 @@ def test_choices_are_near_the_fastest(gm, records):
         q = [v for v, k in quality if k == kind]
         assert len(q) == 197 and gm.geomean(q) < 1.015 and max(q) < 1.35
     q = gm.grad_quality(compiled_gradients(), records["gradients"])
-    assert len(q) == 92 and gm.geomean(q) < 1.0115 and max(q) < 1.2
+    assert len(q) == 100 and gm.geomean(q) < 1.0115 and max(q) < 1.25
 
 
 def test_shapes_are_those_built(gm):
