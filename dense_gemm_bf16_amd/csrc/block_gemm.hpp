@@ -303,14 +303,17 @@ __device__ __forceinline__ void scale_sums(const BlockArgs& a, f32x4 (&acc)[FM][
 // act(g) * u, with act(g) = g sigmoid(z): z = g for silu; for gelu in its tanh
 // form, g (1 + tanh(y)) / 2 = g sigmoid(2 y) with y = sqrt(2 / pi) (g +
 // 0.044715 g^3).  For a 16-bit H, sigmoid(z) = 1 / (1 + 2^(-z log2 e)) by the
-// vector unit's 2^x and 1/x (1 ulp each); the exponent's rounding is |z| 2^-24
-// relative, 2^-17 where the result nears fp32's smallest, against the 2^-9 or
-// 2^-12 of H's own rounding.  An fp32 H shows it, so there the exponent's
-// rounding error is made up for and the power is of -|z|, which neither
-// overflows nor cancels: a few ulp for every z (results below 2^-120 may be
-// zero).  Six and fourteen operations: with the longer form everywhere the
-// activation would take 5 % of a bf16 product's time and 9 % of an integer
-// one's at 8192 x 14336 x 4096.
+// vector unit's 2^x and 1/x (1 ulp each); the exponent's roundings (gelu's z has
+// five more) are up to 7 |z| 2^-24 relative, 2^-14 where the result nears fp32's
+// smallest, against the 2^-9 or 2^-12 of H's own rounding.  An fp32 H shows
+// them, so there the exponent is carried past fp32 (silu's product's rounding
+// error is made up for, gelu's z is taken in fp64: in fp32 its own roundings
+// left results up to 155 2^-24 off) and the power is of -|z|, which neither
+// overflows nor cancels: less than 8 2^-24 off for every z (results below
+// 2^-120 may be zero).  Six and fourteen operations for silu: with the longer
+// form everywhere the activation would take 5 % of a bf16 product's time and 9 %
+// of an integer one's at 8192 x 14336 x 4096.  (fp32 H of that size: silu 818-822
+// us, gelu 840-842, 834-840 with its z in fp32.)
 constexpr float kLog2e = 1.44269504f, kLog2eLow = 1.92596299e-8f, kLn2 = 0.69314718f;
 
 __device__ __forceinline__ float gate_argument(float g, bool geglu) {
@@ -318,23 +321,32 @@ __device__ __forceinline__ float gate_argument(float g, bool geglu) {
   return geglu ? y : g;
 }
 
-// exp(-x) for x >= 0 (x is cut at 200, past which it is zero).
-__device__ __forceinline__ float exp_of_minus(float x) {
-  x = fminf(x, 200.0f);
-  const float t = x * -kLog2e;
-  const float low = __builtin_fmaf(x, -kLog2e, -t) - x * kLog2eLow;
+// exp(-|z|) of the gate's z (|z| is cut at 200, past which it is zero).
+__device__ __forceinline__ float exp_of_minus(float g, bool geglu) {
+  float t, low;  // -|z| log2 e
+  if (geglu) {
+    const double d = (double)g;
+    const double z = d * __builtin_fma(0.07135481627260025, d * d, 1.5957691216057308);
+    const double y = __builtin_fmin(__builtin_fabs(z), 200.0) * -1.4426950408889634;
+    t = (float)y;
+    low = (float)(y - (double)t);
+  } else {
+    const float x = fminf(fabsf(g), 200.0f);
+    t = x * -kLog2e;
+    low = __builtin_fmaf(x, -kLog2e, -t) - x * kLog2eLow;
+  }
   const float e = __builtin_amdgcn_exp2f(t);
   return __builtin_fmaf(e, low * kLn2, e);
 }
 
 template <int OUT>
 __device__ __forceinline__ float gate(float g, float u, bool geglu) {
-  const float z = gate_argument(g, geglu);
   if constexpr (OUT == kStoreF32) {
-    const float e = exp_of_minus(fabsf(z));
+    const float e = exp_of_minus(g, geglu);
     const float r = 1.0f / (1.0f + e);
-    return g * (z >= 0.0f ? r : e * r) * u;
+    return g * (g >= 0.0f ? r : e * r) * u;
   } else {
+    const float z = gate_argument(g, geglu);
     return g * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -kLog2e)) * u;
   }
 }

@@ -40,6 +40,15 @@ def gate_error(g, u, act, dg=0.0, du=0.0):
         + (np.abs(g) + dg) * du
 
 
+def gate_error_fp32_out(g, u, act):
+    """What an fp32 H may miss of act(g) u, g and u known: the exponent is carried
+    past fp32, so |z| does not enter.  The power is off by 2 U (one step) and U
+    (its low part's product and sum), 1 + e and the reciprocal by U each, three
+    products by U each: 8 U relative.  A power below 2^-126 may be zero, and a
+    result below it a step of 2^-149 off."""
+    return 8 * U * np.abs(gate(g, u, act)) + TINY32 * np.abs(g * u) + 2.0 ** -149 * (1 + np.abs(u))
+
+
 def gate_gradients(dh, g, u, act):
     """(dg, du) of h = act(g) u."""
     z, dz = argument(g, act)

@@ -196,6 +196,30 @@ def test_gated_automatic_shapes(M, F, K):
         check_gated(gated(a, sa, w, sw, "geglu", out), a, sa, w, sw, "geglu", out)
 
 
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+@pytest.mark.parametrize("config", [None, *GATED])
+def test_fp32_gates_are_a_few_roundings_off(config, act):
+    """One product of 1 and 1 each, so g and u are the scales of their columns:
+    gates over the whole range, small, far out and of every size between."""
+    rng = np.random.default_rng(6)
+    F = 4096
+    sw = rng.normal(0, 2, 2 * F)
+    sw[:1500] = rng.uniform(-9, -0.1, 1500)  # (gelu's exponent reaches 80 at -9)
+    sw[1500:2500] = rng.uniform(-87, 20, 1000)
+    sw[2500:3500] = rng.choice([-1, 1], 1000) * np.exp(rng.uniform(-60, 60, 1000))
+    sw[3500:3512] = [0, -0.0, 88, -88, 103.9, -103.9, 200, -200, 1e30, -1e30, 3e38, -3e38]
+    sw = sw.astype(np.float32)
+    a, w = np.zeros((3, 40), np.int8), np.zeros((2 * F, 40), np.int8)
+    a[:, 17], w[:, 17] = 1, 1
+    got = gated(a, np.ones(3, np.float32), w, sw, act, "f32", config)
+    g, u = sw[:F].astype(np.float64), sw[F:].astype(np.float64)
+    want, bound = ref.gate(g, u, act), ref.gate_error_fp32_out(g, u, act)
+    fits = np.abs(want) < np.finfo(np.float32).max
+    off = np.abs(got - want)[:, fits]
+    assert (off <= bound[fits]).all(), float((off / bound[fits]).max())
+    assert (np.abs(got[:, ~fits]) == np.inf).all()
+
+
 @pytest.mark.parametrize("config", GATED)
 def test_gated_h_outside_its_range_is_left_alone(config):
     import torch
