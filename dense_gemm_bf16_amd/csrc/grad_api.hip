@@ -339,7 +339,7 @@ int gemm_gated_backward_ex(const char* config, int type, int64_t M, int64_t F, i
   if (act != GEMM_ACT_SWIGLU && act != GEMM_ACT_GEGLU) return GEMM_ERR_INVALID_ARG;
   if (dW && dw_type != type && dw_type != GEMM_TYPE_F32) return GEMM_ERR_INVALID_ARG;
   const int64_t Fp = up8(F < k2G ? F : k2G), kept_f = (Fp + 15) / 16 * 16, ld = gate_columns(Fp);
-  // (a workgroup of 256 for 2048 values of dGU: a grid holds fewer than 2^32 threads)
+  // (2^32 pieces of eight columns: dG, dU and what was kept would take 340 GB)
   if (size_refused(M, F, K) || (M > 0 && Fp / 8 >= 2 * k2G / M) || lddh >= kStrideLimit ||
       ldx >= kStrideLimit || ldw >= kStrideLimit || ld_kept >= kStrideLimit ||
       lddx >= kStrideLimit || lddw >= kStrideLimit)

@@ -330,6 +330,38 @@ def test_gated_gradients(M, F, K, t, act):
     check_gated_backward(dx, dw, dh, x, w, kept, act, t, "f32" if f32 else t)
 
 
+@pytest.mark.parametrize("M, F, K", [(131072, 8, 16), (131077, 9, 24), (300001, 3, 8)])
+def test_gated_gradients_of_many_rows(M, F, K):
+    """More rows than the gate's gradient has workgroups for: they walk the rest."""
+    import torch
+
+    rng = np.random.default_rng(M)
+    x, w, dh = normal(rng, (M, K), "bf16"), normal(rng, (2 * F, K), "bf16"), normal(rng, (M, F), "bf16")
+    _, kept = forward(x, w)
+    dx, dw = gated_backward(dh, x, w, kept, "swiglu", dw_dtype=torch.float32)
+    check_gated_backward(dx, dw, dh, x, w, kept, "swiglu", "bf16", "f32")
+
+
+def test_gated_gradients_of_more_rows_than_threads():
+    """2^26 rows, each a wave's worth of the gate's gradient: 2^32 threads."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    M, F, K = (1 << 26) + 5, 8, 8
+    torch.manual_seed(3)
+    x = torch.randint(-300, 300, (M, K), device="cuda", dtype=torch.int16).to(torch.bfloat16) / 256
+    dh = torch.randint(-300, 300, (M, F), device="cuda", dtype=torch.int16).to(torch.bfloat16) / 256
+    w = torch.randn(2 * F, K, device="cuda").to(torch.bfloat16)
+    h, kept = g.gated_matmul(x, w, save=True)
+    dx, _ = g.gated_matmul_backward(dh, x, w, kept, dw=False)
+    at = torch.cat([torch.arange(i, i + 40) for i in (0, 131052, 1 << 20, (1 << 25) - 20, M - 40)]).cuda()
+    h, kept, dx, x, dh, w = h[at].cpu(), kept[at], dx[at], x[at].cpu(), dh[at].cpu(), w.cpu()
+    check_forward(h, kept, x, w, "swiglu", "bf16")
+    _, dw = gated_backward(dh, x, w, kept, "swiglu")
+    check_gated_backward(dx, dw, dh, x, w, kept, "swiglu", "bf16", "bf16")
+
+
 def test_gated_gradients_one_at_a_time_and_in_place_of_others():
     """Either output alone, and given tensors whose surroundings stay."""
     import torch
