@@ -284,8 +284,9 @@ int gemm_backward_ex(const char* config, int type, int64_t M, int64_t N, int64_t
   if (M < 0 || N < 0 || K < 0) return GEMM_ERR_INVALID_ARG;
   if (type != GEMM_TYPE_BF16 && type != GEMM_TYPE_F16) return GEMM_ERR_INVALID_ARG;
   if (dB && db_type != type && db_type != GEMM_TYPE_F32) return GEMM_ERR_INVALID_ARG;
-  if (size_refused(M, N, K) || lddc >= kStrideLimit || lda >= kStrideLimit ||
-      ldb >= kStrideLimit || ldda >= kStrideLimit || lddb >= kStrideLimit)
+  if (size_refused(M, N, K) || lddc >= kStrideLimit ||
+      (dA && (ldb >= kStrideLimit || ldda >= kStrideLimit)) ||
+      (dB && (lda >= kStrideLimit || lddb >= kStrideLimit)))
     return GEMM_ERR_UNSUPPORTED;
   const bool has_a = dA && M > 0 && K > 0, has_b = dB && N > 0 && K > 0;
   if (lddc < N || (dA && (ldb < K || ldda < K)) || (dB && (lda < K || lddb < K)))
@@ -293,9 +294,9 @@ int gemm_backward_ex(const char* config, int type, int64_t M, int64_t N, int64_t
   if ((has_a || has_b) && M > 0 && N > 0 &&
       (!dC || (has_a && !B) || (has_b && !A)))
     return GEMM_ERR_INVALID_ARG;
-  if (misaligned(dC, 16) || misaligned(A, 16) || misaligned(B, 16) || misaligned(dA, 16) ||
-      misaligned(dB, 16) || misaligned(work, 16) || (lddc & 7) || (dA && ((ldb | ldda) & 7)) ||
-      (dB && ((lda | lddb) & 7)))
+  if (misaligned(dC, 16) || (dB && misaligned(A, 16)) || (dA && misaligned(B, 16)) ||
+      misaligned(dA, 16) || misaligned(dB, 16) || misaligned(work, 16) || (lddc & 7) ||
+      (dA && ((ldb | ldda) & 7)) || (dB && ((lda | lddb) & 7)))
     return GEMM_ERR_MISALIGNED;
   const GradShape pa = has_a ? input_shape(M, N, K) : kNoProduct;
   const GradShape pb = has_b ? weight_shape(M, N, K) : kNoProduct;
@@ -341,8 +342,8 @@ int gemm_gated_backward_ex(const char* config, int type, int64_t M, int64_t F, i
   const int64_t Fp = up8(F < k2G ? F : k2G), kept_f = (Fp + 15) / 16 * 16, ld = gate_columns(Fp);
   // (2^32 pieces of eight columns: dG, dU and what was kept would take 340 GB)
   if (size_refused(M, F, K) || (M > 0 && Fp / 8 >= 2 * k2G / M) || lddh >= kStrideLimit ||
-      ldx >= kStrideLimit || ldw >= kStrideLimit || ld_kept >= kStrideLimit ||
-      lddx >= kStrideLimit || lddw >= kStrideLimit)
+      ld_kept >= kStrideLimit || (dX && (ldw >= kStrideLimit || lddx >= kStrideLimit)) ||
+      (dW && (ldx >= kStrideLimit || lddw >= kStrideLimit)))
     return GEMM_ERR_UNSUPPORTED;
   const bool has_x = dX && M > 0 && K > 0, has_w = dW && F > 0 && K > 0;
   if (lddh < F || ld_kept < 6 * kept_f || (dX && (ldw < K || lddx < K)) ||
@@ -350,9 +351,9 @@ int gemm_gated_backward_ex(const char* config, int type, int64_t M, int64_t F, i
     return GEMM_ERR_INVALID_ARG;
   if ((has_x || has_w) && M > 0 && F > 0 && (!dH || !kept || (has_x && !W) || (has_w && !X)))
     return GEMM_ERR_INVALID_ARG;
-  if (misaligned(dH, 16) || misaligned(X, 16) || misaligned(W, 16) || misaligned(kept, 16) ||
-      misaligned(dX, 16) || misaligned(dW, 16) || misaligned(work, 16) || (lddh & 7) ||
-      (ld_kept & 15) || (dX && ((ldw | lddx) & 7)) || (dW && ((ldx | lddw) & 7)))
+  if (misaligned(dH, 16) || (dW && misaligned(X, 16)) || (dX && misaligned(W, 16)) ||
+      misaligned(kept, 16) || misaligned(dX, 16) || misaligned(dW, 16) || misaligned(work, 16) ||
+      (lddh & 7) || (ld_kept & 15) || (dX && ((ldw | lddx) & 7)) || (dW && ((ldx | lddw) & 7)))
     return GEMM_ERR_MISALIGNED;
   const GradShape px = has_x ? gated_input_shape(M, F, K) : kNoProduct;
   const GradShape pw = has_w ? gated_weight_shape(M, F, K) : kNoProduct;

@@ -221,6 +221,20 @@ def test_workspaces(g):
                     dB=NUL, nbytes=1 << 62, config=b"b256x256_k2_k1") == 3
 
 
+def test_what_is_not_used_is_not_checked(g):
+    """Without dA, B may be anything, without dB A, and likewise W and X (K = 0:
+    nothing is launched)."""
+    assert backward(g, K=0, dA=NUL, B=ODD, ldb=3) == 0 == backward(g, K=0, dB=NUL, A=ODD, lda=3)
+    assert backward(g, K=0, dA=NUL, ldb=1 << 41, ldda=1 << 41) == 0
+    assert backward(g, K=0, dB=NUL, lda=1 << 41, lddb=1 << 41) == 0
+    assert backward(g, K=0, dA=NUL, A=ODD) == 2 == backward(g, K=0, dB=NUL, B=ODD)
+    assert backward(g, K=0, dA=NUL, lda=1 << 41) == 3 == backward(g, K=0, dB=NUL, ldda=1 << 41)
+    assert gated_backward(g, K=0, dX=NUL, W=ODD, ldw=3, lddx=1 << 41) == 0
+    assert gated_backward(g, K=0, dW=NUL, X=ODD, ldx=1 << 41, lddw=3) == 0
+    assert gated_backward(g, K=0, dX=NUL, X=ODD) == 2 == gated_backward(g, K=0, dW=NUL, W=ODD)
+    assert gated_backward(g, K=0, dX=NUL, ldx=1 << 41) == 3 == gated_backward(g, K=0, dW=NUL, ldw=1 << 41)
+
+
 def test_empty_calls_launch_nothing(g):
     assert i8(g, M=0, A=NUL, SA=NUL, C=NUL) == 0 and i8(g, N=0, B=NUL, SB=NUL, C=NUL) == 0
     assert i8_gated(g, M=0, A=NUL, SA=NUL, H=NUL) == 0 and i8_gated(g, F=0, W=NUL, SW=NUL, H=NUL) == 0

@@ -385,6 +385,33 @@ def test_gated_gradients_one_at_a_time_and_in_place_of_others():
     assert (bx == 7).all() and (bw == 7).all()
 
 
+def test_the_operand_of_a_gradient_that_is_left_out_may_lie_anywhere():
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = np.random.default_rng(12)
+    M, F, K = 70, 40, 56
+    dc, x, w = normal(rng, (M, 2 * F), "bf16"), normal(rng, (M, K), "bf16"), normal(rng, (2 * F, K), "bf16")
+    dc, x, w, dh = dev(dc), dev(x), dev(w), dev(normal(rng, (M, F), "bf16"))
+    _, kept = g.gated_matmul(x, w, save=True)
+
+    def odd(t):  # the same, two bytes off 16, rows an odd number of elements apart
+        wide = torch.zeros(len(t), t.shape[1] + 3, device="cuda", dtype=t.dtype)
+        wide[:, 1:-2] = t
+        return wide[:, 1:-2]
+
+    pairs = ((g.matmul_backward(dc, x, odd(w), dA=False)[1], g.matmul_backward(dc, x, w, dA=False)[1]),
+             (g.matmul_backward(dc, odd(x), w, dB=False)[0], g.matmul_backward(dc, x, w, dB=False)[0]),
+             (g.gated_matmul_backward(dh, x, odd(w), kept, dx=False)[1],
+              g.gated_matmul_backward(dh, x, w, kept, dx=False)[1]),
+             (g.gated_matmul_backward(dh, odd(x), w, kept, dw=False)[0],
+              g.gated_matmul_backward(dh, x, w, kept, dw=False)[0]))
+    torch.cuda.synchronize()
+    for got, want in pairs:
+        assert torch.equal(got, want)
+
+
 def test_gated_gradients_of_special_values():
     """Gates far out: nothing overflows; an infinite or NaN gradient reaches its
     own row of dx only."""
