@@ -277,6 +277,30 @@ def test_quantize_rows(M):
     assert np.array_equal(q, want) and np.array_equal(s, scale)
 
 
+@pytest.mark.parametrize("t", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("M, K", [
+    (3, 513), (3, 777), (3, 1024), (259, 1024), (259, 1025), (255, 2049), (256, 2049), (259, 4095),
+    (255, 4096), (256, 4096), (259, 4097), (259, 8185), (259, 8191), (255, 8192), (256, 8192), (259, 8193)])
+def test_quantize_many_rows_bit_for_bit(M, K, t):
+    """Each form of the kernel for rows held in registers, at the ends of its
+    columns and on both sides of the 256 rows from which four waves take a row
+    of up to 8192; a row's largest value at any place of it, NaN past its end."""
+    import torch
+
+    rng = np.random.default_rng(M + K)
+    v = rng.normal(0, 1, (M, K)).astype(np.float32)
+    at = rng.integers(0, K, M)
+    at[:9] = np.minimum([0, 7, 8, 511, 512, 2047, 2048, K - 2, K - 1], K - 1)[:M]
+    v[np.arange(M), at] = rng.choice([-1, 1], M) * rng.uniform(6, 60, M)
+    x = torch.from_numpy(v).to(dtype(t))
+    buf = torch.full((M, K + 5), float("nan"), dtype=x.dtype)
+    buf[:, 2:K + 2] = x
+    for y in (buf.cuda()[:, 2:K + 2], x.cuda()):
+        q, s = quantized(y)
+        want, scale = ref.quantize(x.float().numpy())
+        assert np.array_equal(q, want) and np.array_equal(s, scale)
+
+
 def test_quantize_special_rows():
     """Largest and smallest values, ties, infinities and NaN; rows of zeros."""
     import torch
