@@ -221,6 +221,25 @@ def test_workspaces(g):
                     dB=NUL, nbytes=1 << 62, config=b"b256x256_k2_k1") == 3
 
 
+def test_workspaces_a_byte_too_small(g):
+    """Refused by either backward call, split or not."""
+    sizes = dict(M=300, K=136)
+    gated_size = dict(F=200, lddh=200, ldx=136, ldw=136, ld_kept=1248, lddx=136, lddw=136)
+    for config in (b"b128x128_k1_k1", b"b128x128_k2_k3", b"b256x256_k3_k2"):
+        need = g.gated_backward_work_size(300, 200, 136, config.decode())
+        split = 0 if config.endswith(b"k1_k1") else 4 * 136 * (
+            2 * 300 + 3 * 400 if config.endswith(b"k3") else 3 * 300 + 2 * 400)
+        assert need == 300 * 2 * 256 * 2 + split  # dG and dU in rows of 128-byte lines, and the parts
+        assert gated_backward(g, config=config, nbytes=need - 1, **sizes, **gated_size) == 6
+        need = g.backward_work_size(300, 400, 136, config.decode())
+        assert need == split
+        if need:
+            assert backward(g, N=400, lddc=400, lda=136, ldb=136, ldda=136, lddb=136, config=config,
+                            nbytes=need - 1, **sizes) == 6
+    need = g.gated_backward_work_size(8, 9, 64)
+    assert need == 8 * 2 * 64 * 2 and gated_backward(g, nbytes=need - 1) == 6
+
+
 def test_what_is_not_used_is_not_checked(g):
     """Without dA, B may be anything, without dB A, and likewise W and X (K = 0:
     nothing is launched)."""

@@ -656,6 +656,36 @@ def test_products_in_a_given_workspace_are_the_same(M, N, K, t):
     assert torch.equal(c, want) and (work[n:] == 99).all()
 
 
+@pytest.mark.parametrize("config", [None, "b128x128_k2_k3", "b256x256_k3_k2"])
+def test_gradients_in_a_workspace_of_just_their_size(config):
+    """Enough, and nothing past it is written."""
+    import torch
+
+    import dense_gemm_bf16_amd as g
+
+    rng = np.random.default_rng(15)
+    M, F, K = 300, 200, 136
+    x, w, dh = (dev(normal(rng, s, "bf16")) for s in ((M, K), (2 * F, K), (M, F)))
+    dc = dev(normal(rng, (M, 2 * F), "bf16"))
+    _, kept = g.gated_matmul(x, w, save=True)
+    wants = (g.gated_matmul_backward(dh, x, w, kept, config=config),
+             g.matmul_backward(dc, x, w, config=config))
+    for want, n in zip(wants, (g.gated_backward_work_size(M, F, K, config),
+                               g.backward_work_size(M, 2 * F, K, config))):
+        work = torch.full((n + 4096,), 99, device="cuda", dtype=torch.uint8)
+        dx = torch.full((M, K), 7.0, device="cuda", dtype=torch.bfloat16)
+        dw = torch.full((2 * F, K), 7.0, device="cuda", dtype=torch.bfloat16)
+        outs = (dx, K, dw, K, g.GEMM_TYPE_BF16, work, n)
+        if want is wants[0]:
+            g.gemm_gated_backward_ex(config, g.GEMM_TYPE_BF16, M, F, K, dh, dh.stride(0), x, x.stride(0), w,
+                                     w.stride(0), g.GEMM_ACT_SWIGLU, kept, kept.stride(0), *outs)
+        else:
+            g.gemm_backward_ex(config, g.GEMM_TYPE_BF16, M, 2 * F, K, dc, dc.stride(0), x, x.stride(0), w,
+                               w.stride(0), *outs)
+        torch.cuda.synchronize()
+        assert torch.equal(dx, want[0]) and torch.equal(dw, want[1]) and (work[n:] == 99).all()
+
+
 def test_two_captured_layers_replayed_at_once():
     """Graphs captured on one stream, with split plans, replayed on two."""
     import torch
