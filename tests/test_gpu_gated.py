@@ -463,6 +463,48 @@ def test_gradients_against_differences():
             assert abs(slope - told) <= 3 * HALF_STEP["bf16"] * size
 
 
+@pytest.mark.parametrize("t", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+def test_each_gradient_against_differences(act, t):
+    """Entries of dx and dW, one by one, against central differences of the loss
+    sum(r * h(x, W)) in 64 bits.  Kept g and u are off by an fp32 sum's error and
+    half a step of 24 bits, which reaches dg by |act''| <= 0.8 and |act'| <= 1.13
+    (and u's likewise); dg and du are rounded once, then summed and rounded."""
+    rng = np.random.default_rng(14)
+    M, F, K = 40, 56, 48
+    x, w = normal(rng, (M, K), t), normal(rng, (2 * F, K), t, K ** -0.5)
+    r = normal(rng, (M, F), t)
+    _, kept = forward(x, w, act)
+    dx, dw = (f64(v) for v in gated_backward(r, x, w, kept, act))
+    X, W, R = f64(x), f64(w), np.abs(f64(r))
+    GU, err = ref.product(X, W)
+    err = err + ref.KEPT_HALF_STEP * (np.abs(GU) + err)
+    (g, u), (eg, eu) = np.split(GU, 2, 1), np.split(err, 2, 1)
+    dg, du = ref.gate_gradients(f64(r), g, u, act)
+    d, e = np.concatenate([dg, du], 1), np.concatenate(ref.gate_gradient_error(f64(r), g, u, act), 1)
+    e = e + np.concatenate([R * (0.8 * eg * (np.abs(u) + eu) + 1.13 * eu), R * 1.13 * eg], 1)
+    e = e + HALF_STEP[t] * (np.abs(d) + e) + TINY[t]
+    bx = e @ np.abs(W) + 2 * U * (2 * F + 16) * ((np.abs(d) + e) @ np.abs(W))
+    bw = e.T @ np.abs(X) + 2 * U * (M + 16) * ((np.abs(d) + e).T @ np.abs(X))
+
+    def loss(X, W):
+        GU = X @ W.T
+        return (f64(r) * ref.gate(GU[:, :F], GU[:, F:], act)).sum()
+
+    s = 2.0 ** -16
+    for got, bound, of in ((dx, bx, X), (dw, bw, W)):
+        for i in rng.choice(of.size, 400, replace=False):
+            at = np.unravel_index(i, of.shape)
+            one = np.zeros_like(of)
+            one[at] = s
+            ends = [loss(X + k * one, W) if of is X else loss(X, W + k * one) for k in (1, -1)]
+            slope = (ends[0] - ends[1]) / (2 * s)
+            # (the differences: a third derivative of at most 1e3 times s^2 / 6,
+            # and two losses of at most 1e3 to 64 bits)
+            tol = bound[at] + HALF_STEP[t] * (abs(slope) + bound[at]) + TINY[t] + 1e-7
+            assert abs(got[at] - slope) <= tol, (at, got[at], slope, tol)
+
+
 def test_a_captured_training_step():
     """Forward and backward in one graph, replayed with new contents between
     eager work; a second graph of other sizes beside it keeps its own
