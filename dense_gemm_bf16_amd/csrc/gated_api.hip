@@ -32,9 +32,12 @@ constexpr int64_t kMaxIntK = 131071;  // 2^14 K stays below 2^31
 //
 // Fitted to 591 products (M 1 to 4096, B from 512 x 1024 to 28672 x 4096 and down
 // to 128 bytes deep, integers plain and gated, bf16 gated), each timed in the
-// shapes that were in question; its choice ran within 1.2 % of the fastest of
-// them (geometric mean; 27 % at worst).  gated_model.py holds the same model, the
-// sweep, its times and the fit, which gives these constants.
+// shapes that were in question, with a bf16 output and without keeping g and u;
+// the same constants choose for the other outputs and for fp16.  What it chooses
+// ran within 1.2 % of the fastest timed (geometric mean; 27 % at worst); the
+// eleven of them that are two launches took 2 % less than the fastest single
+// shape (12 % less to 9 % more).  gated_model.py holds the same model, the sweep,
+// its times and the fit, which gives these constants.
 struct Cost {
   float step, tile, part, stair, base;  // us, us, share, share, us
 };

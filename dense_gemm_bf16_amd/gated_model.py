@@ -29,6 +29,7 @@ choice: the times of unlike plans lie closer than a model of them is off.
 Usage::
 
     python -m dense_gemm_bf16_amd.gated_model sweep --out timings.json   # GPU
+    python -m dense_gemm_bf16_amd.gated_model choices --out timings.json # GPU
     python -m dense_gemm_bf16_amd.gated_model fit                        # CPU
 """
 from __future__ import annotations
@@ -149,13 +150,29 @@ def fit(records):
 
 def choice_quality(constants, records):
     """(time of the shape the model picks over the fastest, kind) of each
-    product; one launch only."""
+    product, among the shapes that the sweep timed: one launch only."""
     out = []
     for r in records:
         b, gated = KINDS[r["kind"]]
         among = {s: c for s, c in constants[b].items() if s in r["times"]}
         _, pick = cheapest(among, gated, r["M"], r["N"] * (2 if gated else 1), r["K"] * b)
         out.append((r["times"][pick] / min(r["times"].values()), r["kind"]))
+    return out
+
+
+def library_quality(constants, products, choices):
+    """(time of what the library runs over the fastest of it and the shapes that
+    were timed, kind) of each product.  What the sweep did not time (two launches,
+    a shape that was not in question there) is in `choices`, timed beside the
+    product's fastest shape."""
+    later = {(r["kind"], r["M"], r["N"], r["K"]): r["times"] for r in choices}
+    out = []
+    for r in products:
+        b, gated = KINDS[r["kind"]]
+        name, times = choose(constants[b], gated, r["M"], r["N"], r["K"] * b), r["times"]
+        if name not in times:
+            times = later[r["kind"], r["M"], r["N"], r["K"]]
+        out.append((times[name] / min(times.values()), r["kind"]))
     return out
 
 
@@ -272,8 +289,9 @@ def _rows(shape, dtype, unit):
     return torch.empty((shape[0], -(-shape[1] // unit) * unit), device="cuda", dtype=dtype)[:, :shape[1]]
 
 
-def time_product(kind, M, rows_b, K):
-    """The times of one product in every shape that is in question."""
+def time_product(kind, M, rows_b, K, plans=None):
+    """The times of one product in every shape that is in question, or as the
+    plans named (two launches: only what the library chooses)."""
     import torch
 
     import dense_gemm_bf16_amd as g
@@ -299,7 +317,9 @@ def time_product(kind, M, rows_b, K):
             g.gated_matmul(A[i], B[i], config=shape, out=C)
 
     times = {}
-    for shape, (bm, _, _, _) in SHAPES.items():
+    for plan in plans or ():
+        times[plan] = _replay_us(lambda i: run(i, None if "+" in plan else plan), sets)
+    for shape, (bm, _, _, _) in SHAPES.items() if plans is None else ():
         if (gated and shape == NOT_GATED) or M > 64 * bm or (bm >= 256 and M <= 64) or \
                 (shape[0] == "r" and M > 400):
             continue
@@ -358,18 +378,44 @@ def sweep(out_path: str, every: int = 1) -> None:
         json.dump(data, f, separators=(",", ":"))
 
 
+def time_choices(path: str, out_path: str) -> None:
+    """Adds `choices` to the sweep's data."""
+    import dense_gemm_bf16_amd as g
+
+    with open(path) as f:
+        data = json.load(f)
+    data["choices"] = []
+    for r in data["products"]:
+        kind, M, N, K, timed = r["kind"], r["M"], r["N"], r["K"], r["times"]
+        size, gated = KINDS[kind]
+        name = g.gated_config_name(g.GEMM_TYPE_I8 if size == 1 else g.GEMM_TYPE_BF16, M, N, K) if gated \
+            else g.i8_config_name(M, N, K)
+        if name not in timed:
+            c = time_product(kind, M, 2 * N if gated else N, K, (name, min(timed, key=timed.get)))
+            data["choices"].append(c)
+            print(kind, M, N, K, c["times"], flush=True)
+    with open(out_path, "w") as f:
+        json.dump(data, f, separators=(",", ":"))
+
+
 def main(argv=None) -> int:
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     sub = ap.add_subparsers(dest="cmd", required=True)
     sw = sub.add_parser("sweep", help="time every shape and plan on the GPU")
     sw.add_argument("--out", required=True)
     sw.add_argument("--every", type=int, default=1, help="only every n-th size")
+    ch = sub.add_parser("choices", help="time what the library chooses and the sweep did not time")
+    ch.add_argument("--data", default=DATA)
+    ch.add_argument("--out", required=True)
     ft = sub.add_parser("fit", help="fit the constants and report the choice quality")
     ft.add_argument("--data", default=DATA)
     args = ap.parse_args(argv)
     if args.cmd == "sweep":
         sys.path.insert(0, os.path.dirname(_HERE))
         sweep(args.out, args.every)
+        return 0
+    if args.cmd == "choices":
+        time_choices(args.data, args.out)
         return 0
     with open(args.data) as f:
         data = json.load(f)
@@ -384,6 +430,8 @@ def main(argv=None) -> int:
         q = [v for v, k in quality if k == kind]
         print(f"{kind}: {len(q)} products, model's pick / fastest timed {geomean(q):.4f} "
               f"(worst {max(q):.3f})")
+    q = [v for v, _ in library_quality(constants, data["products"], data["choices"])]
+    print(f"as the library runs them: {geomean(q):.4f} (worst {max(q):.3f})")
     half = data["gradients"][::2]
     found = search(half, START)
     print("gradients", {n: tuple(round(x, 3) for x in c) for n, c in found.items()})

@@ -74,6 +74,20 @@ def test_choices_are_near_the_fastest(gm, records):
     assert len(q) == 100 and gm.geomean(q) < 1.0115 and max(q) < 1.25
 
 
+def test_what_the_library_runs_is_timed_and_near_the_fastest(gm, records):
+    """Two launches and shapes that the sweep left out among them."""
+    import numpy as np
+
+    c = {b: {s: tuple(float(np.float32(v)) for v in k) for s, k in by.items()}
+         for b, by in compiled(gm).items()}
+    assert sum("+" in p for r in records["choices"] for p in r["times"]) >= 11
+    quality = gm.library_quality(c, records["products"], records["choices"])
+    assert len(quality) == 591
+    q = [v for v, _ in quality]
+    print(gm.geomean(q), max(q))
+    assert gm.geomean(q) < 1.013 and max(q) < 1.35
+
+
 def test_shapes_are_those_built(gm):
     import dense_gemm_bf16_amd as g
 
