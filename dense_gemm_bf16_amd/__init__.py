@@ -920,7 +920,8 @@ def gated_matmul(x, W, act="swiglu", out=None, save=False, config=None):
     """h (M x F) = act(g) * u with g = x . Wg^T and u = x . Wu^T: x (M x K) and W
     (2F x K: Wg's rows, then Wu's) both bfloat16 or both float16.  act: "swiglu"
     (silu) or "geglu" (gelu, tanh form).  save: return (h, kept), kept (uint8) what
-    gated_matmul_backward needs: g and u to 24 bits, 6 bytes for each column."""
+    gated_matmul_backward needs: g and u to 24 bits, 6 bytes for each column.
+    h is part of no autograd graph, also where x or W requires gradients."""
     _need(x, "x")
     dev, code = x.device, _type(x.dtype, "x", (GEMM_TYPE_BF16, GEMM_TYPE_F16))
     _need(W, "W", dev, x.dtype)
@@ -1030,7 +1031,8 @@ def gated_mlp(x, W1, W2, act="swiglu", save=False):
     """A gated feed-forward layer: y (M x N) = (act(g) * u) . W2^T, (g, u) the
     two halves of x . W1^T.  x (M x K), W1 (2F x K) and W2 (N x F) are all
     bfloat16 or all float16.  save: return (y, h, kept), h (M x F) and what
-    gated_matmul kept, for gated_mlp_backward."""
+    gated_matmul kept, for gated_mlp_backward.  y is part of no autograd graph,
+    also where x, W1 or W2 requires gradients."""
     if W2.dim() != 2 or W1.dim() != 2 or 2 * W2.shape[1] != W1.shape[0]:
         raise ValueError("need W1 (2F x K) and W2 (N x F)")
     _need(x, "x")

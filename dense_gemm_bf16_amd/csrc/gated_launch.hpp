@@ -81,8 +81,9 @@ hipError_t launch_gated_row(const BlockArgs& a, int grid, hipStream_t s, int op,
 
 // The block products' tiles, and one between the two largest, for products whose
 // last pass over the CUs those would leave part empty (integers 777 x 10240 x
-// 4104 47.0 us, 256 x 256 54.4, 256 x 128 69.1; fp16 gated 777 x 5001 x 2055 46.5,
-// 52.9, 67.8; where passes are whole, 6-10 % slower than 256 x 256).
+// 4104, bf16 out, 44-47 us, 256 x 256 51-54, 256 x 128 66-69; fp16 gated 777 x
+// 5001 x 2055 43-44, 50, 65, each in a graph of such launches; where passes are
+// whole, 6-10 % slower than 256 x 256).
 #define GATED_TILES(X)               \
   BLOCK_TILES(X)                     \
   X(b256x192, 256, 192, 2, 4, 1, 2)
